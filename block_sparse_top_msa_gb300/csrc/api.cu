@@ -485,7 +485,8 @@ msa_status_t build_forward(
     const int32_t* cu_seqlens_k, const int32_t* page_table, int max_pages, int num_pages,
     const int32_t* seqused_k, int batch, int total_q, int total_k, int num_qo_heads,
     int num_kv_heads, int head_dim, int max_seqlen_q, int causal, float softmax_scale, void* out,
-    float* lse, void* workspace, size_t workspace_bytes, ForwardPlan* plan) {
+    float* lse, void* workspace, size_t workspace_bytes, ForwardPlan* plan,
+    const uint32_t* tree_mask = nullptr, int mask_words = 0) {
   // ---- argument checks (host only; nothing is read from the device) ----
   const bool paged = page_table != nullptr;
   if (cu_seqlens_k != nullptr && paged) return MSA_INVALID_ARG;   // two length sources
@@ -558,7 +559,7 @@ msa_status_t build_forward(
 
   const SwappedLayout S =
       swapped_layout(batch, total_q, num_qo_heads, num_kv_heads, topk, max_seqlen_q);
-  if (use_swapped(S, esize, max_seqlen_q))
+  if (tree_mask == nullptr && use_swapped(S, esize, max_seqlen_q))
     return build_swapped(q, q_dtype, k, v, q2k_indices, topk, cu_seqlens_q, cu_seqlens_k,
                          page_table, max_pages, num_pages, seqused_k, batch, total_q, total_k,
                          num_qo_heads, num_kv_heads, causal, scale_log2, out, lse, ws, S, fault,
@@ -642,7 +643,26 @@ msa_status_t build_forward(
   // The counter reset before a direct launch is an ordinary launch, so every
   // earlier kernel (a decode pass included) has completed when it starts.
   a.wait_late = a.direct;
+  a.tree_mask = tree_mask;
+  a.mask_words = mask_words;
   return MSA_OK;
+}
+
+// The tree form of the paged forward: the same checks and plan, not causal,
+// with the mask over each sequence's own query tokens.
+msa_status_t build_tree(
+    const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
+    const int32_t* q2k_indices, int topk, const int32_t* cu_seqlens_q, const uint32_t* tree_mask,
+    int mask_words, const int32_t* page_table, int max_pages, int num_pages,
+    const int32_t* seqused_k, int batch, int total_q, int num_qo_heads, int num_kv_heads,
+    int head_dim, int max_seqlen_q, float softmax_scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, ForwardPlan* plan) {
+  if (page_table == nullptr || tree_mask == nullptr || !aligned(tree_mask, 4)) return MSA_INVALID_ARG;
+  if (mask_words < 1 || (long long)mask_words * 32 < max_seqlen_q) return MSA_INVALID_ARG;
+  return build_forward(q, q_dtype, k, v, kv_dtype, q2k_indices, topk, cu_seqlens_q, nullptr,
+                       page_table, max_pages, num_pages, seqused_k, batch, total_q, 0, num_qo_heads,
+                       num_kv_heads, head_dim, max_seqlen_q, 0, softmax_scale, out, lse, workspace,
+                       workspace_bytes, plan, tree_mask, mask_words);
 }
 
 // The packed-NVFP4 paged route: the E4M3 kernel instance (converter warps),
@@ -767,7 +787,9 @@ msa_status_t launch_forward(const ForwardPlan& p, cudaStream_t stream) {
                    : launch_build_union(p.u, stream);
   if (e != cudaSuccess) return MSA_CUDA_ERROR;
   mark(1, stream);
-  e = p.swapped ? launch_prefill_swapped(p.a, stream) : launch_prefill(p.a, stream);
+  e = p.swapped                      ? launch_prefill_swapped(p.a, stream)
+      : p.a.tree_mask != nullptr ? launch_tree(p.a, stream)
+                                 : launch_prefill(p.a, stream);
   mark(2, stream);
   return from_cuda(e);
 }
@@ -871,7 +893,45 @@ msa_status_t msa_sparse_attention_nvfp4_prepare(
 
 #undef MSA_FP4_ARGS
 
+#define MSA_TREE_ARGS                                                                           \
+  q, q_dtype, k, v, kv_dtype, q2k_indices, topk, cu_seqlens_q, tree_mask, mask_words,           \
+      page_table, max_pages, num_pages, seqused_k, batch, total_q, num_qo_heads, num_kv_heads, \
+      head_dim, max_seqlen_q, softmax_scale, out, lse, workspace, workspace_bytes
 
+msa_status_t msa_tree_attention(
+    const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
+    const int32_t* q2k_indices, int topk, const int32_t* cu_seqlens_q, const uint32_t* tree_mask,
+    int mask_words, const int32_t* page_table, int max_pages, int num_pages,
+    const int32_t* seqused_k, int batch, int total_q, int num_qo_heads, int num_kv_heads,
+    int head_dim, int max_seqlen_q, float softmax_scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream) {
+  msa::ForwardPlan p;
+  const msa_status_t st = msa::build_tree(MSA_TREE_ARGS, &p);
+  if (st != MSA_OK) return st;
+  return msa::launch_forward(p, stream);
+}
+
+msa_status_t msa_tree_attention_prepare(
+    const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
+    const int32_t* q2k_indices, int topk, const int32_t* cu_seqlens_q, const uint32_t* tree_mask,
+    int mask_words, const int32_t* page_table, int max_pages, int num_pages,
+    const int32_t* seqused_k, int batch, int total_q, int num_qo_heads, int num_kv_heads,
+    int head_dim, int max_seqlen_q, float softmax_scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, msa_attention_plan_t** plan_out) {
+  if (plan_out == nullptr) return MSA_INVALID_ARG;
+  *plan_out = nullptr;
+  msa_attention_plan_t* plan = new (std::nothrow) msa_attention_plan_t;
+  if (plan == nullptr) return MSA_CUDA_ERROR;
+  const msa_status_t st = msa::build_tree(MSA_TREE_ARGS, &plan->p);
+  if (st != MSA_OK) {
+    delete plan;
+    return st;
+  }
+  *plan_out = plan;
+  return MSA_OK;
+}
+
+#undef MSA_TREE_ARGS
 
 msa_status_t msa_proxy_score(const void* q, msa_dtype_t q_dtype, const void* k,
                              msa_dtype_t k_dtype, const int32_t* cu_seqlens_q,

@@ -129,8 +129,13 @@ struct PrefillArgs {
   // attention kernel waits for it only before its first claim from the
   // counter.
   int wait_late;
+  // Tree attention only (launch_tree): row t's mask_words words say which of
+  // its sequence's query tokens it sees among the last Lq keys.
+  const uint32_t* tree_mask;
+  int mask_words;
 };
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t s);
+cudaError_t launch_tree(const PrefillArgs& a, cudaStream_t s);
 // The swapped-orientation prefill kernel (bf16 / fp16 K/V, G a multiple of 8
 // and at most 64, tile_tokens * G <= 256, tile_tokens <= 32, no splits).
 cudaError_t launch_prefill_swapped(const PrefillArgs& a, cudaStream_t s);
@@ -235,5 +240,107 @@ struct Fp4DecodeArgs {
 size_t fp4_decode_workspace_bytes(long long units, int topk);
 void place_fp4_decode_workspace(Fp4DecodeArgs* a, uint8_t* ws, long long units, int topk);
 cudaError_t launch_fp4_decode(const Fp4DecodeArgs& a, cudaStream_t s);
+
+// Per-head norm and rotation of q and k (rope.cu).
+struct RopeArgs {
+  const void* q = nullptr;  // (tokens, hq, 128) with token stride q_stride (elements); k, v alike
+  const void* k = nullptr;
+  const void* v = nullptr;
+  long long q_stride = 0, k_stride = 0, v_stride = 0;
+  int f16 = 0;  // else bf16
+  int kv = 0;   // 0: K to k_out; 1: K and V to 16-bit pools; 2: to E4M3 pools
+  const float* wq = nullptr;  // (128)
+  const float* wk = nullptr;
+  const float* cos_sin = nullptr;  // (max_position, rotary): cosines, then sines
+  int max_position = 0, rotary = 0, interleaved = 0;
+  const int32_t* positions = nullptr;  // (tokens)
+  float eps = 0.f;
+  int tokens = 0, hq = 0, hkv = 0;
+  void* q_out = nullptr;  // (tokens, hq, 128)
+  void* k_out = nullptr;
+  const int32_t* cu_q = nullptr;
+  int batch = 0;
+  const int32_t* page_table = nullptr;  // (batch, max_pages)
+  int max_pages = 0, num_pages = 0;
+  const int32_t* seqused_k = nullptr;
+  void* k_pool = nullptr;  // (num_pages, hkv, 128, 128)
+  void* v_pool = nullptr;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s);
+
+struct RopeBwdArgs {
+  const void* dq_out = nullptr;  // (tokens, hq, 128)
+  const void* dk_out = nullptr;
+  const void* q = nullptr;  // token strides in elements
+  const void* k = nullptr;
+  long long q_stride = 0, k_stride = 0;
+  int f16 = 0;
+  const float* wq = nullptr;
+  const float* wk = nullptr;
+  const float* cos_sin = nullptr;
+  int max_position = 0, rotary = 0, interleaved = 0;
+  const int32_t* positions = nullptr;
+  float eps = 0.f;
+  int tokens = 0, hq = 0, hkv = 0;
+  void* dq = nullptr;
+  void* dk = nullptr;
+  long long dq_stride = 0, dk_stride = 0;
+  float* dwq = nullptr;  // (128)
+  float* dwk = nullptr;
+  float* partials = nullptr;  // (blocks, 128): Q's blocks, then K's
+  int q_blocks = 0;
+};
+struct RopeBwdGrid {
+  int q_blocks, k_blocks;
+};
+RopeBwdGrid rope_bwd_grid(long long tokens, int hq, int hkv);
+cudaError_t launch_rope_bwd(const RopeBwdArgs& a, int k_blocks, cudaStream_t s);
+
+// Pages of a cache (cache.cu). Pools are (num_pages, ...) arrays of
+// page_bytes per page that share one page numbering: K and V of every layer.
+constexpr int kMaxCachePools = 256;    // pools per launch (longer lists take several)
+constexpr int kMaxCacheRows = 16384;   // page table rows, and requests per call
+constexpr int kMaxCopyPairs = 4096;    // page pairs per copy call
+struct CachePools {
+  void* base[kMaxCachePools];
+};
+
+struct CacheAcceptArgs {
+  int num_pools = 0;
+  int row_bytes = 0;   // one token's row of one KV head
+  int hkv = 0;
+  const int32_t* page_table = nullptr;
+  int max_pages = 0, num_pages = 0, batch = 0;
+  const int32_t* seqused_k = nullptr;
+  const int32_t* cu_q = nullptr;
+  const int32_t* path = nullptr;      // (batch, max_path)
+  const int32_t* path_len = nullptr;  // (batch)
+  int max_path = 0;
+  int32_t* seqused_out = nullptr;
+};
+cudaError_t launch_cache_accept(const CachePools& p, const CacheAcceptArgs& a, cudaStream_t s);
+
+struct CacheTableArgs {
+  int32_t* page_table = nullptr;  // (num_rows, max_pages), -1 where a row has no page
+  int max_pages = 0, num_rows = 0, num_pages = 0;
+  int32_t* seqused_k = nullptr;   // (num_rows)
+  int32_t* page_refs = nullptr;   // (num_pages): table entries naming the page
+  const int32_t* rows = nullptr;  // (n): the rows freed, extended, or forked to
+  const int32_t* src_rows = nullptr;  // (n): fork only
+  const int32_t* lengths = nullptr;   // (n): extend only, the new lengths
+  int n = 0;
+  int32_t* status = nullptr;  // (n)
+  int32_t* plan = nullptr;    // fork: (n) the fresh page, -1 none, -2 refused; then the list
+  int32_t* list = nullptr;    // (num_pages): free pages, ascending
+};
+cudaError_t launch_cache_free(const CacheTableArgs& a, cudaStream_t s);
+cudaError_t launch_cache_extend(const CacheTableArgs& a, cudaStream_t s);
+// The plan and the tables; the begun pages' copies follow for each group of pools.
+cudaError_t launch_cache_fork(const CacheTableArgs& a, cudaStream_t s);
+cudaError_t launch_cache_fork_copy(const CachePools& p, int num_pools, long long page_bytes,
+                                   const CacheTableArgs& a, cudaStream_t s);
+cudaError_t launch_cache_copy_pages(const CachePools& p, int num_pools, long long page_bytes,
+                                    int num_pages, const int32_t* src, const int32_t* dst, int n,
+                                    cudaStream_t s);
 
 }  // namespace msa

@@ -225,6 +225,189 @@ msa_status_t msa_sparse_attention_nvfp4_prepare(
     size_t workspace_bytes, msa_attention_plan_t** plan);
 
 /*
+ * Attention for a tree of drafted tokens over a paged cache.
+ *
+ * A request's Lq query tokens are its last Lq keys as well (written to the
+ * cache before the call, e.g. by msa_qk_norm_rope_append), and which of them
+ * a token sees is its row of tree_mask: bit j % 32 of word j / 32 says that it
+ * sees its request's query token j, at cache position Lk - Lq + j. A tree of
+ * drafts sets the bits of a node's ancestors and its own; lower-triangular
+ * bits give the causal order. Earlier keys are seen as without a mask. As in
+ * msa_sparse_attention_fwd only the blocks that the token lists are attended,
+ * the drafts' own blocks included: list them. Everything else (layouts,
+ * dtypes, workspace, a row that sees nothing giving out = 0 and lse = -inf)
+ * is the paged msa_sparse_attention_fwd, not causal.
+ *   tree_mask   device uint32 (Tq, mask_words)
+ *   mask_words  words per row, at least max_seqlen_q / 32 rounded up; tokens
+ *               past 32 * mask_words are not seen
+ * K and V of the keys below seqused_k have to be finite; what the pages hold
+ * past them does not matter. A NULL or misaligned tree_mask, a NULL
+ * page_table or too few words: MSA_INVALID_ARG; otherwise as the forward.
+ * msa_tree_attention_prepare binds the call into a plan that
+ * msa_sparse_attention_run launches. Workspace:
+ * msa_sparse_attention_workspace_size (or _kv) with paged = 1. Rows at or past
+ * cu_seqlens_q[B] are left as they were.
+ */
+msa_status_t msa_tree_attention(
+    const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
+    const int32_t* q2k_indices, int topk, const int32_t* cu_seqlens_q, const uint32_t* tree_mask,
+    int mask_words, const int32_t* page_table, int max_pages, int num_pages,
+    const int32_t* seqused_k, int batch, int total_q, int num_qo_heads, int num_kv_heads,
+    int head_dim, int max_seqlen_q, float softmax_scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream);
+msa_status_t msa_tree_attention_prepare(
+    const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
+    const int32_t* q2k_indices, int topk, const int32_t* cu_seqlens_q, const uint32_t* tree_mask,
+    int mask_words, const int32_t* page_table, int max_pages, int num_pages,
+    const int32_t* seqused_k, int batch, int total_q, int num_qo_heads, int num_kv_heads,
+    int head_dim, int max_seqlen_q, float softmax_scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, msa_attention_plan_t** plan);
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the
+ * same pass: what makes the attention's q and k out of a projection's output.
+ *
+ * Each row x of 128 values (one token, one head) becomes R(x r w) with
+ * r = (mean of x^2 + eps)^(-1/2), w the weight of q or of k, and R the
+ * rotation of the first rotary_dim elements by the token's table row:
+ * (a, b) -> (a c - b s, b c + a s) for the pairs (i, i + rotary_dim / 2), or
+ * (2 i, 2 i + 1) when interleaved, with c = row[i], s = row[rotary_dim / 2 + i].
+ * Computed in float32, rounded once.
+ *
+ *   q, k         device, dtype MSA_BF16 or MSA_FP16, (T, Hq, d) and (T, Hkv, d)
+ *                with heads contiguous and token strides q_stride, k_stride in
+ *                elements (multiples of 8, at least a token's own size): slices
+ *                of a packed projection are taken as they are
+ *   q_weight, k_weight  device float32 (d)
+ *   cos_sin      device float32 (max_position, rotary_dim); NULL with rotary_dim 0
+ *   positions    device int32 (T). A token whose position is outside
+ *                [0, max_position) is padding: its rows of q_out and k_out are
+ *                zeros, its cache rows are left as they were, and it has no
+ *                part in a gradient.
+ *   rotary_dim   0 (norm only) to 128, a multiple of 16
+ *   eps          positive, finite
+ *   q_out, k_out device, (T, Hq, d) and (T, Hkv, d), of q's dtype; may be the
+ *                inputs themselves when those are contiguous
+ * MSA_INVALID_ARG for a NULL or misaligned pointer (per-token arrays may be
+ * NULL when T is 0), sizes below 1 (T may be 0), a stride other than above or
+ * a bad eps; MSA_UNSUPPORTED for head_dim != 128, another dtype
+ * or rotary_dim, or T * (Hq + 2 Hkv) >= 2^31.
+ *
+ * msa_qk_norm_rope_append writes K (normalised and rotated) and V (as it is)
+ * to a paged cache in the place of k_out. Token t, the i-th of the Lq tokens
+ * of sequence b (cu_seqlens_q), goes to position seqused_k[b] - Lq + i of the
+ * row b of page_table, where the attention finds it (seqused_k counts the new
+ * tokens). Positions for the rotation are given apart, as tokens of a tree
+ * share them. Pools are (num_pages, Hkv, 128, d) of kv_dtype: q's dtype, or
+ * MSA_FP8_E4M3 with bf16 q (rounded to nearest even, magnitudes above 448 as
+ * 448). A token without a mapped page is not written to the cache; tokens at
+ * or past cu_seqlens_q[batch] are not written at all, q_out included. No two
+ * tokens of a call may share a cache row.
+ */
+msa_status_t msa_qk_norm_rope(const void* q, long long q_stride, const void* k, long long k_stride,
+                              msa_dtype_t dtype, const float* q_weight, const float* k_weight,
+                              float eps, const float* cos_sin, int max_position, int rotary_dim,
+                              int interleaved, const int32_t* positions, int total_q,
+                              int num_qo_heads, int num_kv_heads, int head_dim, void* q_out,
+                              void* k_out, cudaStream_t stream);
+msa_status_t msa_qk_norm_rope_append(
+    const void* q, long long q_stride, const void* k, long long k_stride, const void* v,
+    long long v_stride, msa_dtype_t dtype, const float* q_weight, const float* k_weight, float eps,
+    const float* cos_sin, int max_position, int rotary_dim, int interleaved,
+    const int32_t* positions, const int32_t* cu_seqlens_q, int batch, const int32_t* page_table,
+    int max_pages, int num_pages, const int32_t* seqused_k, int total_q, int num_qo_heads,
+    int num_kv_heads, int head_dim, void* q_out, void* k_pool, void* v_pool,
+    msa_dtype_t kv_dtype, cudaStream_t stream);
+
+/*
+ * Gradients of msa_qk_norm_rope. dq_out and dk_out, contiguous, are those of
+ * its outputs; q, k and the rest its inputs. With u = R^T dy and g = u w:
+ * dx = r (g - x r^2 mean(g x)), in the inputs' dtype with token strides
+ * dq_stride, dk_stride (as the inputs' rules), and the weights' gradients
+ * sum u x r over all tokens and heads, float32 (d), summed in a fixed order:
+ * the same inputs give the same bits. dq, dk may be dq_out, dk_out when their
+ * strides are the contiguous ones.
+ * workspace: msa_qk_norm_rope_bwd_workspace_size(...) bytes, 256-byte aligned,
+ * uninitialised; calls that share one must be ordered on the device.
+ */
+size_t msa_qk_norm_rope_bwd_workspace_size(int total_q, int num_qo_heads, int num_kv_heads);
+msa_status_t msa_qk_norm_rope_bwd(
+    const void* dq_out, const void* dk_out, const void* q, long long q_stride, const void* k,
+    long long k_stride, msa_dtype_t dtype, const float* q_weight, const float* k_weight, float eps,
+    const float* cos_sin, int max_position, int rotary_dim, int interleaved,
+    const int32_t* positions, int total_q, int num_qo_heads, int num_kv_heads, int head_dim,
+    void* dq, long long dq_stride, void* dk, long long dk_stride, float* dq_weight,
+    float* dk_weight, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Pages of a cache.
+ *
+ * `pools` is a host array of num_pools device pointers: the K and V pools of
+ * every layer, which share one page numbering, each num_pages pages of
+ * page_bytes contiguous bytes (a multiple of 16). Sequences are rows of
+ * page_table (num_rows, max_pages), -1 where a row has no page, with their
+ * lengths seqused_k; page_refs (num_pages) counts the entries that name each
+ * page, and a page whose count is 0 is free. A caller starts with -1, 0 and 0.
+ * A request that cannot be carried out changes nothing and says so in
+ * status (device int32, one per request): 0 done, 1 refused, 2 no free page.
+ * Free pages are handed out lowest first, in the order of the requests; once
+ * one finds too few, none after it gets any. num_rows and the number of
+ * requests are at most 16384 (MSA_UNSUPPORTED above).
+ *
+ * msa_cache_extend: row rows[i] grows to lengths[i] tokens: a page for each
+ *   block below the new length that has none (from the block that the row
+ *   ends in on). Refused: a row out of range or already listed, a length
+ *   below the present one or above max_pages * 128.
+ * msa_cache_fork: row dst_rows[i] becomes a copy of row src_rows[i] with the
+ *   same length: whole pages are shared (their counts rise), a page that the
+ *   row ends in is copied to a free one in every pool. Refused: a row out of
+ *   range, a destination already listed or not empty, a source that is a
+ *   destination of the call.
+ * msa_cache_free: the rows' pages lose a holder each; the rows are empty
+ *   after it. Rows out of range are passed over, and a row is freed once.
+ * msa_cache_copy_pages: page src_pages[i] to page dst_pages[i] in every pool,
+ *   at most 4096 pairs. A pair is passed over when a page is outside the pool,
+ *   when a later pair has its destination, or when its source is another
+ *   pair's destination.
+ * msa_cache_accept: of request b's Lq drafted tokens (its last Lq cache
+ *   positions) the path path[b, 0 .. path_len[b]) is kept: the row of its j-th
+ *   moves to position Lk - Lq + j in every pool, and seqused_out[b] = Lk - Lq
+ *   + the path's length. path (batch, max_path) ascends; it ends before an
+ *   entry that does not, or that names no draft. Rows without a mapped page
+ *   are not moved. Pools are (num_pages, Hkv, 128, row_bytes) with row_bytes a
+ *   multiple of 16 (256 for 16-bit and 128 for E4M3 caches of head_dim 128;
+ *   planar NVFP4 pages are not made of rows and cannot be given here).
+ *   seqused_out is another array than seqused_k. The request's last pages must
+ *   be its own (as extend and fork leave them).
+ * workspace of msa_cache_fork and msa_cache_extend: as their size query says,
+ * 256-byte aligned, uninitialised; calls that share one, or the same tables,
+ * must be ordered on the device. MSA_INVALID_ARG for a NULL or misaligned
+ * pointer (page_table, seqused_k, ... 4 bytes, pools 16) or sizes below 1
+ * (n may be 0).
+ */
+size_t msa_cache_workspace_size(int n, int num_pages);
+msa_status_t msa_cache_extend(int32_t* page_table, int max_pages, int num_rows, int32_t* seqused_k,
+                              int32_t* page_refs, int num_pages, const int32_t* rows,
+                              const int32_t* lengths, int n, int32_t* status, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+msa_status_t msa_cache_fork(void* const* pools, int num_pools, long long page_bytes,
+                            int32_t* page_table, int max_pages, int num_rows, int32_t* seqused_k,
+                            int32_t* page_refs, int num_pages, const int32_t* src_rows,
+                            const int32_t* dst_rows, int n, int32_t* status, void* workspace,
+                            size_t workspace_bytes, cudaStream_t stream);
+msa_status_t msa_cache_free(int32_t* page_table, int max_pages, int num_rows, int32_t* seqused_k,
+                            int32_t* page_refs, int num_pages, const int32_t* rows, int n,
+                            cudaStream_t stream);
+msa_status_t msa_cache_copy_pages(void* const* pools, int num_pools, long long page_bytes,
+                                  int num_pages, const int32_t* src_pages,
+                                  const int32_t* dst_pages, int n, cudaStream_t stream);
+msa_status_t msa_cache_accept(void* const* pools, int num_pools, int row_bytes, int num_kv_heads,
+                              const int32_t* page_table, int max_pages, int num_pages, int batch,
+                              const int32_t* seqused_k, const int32_t* cu_seqlens_q,
+                              const int32_t* path, const int32_t* path_len, int max_path,
+                              int32_t* seqused_out, cudaStream_t stream);
+
+/*
  * Dense proxy pass, MSA stage 1 ("flashinfer.msa_ops.msa_proxy_score").
  *
  * output[h, t, q] = max over the keys j of KV block t of the UNSCALED logit
