@@ -2,9 +2,10 @@
 
 Thin Python binding over the C ABI of ``libmsa.so`` (declared in
 ``include/msa.h``). Every function here only marshals torch CUDA tensors into
-raw device pointers and sizes and calls the C entry point of the same name;
-all computation happens in the library's CUDA kernels. There is no fallback:
-if the library has not been built, every call raises.
+raw device pointers and sizes and calls the C entry point of the same name
+(with ctypes, or through the compiled module ``_binding`` for the operators
+around the attention); all computation happens in the library's CUDA kernels.
+There is no fallback: if the library has not been built, every call raises.
 
 Convenience defaults that need information the C ABI takes explicitly
 (``max_seqlen_q``, ``max_k_tiles``) are derived here from ``cu_seqlens`` /
@@ -599,70 +600,25 @@ def msa_selftest_wait_timeout(timeout_us, stream=None):
 
 # --------------------------------------------------------------------------
 # A serving step around the attention: q, k and v from a projection, attention
-# of drafted trees, and the cache's pages
+# of drafted trees, and the cache's pages. Their arguments are checked and
+# their outputs allocated by a compiled binding (csrc/binding.cpp): shapes,
+# dtypes and devices that do not fit raise ValueError or TypeError before
+# anything is launched. All tensors of a call are on one device, which need
+# not be the current one; ``stream`` defaults to that device's current stream,
+# and outputs and workspaces are allocated on the stream the call runs on.
 # --------------------------------------------------------------------------
-def _tensor(name, t, device, dtypes, shape, contiguous=True):
-    """Checks one tensor argument; None in ``shape`` stands for any size."""
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must be a CUDA tensor on {device or 'a GPU'}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+_native = None
 
 
-_F32, _I32 = (torch.float32,), (torch.int32,)
-_HALVES = (torch.bfloat16, torch.float16)
-
-
-def _heads(name, t, device, dtypes, shape):
-    """A (tokens, heads, 128) tensor whose heads are contiguous; returns its
-    token stride."""
-    _tensor(name, t, device, dtypes, shape, contiguous=False)
-    tokens, heads, d = t.shape
-    if tokens and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
-        raise ValueError(f"{name}: each token's heads must be contiguous")
-    return t.stride(0) if tokens > 1 else heads * d
-
-
-def _empty(shape, dtype, device, stream):
-    """An uninitialised tensor that belongs to the stream the call runs on."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _call(name, device, stream, *args):
-    """Calls the C entry point on ``device``, on ``stream`` or its current one."""
-    fn = getattr(lib(), name)
-    if device.index == torch.cuda.current_device():
-        st = fn(*args, _stream(stream))
-    else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream(stream))
-    if st != MSA_OK:
-        raise MSAError(name, st)
-
-
-def _rope_args(q, k, q_weight, k_weight, cos_sin, positions):
-    """The checks of the norm and rotation's inputs; returns the device, the
-    token strides, max_position and rotary_dim."""
-    dev = q.device
-    qs = _heads("q", q, None, _HALVES, (None, None, 128))
-    ks = _heads("k", k, dev, (q.dtype,), (q.shape[0], None, 128))
-    _tensor("q_weight", q_weight, dev, _F32, (128,))
-    _tensor("k_weight", k_weight, dev, _F32, (128,))
-    _tensor("positions", positions, dev, _I32, (q.shape[0],))
-    if cos_sin is None:
-        return dev, qs, ks, (1 << 31) - 1, 0
-    _tensor("cos_sin", cos_sin, dev, _F32, (None, None))
-    return dev, qs, ks, cos_sin.shape[0], cos_sin.shape[1]
+def _step():
+    """The compiled binding. Raises if it was never built."""
+    global _native
+    if _native is None:
+        lib()
+        from . import _binding as module
+        module.set_error(MSAError)
+        _native = module
+    return _native
 
 
 def msa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, *, eps=1e-6, interleaved=False,
@@ -675,15 +631,8 @@ def msa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, *, eps=1e-6, 
     position's cosines and then its sines; None only normalises. Returns
     ``(q_out, k_out)``, contiguous.
     """
-    dev, qs, ks, most, rotary = _rope_args(q, k, q_weight, k_weight, cos_sin, positions)
-    q_out = _empty(q.shape, q.dtype, dev, stream) if q_out is None else _tensor(
-        "q_out", q_out, dev, (q.dtype,), q.shape)
-    k_out = _empty(k.shape, k.dtype, dev, stream) if k_out is None else _tensor(
-        "k_out", k_out, dev, (q.dtype,), k.shape)
-    _call("msa_qk_norm_rope", dev, stream, _p(q), qs, _p(k), ks, _dtype_code(q), _p(q_weight),
-          _p(k_weight), float(eps), _p(cos_sin), most, rotary, int(bool(interleaved)),
-          _p(positions), q.shape[0], q.shape[1], k.shape[1], 128, _p(q_out), _p(k_out))
-    return q_out, k_out
+    return (_native or _step()).qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps,
+                                              interleaved, q_out, k_out, stream)
 
 
 def msa_qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, cu_seqlens_q, k_pool,
@@ -693,24 +642,9 @@ def msa_qk_norm_rope_append(q, k, v, q_weight, k_weight, cos_sin, positions, cu_
     (num_pages, Hkv, 128, 128) of q's dtype or E4M3; see
     ``msa_qk_norm_rope_append`` in include/msa.h. ``seqused_k`` counts the new
     tokens, which are their sequences' last. Returns ``q_out``."""
-    dev, qs, ks, most, rotary = _rope_args(q, k, q_weight, k_weight, cos_sin, positions)
-    hkv = k.shape[1]
-    vs = _heads("v", v, dev, (q.dtype,), k.shape)
-    batch = cu_seqlens_q.shape[0] - 1
-    _tensor("cu_seqlens_q", cu_seqlens_q, dev, _I32, (None,))
-    _tensor("page_table", page_table, dev, _I32, (batch, None))
-    _tensor("seqused_k", seqused_k, dev, _I32, (batch,))
-    _tensor("k_pool", k_pool, dev, _HALVES + (torch.float8_e4m3fn, torch.uint8),
-            (None, hkv, 128, 128))
-    _tensor("v_pool", v_pool, dev, (k_pool.dtype,), k_pool.shape)
-    q_out = _empty(q.shape, q.dtype, dev, stream) if q_out is None else _tensor(
-        "q_out", q_out, dev, (q.dtype,), q.shape)
-    _call("msa_qk_norm_rope_append", dev, stream, _p(q), qs, _p(k), ks, _p(v), vs, _dtype_code(q),
-          _p(q_weight), _p(k_weight), float(eps), _p(cos_sin), most, rotary,
-          int(bool(interleaved)), _p(positions), _p(cu_seqlens_q), batch, _p(page_table),
-          page_table.shape[1], k_pool.shape[0], _p(seqused_k), q.shape[0], q.shape[1], hkv, 128,
-          _p(q_out), _p(k_pool), _p(v_pool), _dtype_code(k_pool))
-    return q_out
+    return (_native or _step()).qk_norm_rope_append(
+        q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, v, cu_seqlens_q, k_pool,
+        v_pool, page_table, seqused_k, q_out, stream)
 
 
 def msa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions, *, eps=1e-6,
@@ -719,63 +653,9 @@ def msa_qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, posi
     """Gradients of ``msa_qk_norm_rope``: ``(dq, dk, dq_weight, dk_weight)``;
     see ``msa_qk_norm_rope_bwd`` in include/msa.h. ``dq`` and ``dk`` may be
     slices of a packed gradient."""
-    dev, qs, ks, most, rotary = _rope_args(q, k, q_weight, k_weight, cos_sin, positions)
-    _tensor("dq_out", dq_out, dev, (q.dtype,), q.shape)
-    _tensor("dk_out", dk_out, dev, (q.dtype,), k.shape)
-    dq = _empty(q.shape, q.dtype, dev, stream) if dq is None else dq
-    dk = _empty(k.shape, k.dtype, dev, stream) if dk is None else dk
-    dqs = _heads("dq", dq, dev, (q.dtype,), q.shape)
-    dks = _heads("dk", dk, dev, (q.dtype,), k.shape)
-    dq_weight = _empty((128,), torch.float32, dev, stream) if dq_weight is None else _tensor(
-        "dq_weight", dq_weight, dev, _F32, (128,))
-    dk_weight = _empty((128,), torch.float32, dev, stream) if dk_weight is None else _tensor(
-        "dk_weight", dk_weight, dev, _F32, (128,))
-    if workspace is None:
-        need = lib().msa_qk_norm_rope_bwd_workspace_size(q.shape[0], q.shape[1], k.shape[1])
-        workspace = _empty((max(need, 256),), torch.uint8, dev, stream)
-    _tensor("workspace", workspace, dev, (torch.uint8,), (None,))
-    _call("msa_qk_norm_rope_bwd", dev, stream, _p(dq_out), _p(dk_out), _p(q), qs, _p(k), ks,
-          _dtype_code(q), _p(q_weight), _p(k_weight), float(eps), _p(cos_sin), most, rotary,
-          int(bool(interleaved)), _p(positions), q.shape[0], q.shape[1], k.shape[1], 128, _p(dq),
-          dqs, _p(dk), dks, _p(dq_weight), _p(dk_weight), _p(workspace), workspace.numel())
-    return dq, dk, dq_weight, dk_weight
-
-
-def _tree_args(q, k, v, q2k_indices, cu_seqlens_q, tree_mask, page_table, seqused_k, max_seqlen_q,
-               softmax_scale, return_softmax_lse, out, lse, workspace, stream):
-    dev = q.device
-    _tensor("q", q, None, _HALVES, (None, None, 128))
-    total_q, hq, d = q.shape
-    batch = cu_seqlens_q.shape[0] - 1
-    _tensor("k", k, dev, _HALVES + (torch.float8_e4m3fn, torch.uint8), (None, None, 128, 128))
-    _tensor("v", v, dev, (k.dtype,), k.shape)
-    hkv = k.shape[1]
-    _tensor("q2k_indices", q2k_indices, dev, _I32, (hkv, total_q, None))
-    _tensor("cu_seqlens_q", cu_seqlens_q, dev, _I32, (None,))
-    _tensor("tree_mask", tree_mask, dev, (torch.int32, torch.uint32), (total_q, None))
-    _tensor("page_table", page_table, dev, _I32, (batch, None))
-    _tensor("seqused_k", seqused_k, dev, _I32, (batch,))
-    topk = q2k_indices.shape[2]
-    if max_seqlen_q is None:
-        max_seqlen_q = _q_bound(cu_seqlens_q, total_q)
-    out = _empty(q.shape, q.dtype, dev, stream) if out is None else _tensor(
-        "out", out, dev, (q.dtype,), q.shape)
-    if lse is None and return_softmax_lse:
-        lse = _empty((total_q, hq), torch.float32, dev, stream)
-    if lse is not None:
-        _tensor("lse", lse, dev, _F32, (total_q, hq))
-    if workspace is None:
-        need = msa_sparse_attention_workspace_size_kv(
-            batch, total_q, hq, hkv, d, topk, max(1, max_seqlen_q), True, _dtype_code(k),
-            page_table.shape[1])
-        workspace = _empty((max(need, 256),), torch.uint8, dev, stream)
-    _tensor("workspace", workspace, dev, (torch.uint8,), (None,))
-    args = (_p(q), _dtype_code(q), _p(k), _p(v), _dtype_code(k), _p(q2k_indices), topk,
-            _p(cu_seqlens_q), _p(tree_mask), tree_mask.shape[1], _p(page_table),
-            page_table.shape[1], k.shape[0], _p(seqused_k), batch, total_q, hq, hkv, d,
-            int(max_seqlen_q), float(softmax_scale) if softmax_scale is not None else 0.0,
-            _p(out), _p(lse), _p(workspace), workspace.numel())
-    return args, out, lse, workspace
+    return (_native or _step()).qk_norm_rope_bwd(
+        q, k, q_weight, k_weight, cos_sin, positions, eps, interleaved, dq_out, dk_out, dq, dk,
+        dq_weight, dk_weight, workspace, stream)
 
 
 def msa_tree_attention(q, k, v, q2k_indices, cu_seqlens_q, tree_mask, *, page_table, seqused_k,
@@ -785,12 +665,12 @@ def msa_tree_attention(q, k, v, q2k_indices, cu_seqlens_q, tree_mask, *, page_ta
     ``msa_tree_attention`` in include/msa.h. ``tree_mask`` (Tq, words) int32
     holds each token's visible nodes as bits. Returns ``out`` or ``(out,
     lse)``. ``max_seqlen_q=None`` reads the device as the forward does."""
-    args, out, lse, _ = _tree_args(q, k, v, q2k_indices, cu_seqlens_q, tree_mask, page_table,
-                                   seqused_k, max_seqlen_q, softmax_scale, return_softmax_lse,
-                                   out, lse, workspace, stream)
-    if q.shape[0]:  # torch gives an empty tensor no address
-        _call("msa_tree_attention", q.device, stream, *args)
-    return (out, lse) if lse is not None else out
+    if max_seqlen_q is None:
+        max_seqlen_q = _q_bound(cu_seqlens_q, q.shape[0])
+    out, lse, _, _ = (_native or _step()).tree_attention(
+        q, k, v, q2k_indices, cu_seqlens_q, tree_mask, page_table, seqused_k, max_seqlen_q,
+        softmax_scale, return_softmax_lse, out, lse, workspace, stream, False)
+    return out if lse is None else (out, lse)
 
 
 class TreeAttentionRunner(SparseAttentionRunner):
@@ -800,58 +680,14 @@ class TreeAttentionRunner(SparseAttentionRunner):
     def __init__(self, q, k, v, q2k_indices, cu_seqlens_q, tree_mask, *, page_table, seqused_k,
                  max_seqlen_q=None, softmax_scale=None, return_softmax_lse=False, out=None,
                  lse=None, workspace=None):
-        L = lib()
-        args, self.out, self.lse, self.workspace = _tree_args(
+        if max_seqlen_q is None:
+            max_seqlen_q = _q_bound(cu_seqlens_q, q.shape[0])
+        self.out, self.lse, self.workspace, plan = (_native or _step()).tree_attention(
             q, k, v, q2k_indices, cu_seqlens_q, tree_mask, page_table, seqused_k, max_seqlen_q,
-            softmax_scale, return_softmax_lse, out, lse, workspace, None)
+            softmax_scale, return_softmax_lse, out, lse, workspace, None, True)
         self._bound = (q, k, v, q2k_indices, cu_seqlens_q, tree_mask, page_table, seqused_k)
-        plan = C.c_void_p()
-        with torch.cuda.device(q.device):
-            _check("msa_tree_attention_prepare",
-                   L.msa_tree_attention_prepare(*args, C.byref(plan)))
-        self._plan = plan
-        self._lib = L
-
-
-def _pools(pools):
-    """The pools of a cache as (device, host pointer array, their number,
-    pages, bytes per page, shape of a page). ``pools``: tensors (num_pages,
-    ...) of one shape and dtype, K and V of every layer, or one tensor with a
-    leading dimension over them."""
-    if torch.is_tensor(pools):
-        if pools.dim() < 3 or not pools.is_cuda:
-            raise ValueError("pools must be CUDA tensors of shape (num_pools, num_pages, ...)")
-        n, shape = pools.shape[0], pools.shape[1:]
-        if n < 1 or not pools[0].is_contiguous():
-            raise ValueError("pools: each pool must be contiguous")
-        base, step = pools.data_ptr(), pools.stride(0) * pools.element_size()
-        at, first = [base + i * step for i in range(n)], pools
-    else:
-        n, first = len(pools), pools[0] if len(pools) else None
-        if n < 1 or first.dim() < 2:
-            raise ValueError("pools must be tensors of shape (num_pages, ...)")
-        shape = first.shape
-        for t in pools:
-            _tensor("pools", t, first.device, (first.dtype,), shape)
-        at = [t.data_ptr() for t in pools]
-    page = shape[1:].numel() * first.element_size()
-    return first.device, (C.c_void_p * n)(*at), n, shape[0], page, shape[1:]
-
-
-def _tables(device, page_table, seqused_k, page_refs):
-    """The checks of the cache's tables; returns their C arguments."""
-    _tensor("page_table", page_table, device, _I32, (None, None))
-    rows, width = page_table.shape
-    _tensor("seqused_k", seqused_k, page_table.device, _I32, (rows,))
-    _tensor("page_refs", page_refs, page_table.device, _I32, (None,))
-    return (_p(page_table), width, rows, _p(seqused_k), _p(page_refs), page_refs.shape[0])
-
-
-def _cache_workspace(workspace, n, num_pages, dev, stream):
-    if workspace is None:
-        need = lib().msa_cache_workspace_size(n, num_pages)
-        return _empty((max(need, 256),), torch.uint8, dev, stream)
-    return _tensor("workspace", workspace, dev, (torch.uint8,), (None,))
+        self._plan = C.c_void_p(plan)
+        self._lib = lib()
 
 
 def msa_cache_extend(page_table, seqused_k, page_refs, rows, lengths, *, status=None,
@@ -859,17 +695,8 @@ def msa_cache_extend(page_table, seqused_k, page_refs, rows, lengths, *, status=
     """Rows of a page table grow to new lengths; see ``msa_cache_extend`` in
     include/msa.h. Returns ``status`` (n,) int32: 0 done, 1 refused, 2 no free
     page."""
-    dev = page_table.device
-    tables = _tables(None, page_table, seqused_k, page_refs)
-    _tensor("rows", rows, dev, _I32, (None,))
-    n = rows.shape[0]
-    _tensor("lengths", lengths, dev, _I32, (n,))
-    status = _empty((n,), torch.int32, dev, stream) if status is None else _tensor(
-        "status", status, dev, _I32, (n,))
-    workspace = _cache_workspace(workspace, n, page_refs.shape[0], dev, stream)
-    _call("msa_cache_extend", dev, stream, *tables, _p(rows), _p(lengths), n, _p(status),
-          _p(workspace), workspace.numel())
-    return status
+    return (_native or _step()).cache_extend(page_table, seqused_k, page_refs, rows, lengths,
+                                              status, workspace, stream)
 
 
 def msa_cache_fork(pools, page_table, seqused_k, page_refs, src_rows, dst_rows, *, status=None,
@@ -878,37 +705,19 @@ def msa_cache_fork(pools, page_table, seqused_k, page_refs, src_rows, dst_rows, 
     ``msa_cache_fork`` in include/msa.h. ``pools``: the K and V pools of every
     layer, as a list or stacked in one tensor. Returns ``status`` (n,) int32:
     0 done, 1 refused, 2 no free page."""
-    dev, at, num_pools, num_pages, page, _ = _pools(pools)
-    tables = _tables(dev, page_table, seqused_k, page_refs)
-    if page_refs.shape[0] != num_pages:
-        raise ValueError("page_refs must have an entry for each page of the pools")
-    _tensor("src_rows", src_rows, dev, _I32, (None,))
-    n = src_rows.shape[0]
-    _tensor("dst_rows", dst_rows, dev, _I32, (n,))
-    status = _empty((n,), torch.int32, dev, stream) if status is None else _tensor(
-        "status", status, dev, _I32, (n,))
-    workspace = _cache_workspace(workspace, n, num_pages, dev, stream)
-    _call("msa_cache_fork", dev, stream, at, num_pools, page, *tables, _p(src_rows), _p(dst_rows),
-          n, _p(status), _p(workspace), workspace.numel())
-    return status
+    return (_native or _step()).cache_fork(page_table, seqused_k, page_refs, pools, src_rows,
+                                            dst_rows, status, workspace, stream)
 
 
 def msa_cache_free(page_table, seqused_k, page_refs, rows, *, stream=None):
     """Empties rows of a page table; see ``msa_cache_free`` in include/msa.h."""
-    dev = page_table.device
-    tables = _tables(None, page_table, seqused_k, page_refs)
-    _tensor("rows", rows, dev, _I32, (None,))
-    _call("msa_cache_free", dev, stream, *tables, _p(rows), rows.shape[0])
+    (_native or _step()).cache_free(page_table, seqused_k, page_refs, rows, stream)
 
 
 def msa_cache_copy_pages(pools, src_pages, dst_pages, *, stream=None):
     """Copies pages in every pool; see ``msa_cache_copy_pages`` in
     include/msa.h."""
-    dev, at, num_pools, num_pages, page, _ = _pools(pools)
-    _tensor("src_pages", src_pages, dev, _I32, (None,))
-    _tensor("dst_pages", dst_pages, dev, _I32, src_pages.shape)
-    _call("msa_cache_copy_pages", dev, stream, at, num_pools, page, num_pages, _p(src_pages),
-          _p(dst_pages), src_pages.shape[0])
+    (_native or _step()).cache_copy_pages(pools, src_pages, dst_pages, stream)
 
 
 def msa_cache_accept(pools, page_table, seqused_k, cu_seqlens_q, path, path_len, *,
@@ -917,19 +726,5 @@ def msa_cache_accept(pools, page_table, seqused_k, cu_seqlens_q, path, path_len,
     ``msa_cache_accept`` in include/msa.h. ``pools``: (num_pages, Hkv, 128, d)
     K and V pools of every layer, as a list or stacked in one tensor. Returns
     ``seqused_out`` (B,) int32, the lengths after it."""
-    dev, at, num_pools, num_pages, _, shape = _pools(pools)
-    if len(shape) != 3 or shape[1] != 128:
-        raise ValueError("pools must have shape (num_pages, Hkv, 128, d)")
-    size = (pools if torch.is_tensor(pools) else pools[0]).element_size()
-    batch = cu_seqlens_q.shape[0] - 1
-    _tensor("cu_seqlens_q", cu_seqlens_q, dev, _I32, (None,))
-    _tensor("page_table", page_table, dev, _I32, (batch, None))
-    _tensor("seqused_k", seqused_k, dev, _I32, (batch,))
-    _tensor("path", path, dev, _I32, (batch, None))
-    _tensor("path_len", path_len, dev, _I32, (batch,))
-    seqused_out = _empty((batch,), torch.int32, dev, stream) if seqused_out is None else _tensor(
-        "seqused_out", seqused_out, dev, _I32, (batch,))
-    _call("msa_cache_accept", dev, stream, at, num_pools, shape[2] * size, shape[0],
-          _p(page_table), page_table.shape[1], num_pages, batch, _p(seqused_k), _p(cu_seqlens_q),
-          _p(path), _p(path_len), path.shape[1], _p(seqused_out))
-    return seqused_out
+    return (_native or _step()).cache_accept(pools, page_table, seqused_k, cu_seqlens_q, path,
+                                              path_len, seqused_out, stream)
