@@ -84,6 +84,8 @@ def lib():
         L.msa_sparse_attention_nvfp4_prepare.argtypes = fp4 + [C.POINTER(vp)]
         tree = [vp, i32, vp, vp, i32, vp, i32, vp, vp, i32, vp, i32, i32, vp, i32, i32, i32, i32,
                 i32, i32, f32, vp, vp, vp, sz]
+        L.msa_tree_attention_workspace_size.restype = sz
+        L.msa_tree_attention_workspace_size.argtypes = [i32] * 7
         L.msa_tree_attention.restype = i32
         L.msa_tree_attention.argtypes = tree + [vp]
         L.msa_tree_attention_prepare.restype = i32

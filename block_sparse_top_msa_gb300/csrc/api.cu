@@ -391,6 +391,8 @@ struct ForwardPlan {
   PrefillArgs a{};
   bool swapped = false;  // the swapped-orientation prefill kernel, else the union-tile kernel
   bool skip_union = false;  // direct mode: the attention kernel builds one-token unions itself
+  bool tree = false;        // msa_tree_attention: launch_tree alone
+  TreeArgs t{};
   bool fp4_decode = false;  // packed-NVFP4 decode-shaped call: fp4_decode_kernel alone
   Fp4DecodeArgs f4{};
 };
@@ -485,8 +487,7 @@ msa_status_t build_forward(
     const int32_t* cu_seqlens_k, const int32_t* page_table, int max_pages, int num_pages,
     const int32_t* seqused_k, int batch, int total_q, int total_k, int num_qo_heads,
     int num_kv_heads, int head_dim, int max_seqlen_q, int causal, float softmax_scale, void* out,
-    float* lse, void* workspace, size_t workspace_bytes, ForwardPlan* plan,
-    const uint32_t* tree_mask = nullptr, int mask_words = 0) {
+    float* lse, void* workspace, size_t workspace_bytes, ForwardPlan* plan) {
   // ---- argument checks (host only; nothing is read from the device) ----
   const bool paged = page_table != nullptr;
   if (cu_seqlens_k != nullptr && paged) return MSA_INVALID_ARG;   // two length sources
@@ -559,7 +560,7 @@ msa_status_t build_forward(
 
   const SwappedLayout S =
       swapped_layout(batch, total_q, num_qo_heads, num_kv_heads, topk, max_seqlen_q);
-  if (tree_mask == nullptr && use_swapped(S, esize, max_seqlen_q))
+  if (use_swapped(S, esize, max_seqlen_q))
     return build_swapped(q, q_dtype, k, v, q2k_indices, topk, cu_seqlens_q, cu_seqlens_k,
                          page_table, max_pages, num_pages, seqused_k, batch, total_q, total_k,
                          num_qo_heads, num_kv_heads, causal, scale_log2, out, lse, ws, S, fault,
@@ -643,13 +644,68 @@ msa_status_t build_forward(
   // The counter reset before a direct launch is an ordinary launch, so every
   // earlier kernel (a decode pass included) has completed when it starts.
   a.wait_late = a.direct;
-  a.tree_mask = tree_mask;
-  a.mask_words = mask_words;
   return MSA_OK;
 }
 
-// The tree form of the paged forward: the same checks and plan, not causal,
-// with the mask over each sequence's own query tokens.
+// Layout of the tree attention: units of up to two MMA tiles of consecutive
+// tokens, their unions, and the partials of the units that the CTAs' ranges
+// cut.
+struct TreeLayout {
+  int W, unit_tokens, max_tiles, cap, words, grid, rows_part;
+  size_t off_info, off_len, off_blocks, off_member, off_part_o, off_part_ml, off_cut, total;
+};
+
+// Most tokens of a unit and pages of a sequence: what the union kernel's
+// shared memory holds at the longest lists (128 KB of membership bits, 64 KB
+// of a bitmap and its ranks).
+constexpr int kTreeMaxTokens = 128;
+constexpr int kTreeMaxPages = 1 << 18;
+// Fewest blocks a CTA takes.
+constexpr int kTreeMinRange = 2;
+// Blocks' time that partials and their joining take.
+constexpr int kTreeCutCost = 6;
+
+TreeLayout tree_layout(int batch, int total_q, int hq, int hkv, int topk, int max_seqlen_q) {
+  TreeLayout L{};
+  const int G = hq / hkv, sq = max_seqlen_q < 1 ? 1 : max_seqlen_q;
+  L.W = tile_tokens_for(hq, hkv);
+  if (sq < L.W) L.W = sq;
+  L.unit_tokens = 2 * L.W;
+  if (L.unit_tokens > sq) L.unit_tokens = sq;
+  if (L.unit_tokens > kTreeMaxTokens) L.unit_tokens = kTreeMaxTokens;
+  long long mt = ((long long)total_q + L.unit_tokens - 1) / L.unit_tokens + batch;
+  if (total_q > 0 && mt > total_q) mt = total_q;
+  if (L.unit_tokens >= sq && mt > batch) mt = batch;
+  if (mt < 1) mt = 1;
+  L.max_tiles = (int)mt;
+  L.cap = L.unit_tokens * topk;
+  L.words = (L.cap + 31) / 32;
+  L.rows_part = L.unit_tokens * G;
+  const long long units = (long long)hkv * L.max_tiles;
+  const long long most = (units * L.cap * 2 + kTreeMinRange - 1) / kTreeMinRange;
+  L.grid = most < kPlanSMs ? (int)(most < 1 ? 1 : most) : kPlanSMs;
+  size_t off = 0;
+  auto place = [&](size_t bytes) {
+    const size_t at = off;
+    off += up256(bytes);
+    return at;
+  };
+  L.off_info = place((size_t)units * 2 * sizeof(int4));
+  L.off_len = place((size_t)units * sizeof(int32_t));
+  L.off_blocks = place((size_t)units * L.cap * sizeof(int32_t));
+  L.off_member = place((size_t)units * L.unit_tokens * L.words * sizeof(uint32_t));
+  L.off_part_o = place(2 * (size_t)L.grid * L.rows_part * 128 * sizeof(float));
+  L.off_part_ml = place(2 * (size_t)L.grid * L.rows_part * sizeof(float2));
+  L.off_cut = place((size_t)L.grid * sizeof(int2));
+  L.total = off;
+  return L;
+}
+
+bool tree_sizes_ok(int batch, int total_q, int hq, int hkv, int head_dim, int topk) {
+  return batch >= 1 && total_q >= 0 && hq >= 1 && hkv >= 1 && hq % hkv == 0 && hq / hkv <= 128 &&
+         head_dim == 128 && topk >= 1 && topk <= kMaxTopk;
+}
+
 msa_status_t build_tree(
     const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
     const int32_t* q2k_indices, int topk, const int32_t* cu_seqlens_q, const uint32_t* tree_mask,
@@ -657,12 +713,84 @@ msa_status_t build_tree(
     const int32_t* seqused_k, int batch, int total_q, int num_qo_heads, int num_kv_heads,
     int head_dim, int max_seqlen_q, float softmax_scale, void* out, float* lse, void* workspace,
     size_t workspace_bytes, ForwardPlan* plan) {
-  if (page_table == nullptr || tree_mask == nullptr || !aligned(tree_mask, 4)) return MSA_INVALID_ARG;
+  if (batch < 1 || total_q < 0 || num_qo_heads < 1 || num_kv_heads < 1 ||
+      num_qo_heads % num_kv_heads != 0 || max_pages < 1 || num_pages < 1)
+    return MSA_INVALID_ARG;
+  if (total_q > 0 && max_seqlen_q < 1) return MSA_INVALID_ARG;
+  if (q == nullptr || k == nullptr || v == nullptr || q2k_indices == nullptr ||
+      cu_seqlens_q == nullptr || tree_mask == nullptr || page_table == nullptr ||
+      seqused_k == nullptr || out == nullptr)
+    return MSA_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+      !aligned(q2k_indices, 4) || !aligned(cu_seqlens_q, 4) || !aligned(tree_mask, 4) ||
+      !aligned(page_table, 4) || !aligned(seqused_k, 4) || (lse && !aligned(lse, 4)) ||
+      (workspace && !aligned(workspace, 256)))
+    return MSA_INVALID_ARG;
   if (mask_words < 1 || (long long)mask_words * 32 < max_seqlen_q) return MSA_INVALID_ARG;
-  return build_forward(q, q_dtype, k, v, kv_dtype, q2k_indices, topk, cu_seqlens_q, nullptr,
-                       page_table, max_pages, num_pages, seqused_k, batch, total_q, 0, num_qo_heads,
-                       num_kv_heads, head_dim, max_seqlen_q, 0, softmax_scale, out, lse, workspace,
-                       workspace_bytes, plan, tree_mask, mask_words);
+  if (!tree_sizes_ok(batch, total_q, num_qo_heads, num_kv_heads, head_dim, topk) ||
+      max_pages > kTreeMaxPages)
+    return MSA_UNSUPPORTED;
+  if (q_dtype == MSA_FP16 ? kv_dtype != MSA_FP16
+                          : (q_dtype != MSA_BF16 || (kv_dtype != MSA_BF16 && kv_dtype != MSA_FP8_E4M3)))
+    return MSA_UNSUPPORTED;
+  const TreeLayout L = tree_layout(batch, total_q, num_qo_heads, num_kv_heads, topk, max_seqlen_q);
+  if (workspace == nullptr || workspace_bytes < L.total) return MSA_WORKSPACE_TOO_SMALL;
+  plan->empty = total_q == 0;
+  if (plan->empty) return MSA_OK;
+  unsigned* fault = fault_word();
+  if (fault == nullptr) return MSA_CUDA_ERROR;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  plan->tree = true;
+  TreeArgs& a = plan->t;
+  a.fault = fault;
+  const int G = num_qo_heads / num_kv_heads;
+  const bool e4m3 = kv_dtype == MSA_FP8_E4M3;
+  if (!map_rows(&a.tmap_q, q, 2, num_qo_heads, total_q, (uint32_t)G, (uint32_t)L.W) ||
+      (!e4m3 && (!map_pages(&a.tmap_k, k, 2, num_kv_heads, num_pages) ||
+                 !map_pages(&a.tmap_v, v, 2, num_kv_heads, num_pages))))
+    return MSA_CUDA_ERROR;
+  a.k_pool = static_cast<const uint8_t*>(k);
+  a.v_pool = static_cast<const uint8_t*>(v);
+  a.e4m3 = e4m3 ? 1 : 0;
+  a.f16 = q_dtype == MSA_FP16 ? 1 : 0;
+  a.cu_q = cu_seqlens_q;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.seqused_k = seqused_k;
+  a.num_qo_heads = num_qo_heads;
+  a.num_kv_heads = num_kv_heads;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)head_dim);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.tree_mask = tree_mask;
+  a.mask_words = mask_words;
+  a.tile_tokens = L.W;
+  a.unit_tokens = L.unit_tokens;
+  a.max_tiles = L.max_tiles;
+  a.cap = L.cap;
+  a.words = L.words;
+  a.q2k = q2k_indices;
+  a.topk = topk;
+  a.total_q = total_q;
+  a.batch = batch;
+  a.unit_len = reinterpret_cast<int32_t*>(ws + L.off_len);
+  a.unit_info = reinterpret_cast<int4*>(ws + L.off_info);
+  a.union_blocks = reinterpret_cast<int32_t*>(ws + L.off_blocks);
+  a.member = reinterpret_cast<uint32_t*>(ws + L.off_member);
+  // A 16-bit block takes about as long to bring from memory as two tiles'
+  // products do; an E4M3 block is half the bytes.
+  a.dual_weight = e4m3 ? 2 : 1;
+  a.min_range = kTreeMinRange;
+  a.cut_cost = kTreeCutCost * a.dual_weight;
+  a.grid = L.grid;
+  a.rows_part = L.rows_part;
+  a.part_o = reinterpret_cast<float*>(ws + L.off_part_o);
+  a.part_m = reinterpret_cast<float*>(ws + L.off_part_ml);
+  a.part_l = a.part_m + 2 * (size_t)L.grid * L.rows_part;
+  a.cut = reinterpret_cast<int2*>(ws + L.off_cut);
+  a.out = out;
+  a.lse = lse;
+  return MSA_OK;
 }
 
 // The packed-NVFP4 paged route: the E4M3 kernel instance (converter warps),
@@ -779,6 +907,12 @@ msa_status_t launch_forward(const ForwardPlan& p, cudaStream_t stream) {
     mark(2, stream);
     return from_cuda(e);
   }
+  if (p.tree) {
+    mark(1, stream);
+    const cudaError_t e = launch_tree(p.t, stream);
+    mark(2, stream);
+    return from_cuda(e);
+  }
   cudaError_t e = launch_kv_decode(p.dq, stream);
   if (e != cudaSuccess) return MSA_CUDA_ERROR;
   e = launch_page_decode(p.pd, stream);
@@ -787,9 +921,7 @@ msa_status_t launch_forward(const ForwardPlan& p, cudaStream_t stream) {
                    : launch_build_union(p.u, stream);
   if (e != cudaSuccess) return MSA_CUDA_ERROR;
   mark(1, stream);
-  e = p.swapped                      ? launch_prefill_swapped(p.a, stream)
-      : p.a.tree_mask != nullptr ? launch_tree(p.a, stream)
-                                 : launch_prefill(p.a, stream);
+  e = p.swapped ? launch_prefill_swapped(p.a, stream) : launch_prefill(p.a, stream);
   mark(2, stream);
   return from_cuda(e);
 }
@@ -892,6 +1024,13 @@ msa_status_t msa_sparse_attention_nvfp4_prepare(
 }
 
 #undef MSA_FP4_ARGS
+
+size_t msa_tree_attention_workspace_size(int batch, int total_q, int num_qo_heads,
+                                         int num_kv_heads, int head_dim, int topk,
+                                         int max_seqlen_q) {
+  if (!tree_sizes_ok(batch, total_q, num_qo_heads, num_kv_heads, head_dim, topk)) return 0;
+  return tree_layout(batch, total_q, num_qo_heads, num_kv_heads, topk, max_seqlen_q).total;
+}
 
 #define MSA_TREE_ARGS                                                                           \
   q, q_dtype, k, v, kv_dtype, q2k_indices, topk, cu_seqlens_q, tree_mask, mask_words,           \

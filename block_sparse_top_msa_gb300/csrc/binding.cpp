@@ -340,8 +340,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor out = output("out", a[11], dev, q.scalar_type(), q.sizes());
   Tensor lse;
   if (a[12] != Py_None || as_flag(a[10])) lse = output("lse", a[12], dev, at::kFloat, Shape{total, hq});
-  const Tensor ws = workspace(a[13], dev, msa_sparse_attention_workspace_size_kv(batch, total, hq, hkv, 128, topk,
-                                                                                 max_q < 1 ? 1 : max_q, 1, kt, max_pages));
+  const Tensor ws = workspace(a[13], dev, msa_tree_attention_workspace_size(batch, total, hq, hkv, 128, topk, max_q));
   const bool prepare = as_flag(a[15]);
   msa_attention_plan_t* plan = nullptr;
 #define MSA_TREE_CALL                                                                                        \

@@ -129,13 +129,8 @@ struct PrefillArgs {
   // attention kernel waits for it only before its first claim from the
   // counter.
   int wait_late;
-  // Tree attention only (launch_tree): row t's mask_words words say which of
-  // its sequence's query tokens it sees among the last Lq keys.
-  const uint32_t* tree_mask;
-  int mask_words;
 };
 cudaError_t launch_prefill(const PrefillArgs& a, cudaStream_t s);
-cudaError_t launch_tree(const PrefillArgs& a, cudaStream_t s);
 // The swapped-orientation prefill kernel (bf16 / fp16 K/V, G a multiple of 8
 // and at most 64, tile_tokens * G <= 256, tile_tokens <= 32, no splits).
 cudaError_t launch_prefill_swapped(const PrefillArgs& a, cudaStream_t s);
@@ -145,6 +140,49 @@ int device_sm_count();
 cudaError_t set_smem_limit(const void* kernel, int bytes);
 // The current device's per-block shared-memory limit (opt-in), cached.
 int device_smem_optin();
+
+// Attention of drafted trees (tree.cu).
+struct TreeArgs {
+  unsigned* fault;
+  CUtensorMap tmap_q;  // (d, Hq, Tq) 16-bit, box (64, G, tile_tokens)
+  CUtensorMap tmap_k;  // (.., 128, Hkv, pages), 16-bit caches
+  CUtensorMap tmap_v;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  int e4m3, f16;       // the cache's type, else bf16
+  const int32_t* cu_q;
+  const int32_t* page_table;
+  int max_pages, num_pages;
+  const int32_t* seqused_k;
+  int num_qo_heads, num_kv_heads;
+  float scale_log2;
+  const uint32_t* tree_mask;  // (Tq, mask_words)
+  int mask_words;
+  int tile_tokens, unit_tokens;  // per MMA tile; per unit, at most two tiles
+  int max_tiles;                 // bound on the groups of unit_tokens tokens
+  const int32_t* q2k;            // (Hkv, Tq, topk)
+  int topk, total_q, batch;
+  int cap, words;                // unit_tokens * topk, and its bits in words
+  // Per unit (tile * Hkv + h), written by the union kernel: weighted union
+  // length; (t0, sequence, tokens, union length), t0 = -1 past the last tile,
+  // and (Lq, Lk, 0, 0); the union (cap); each token's membership (words).
+  int32_t* unit_len;
+  int4* unit_info;
+  int32_t* union_blocks;
+  uint32_t* member;
+  int dual_weight;  // of a block of a unit with two tiles
+  int min_range;    // least weighted length of a CTA's range, at least dual_weight
+  int cut_cost;     // what ranges cut out of units cost, in weighted blocks of a CTA's time
+  int grid, rows_part;
+  float* part_o;    // (2 * grid, 128, rows_part): unnormalised O of a range's first and last segment
+  float* part_m;    // (2 * grid, rows_part)
+  float* part_l;
+  int2* cut;        // (grid): the unit that begins in the CTA's range and goes on after it, and the
+                    // one that began before it (of the CTA's first segment); -1: none
+  void* out;
+  float* lse;
+};
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
 
 struct ProxyArgs {
   unsigned* fault;      // device fault word (bounded-wait expiry, capacity)

@@ -240,14 +240,19 @@ msa_status_t msa_sparse_attention_nvfp4_prepare(
  *   tree_mask   device uint32 (Tq, mask_words)
  *   mask_words  words per row, at least max_seqlen_q / 32 rounded up; tokens
  *               past 32 * mask_words are not seen
+ *   workspace   msa_tree_attention_workspace_size(...) bytes, 256-byte aligned,
+ *               uninitialised; calls that share one must be ordered on the device
  * K and V of the keys below seqused_k have to be finite; what the pages hold
  * past them does not matter. A NULL or misaligned tree_mask, a NULL
- * page_table or too few words: MSA_INVALID_ARG; otherwise as the forward.
+ * page_table or too few words: MSA_INVALID_ARG; max_pages above 2^18:
+ * MSA_UNSUPPORTED; otherwise as the forward.
  * msa_tree_attention_prepare binds the call into a plan that
- * msa_sparse_attention_run launches. Workspace:
- * msa_sparse_attention_workspace_size (or _kv) with paged = 1. Rows at or past
- * cu_seqlens_q[B] are left as they were.
+ * msa_sparse_attention_run launches. Rows at or past cu_seqlens_q[B] are left
+ * as they were.
  */
+size_t msa_tree_attention_workspace_size(int batch, int total_q, int num_qo_heads,
+                                         int num_kv_heads, int head_dim, int topk,
+                                         int max_seqlen_q);
 msa_status_t msa_tree_attention(
     const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
     const int32_t* q2k_indices, int topk, const int32_t* cu_seqlens_q, const uint32_t* tree_mask,
