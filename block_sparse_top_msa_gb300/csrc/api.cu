@@ -660,10 +660,10 @@ struct TreeLayout {
 // of a bitmap and its ranks).
 constexpr int kTreeMaxTokens = 128;
 constexpr int kTreeMaxPages = 1 << 18;
-// Fewest blocks a CTA takes.
-constexpr int kTreeMinRange = 2;
-// Blocks' time that partials and their joining take.
-constexpr int kTreeCutCost = 6;
+// In quarters of a block of two tiles (the kernel's weights: 4, and 3 with one
+// tile): the least a CTA takes, and what partials and their joining cost it.
+constexpr int kTreeMinRange = 8;
+constexpr int kTreeCutCost = 24;
 
 TreeLayout tree_layout(int batch, int total_q, int hq, int hkv, int topk, int max_seqlen_q) {
   TreeLayout L{};
@@ -682,7 +682,7 @@ TreeLayout tree_layout(int batch, int total_q, int hq, int hkv, int topk, int ma
   L.words = (L.cap + 31) / 32;
   L.rows_part = L.unit_tokens * G;
   const long long units = (long long)hkv * L.max_tiles;
-  const long long most = (units * L.cap * 2 + kTreeMinRange - 1) / kTreeMinRange;
+  const long long most = (units * L.cap * 4 + kTreeMinRange - 1) / kTreeMinRange;
   L.grid = most < kPlanSMs ? (int)(most < 1 ? 1 : most) : kPlanSMs;
   size_t off = 0;
   auto place = [&](size_t bytes) {
@@ -777,11 +777,8 @@ msa_status_t build_tree(
   a.unit_info = reinterpret_cast<int4*>(ws + L.off_info);
   a.union_blocks = reinterpret_cast<int32_t*>(ws + L.off_blocks);
   a.member = reinterpret_cast<uint32_t*>(ws + L.off_member);
-  // A 16-bit block takes about as long to bring from memory as two tiles'
-  // products do; an E4M3 block is half the bytes.
-  a.dual_weight = e4m3 ? 2 : 1;
   a.min_range = kTreeMinRange;
-  a.cut_cost = kTreeCutCost * a.dual_weight;
+  a.cut_cost = kTreeCutCost;
   a.grid = L.grid;
   a.rows_part = L.rows_part;
   a.part_o = reinterpret_cast<float*>(ws + L.off_part_o);

@@ -170,8 +170,7 @@ struct TreeArgs {
   int4* unit_info;
   int32_t* union_blocks;
   uint32_t* member;
-  int dual_weight;  // of a block of a unit with two tiles
-  int min_range;    // least weighted length of a CTA's range, at least dual_weight
+  int min_range;    // least weighted length of a CTA's range, at least a block's
   int cut_cost;     // what ranges cut out of units cost, in weighted blocks of a CTA's time
   int grid, rows_part;
   float* part_o;    // (2 * grid, 128, rows_part): unnormalised O of a range's first and last segment

@@ -97,9 +97,9 @@ struct __align__(1024) Smem {
   uint64_t q_full, q_empty;
   uint64_t k_full[kKSlots], k_empty[kKSlots];
   uint64_t v_full[kVSlots], v_empty[kVSlots];
-  uint64_t qk_done[2];             // per stream: S readable (and the PV before complete)
-  uint64_t p_full[2][2];           // per stream and 64-key half: P written
-  uint64_t pva_done[2];            // per stream: the first half's PV complete
+  uint64_t qk_done[2][2];          // per stream and 64-key half of a block: S readable
+  uint64_t p_full[2][2];           // P written
+  uint64_t pv_done[2];             // per stream: a half's PV complete
   uint64_t o_done[2], o_free[2];   // per stream: O complete at a segment's end, O read out
   uint64_t ml_full, ml_empty, drain;
   uint64_t q_ready;                // E4M3: Q converted
@@ -151,9 +151,13 @@ MSA_DEV int first_block(long long p0, long long c, int w, int len) {
   return (int)(j < len ? j : len);
 }
 
-// A block of a unit with two tiles weighs more where the products bound the
-// kernel.
-MSA_DEV int unit_weight(const TreeArgs& a, int tokens) { return tokens > a.tile_tokens ? a.dual_weight : 1; }
+// What a block costs a CTA, by the unit's tiles: bringing and decoding it is
+// the same, but two tiles multiply twice (4500 clocks against 3300 with E4M3,
+// about as much apart with 16-bit caches).
+constexpr int kOneTileWeight = 3, kTwoTileWeight = 4;
+MSA_DEV int unit_weight(const TreeArgs& a, int tokens) {
+  return tokens > a.tile_tokens ? kTwoTileWeight : kOneTileWeight;
+}
 
 // Which of block columns 32 * k .. 32 * k + 31 a token of a tree sees, as bits.
 // base: the block's first column as a node number (negative before the
@@ -429,10 +433,11 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       mbar_init(&sm.v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&sm.qk_done[s], 1);
-      mbar_init(&sm.p_full[s][0], 4);
-      mbar_init(&sm.p_full[s][1], 4);
-      mbar_init(&sm.pva_done[s], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sm.qk_done[s][h], 1);
+        mbar_init(&sm.p_full[s][h], 4);
+      }
+      mbar_init(&sm.pv_done[s], 1);
       mbar_init(&sm.o_done[s], 1);
       mbar_init(&sm.o_free[s], 4);
     }
@@ -597,7 +602,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           }
           s.h = s.unit % a.num_kv_heads;
           s.dual = s.nw > W;
-          const int w = s.dual ? a.dual_weight : 1;
+          const int w = unit_weight(a, s.nw);
           bool mine_too;
           if (ulen == 0) {
             mine_too = holds(p0);
@@ -644,7 +649,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     // 100 clocks on each MMA, which takes 73.)
     const uint32_t el = elect_one();
     const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
-    constexpr uint32_t idS = idesc_16bit_f32(128, 128, false, false, kF16Ops);
+    constexpr uint32_t idS = idesc_16bit_f32(128, 64, false, false, kF16Ops);
     constexpr uint32_t idO = idesc_16bit_f32(128, 128, false, true, kF16Ops);
     constexpr uint32_t kTile16 = (2 * kHalf) >> 4, kHalf16 = kHalf >> 4;
     // Descriptors differ in the start address, in their low words.
@@ -661,35 +666,24 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       ok = ok && wait_on(bar, phase, fault, code, abort);
     };
     auto commit = [&](uint64_t* bar) { commit_if(el, bar); };
-    // S of stream st = tile `tile` of Q times K.
-    auto qk = [&](int st, int tile) {
-      wait(&sm.k_full[rk.idx], rk.phase, kFaultWaitTma);
-      if (!ok) return;
-      tc_fence_after();
-      const uint32_t q = q0 + tile * kTile16, k = k0 + rk.idx * kTile16, d = tb + kColS + st * 128;
+    // S of stream st = tile `tile` of Q times K, for the block's 64-key half h.
+    auto qk = [&](int st, int h, int tile) {
+      const uint32_t q = q0 + tile * kTile16, k = k0 + rk.idx * kTile16 + h * 512;
+      const uint32_t d = tb + kColS + st * 128 + h * 64;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const uint32_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
         mma_ss_if(el, d, q + off, k + off, hi, idS, kk > 0);
       }
-      commit(&sm.qk_done[st]);
+      commit(&sm.qk_done[st][h]);
     };
-    // O of stream st = (+=) P V, the block's 64-key half h as soon as its P is
-    // there: the softmax of the other half runs meanwhile.
-    auto pv_half = [&](int st, int h, bool first) {
-      wait(&sm.p_full[st][h], (p_phase >> st) & 1u, kFaultWaitSoftmax);
-      if (h == 0) {
-        if (first && nseg > 0) wait(&sm.o_free[st], (nseg - 1) & 1, kFaultWaitSoftmax);
-        wait(&sm.v_full[rv.idx], rv.phase, kFaultWaitTma);
-      }
-      if (!ok) return;
-      tc_fence_after();
+    // O of stream st = (+=) P V for half h.
+    auto pv = [&](int st, int h, bool first) {
       const uint32_t v = v0 + rv.idx * kTile16 + h * 512;
       const uint32_t tp = tb + kColS + st * 128 + h * 64, d = tb + kColO + st * 128;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) mma_ts_if(el, d, tp + kk * 8, v + kk * 128, hi, idO, kk > 0 || h > 0 || !first);
-      if (h == 0) commit(&sm.pva_done[st]);
-      else p_phase ^= 1u << st;
+      commit(&sm.pv_done[st]);
     };
     Segment s;
     for (int ni = 0; ok; ++ni) {
@@ -703,42 +697,57 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       if (FP8) wait(&sm.q_ready, nseg & 1, kFaultWaitSoftmax);
       else wait(&sm.q_full, nseg & 1, kFaultWaitTma);
       // Two tiles: both streams take every block, K and V going with stream 1.
-      // One tile: block j is stream j & 1's, and S runs two blocks ahead.
+      // One tile: block j is stream j & 1's. Either way the products go by
+      // halves of a block's keys: as soon as a half's P has been consumed, the
+      // S of the same half of the stream's next block takes its place, under
+      // the softmax of the other half. (By whole blocks a stream's softmax and
+      // products ran one after the other, 3700 clocks a block of two tiles
+      // where the products take 2350.)
       const int ahead = dual ? 1 : 2;
-      // The first S of each stream (step -1), then for each block its PV and
-      // the S of the stream's next block; the code is here once, as the
-      // instruction cache is shared with the other roles.
+      auto k_used = [&](int b) {
+        commit(&sm.k_empty[rk.idx]);
+        rk.next();
+        if (b == n - 1) commit(&sm.q_empty);  // the segment's last
+      };
 #pragma unroll 1
-      for (int t = -1; ok && t < n; ++t) {
-        const int i_end = (dual || t < 0) ? 2 : 1;
+      for (int x = 0; ok && x < 4; ++x) {  // the first S of each stream
+        const int st = x >> 1, h = x & 1, b = dual ? 0 : st;
+        if (b >= n) break;
+        if (h == 0) wait(&sm.k_full[rk.idx], rk.phase, kFaultWaitTma);
+        if (!ok) break;
+        tc_fence_after();
+        qk(st, h, dual ? st : 0);
+        if (h == 1 && (!dual || st == 1)) k_used(b);
+      }
 #pragma unroll 1
-        for (int h = t < 0 ? 1 : 0; h < 2; ++h) {
+      for (int t = 0; ok && t < n; ++t) {
+        const int b = t + ahead;  // the stream's next block
+        if (t < ahead && nseg > 0) {
+          // O has been read: of both streams, every phase of each.
+          if (dual || t == 0) wait(&sm.o_free[0], (nseg - 1) & 1, kFaultWaitSoftmax);
+          if (dual || t == 1 || n == 1) wait(&sm.o_free[1], (nseg - 1) & 1, kFaultWaitSoftmax);
+        }
+        wait(&sm.v_full[rv.idx], rv.phase, kFaultWaitTma);
+        if (b < n) wait(&sm.k_full[rk.idx], rk.phase, kFaultWaitTma);
+        const int x_end = dual ? 4 : 2;
 #pragma unroll 1
-          for (int i = 0; i < i_end; ++i) {
-            const int st = (dual || t < 0) ? i : t & 1;
-            if (t >= 0) {
-              pv_half(st, h, t < ahead);
-              if (h == 0) continue;
-              if (!dual || st == 1) {
-                commit(&sm.v_empty[rv.idx]);
-                rv.next();
-              }
-              if (t + ahead >= n) commit(&sm.o_done[st]);
-            }
-            // The block whose S comes next in this stream.
-            const int b = t < 0 ? (dual ? 0 : i) : t + ahead;
-            if (b >= n) continue;
-            qk(st, dual ? st : 0);
-            if (!dual || st == 1) {
-              commit(&sm.k_empty[rk.idx]);
-              rk.next();
-              if (b == n - 1) commit(&sm.q_empty);  // the segment's last
-            }
+        for (int x = 0; ok && x < x_end; ++x) {
+          const int st = dual ? x & 1 : t & 1, h = dual ? x >> 1 : x;
+          wait(&sm.p_full[st][h], (p_phase >> st) & 1u, kFaultWaitSoftmax);
+          if (!ok) break;
+          tc_fence_after();
+          pv(st, h, t < ahead);
+          if (b < n) qk(st, h, dual ? st : 0);
+          if (h == 1) {
+            p_phase ^= 1u << st;
+            if (b >= n) commit(&sm.o_done[st]);
           }
         }
+        if (!ok) break;
+        commit(&sm.v_empty[rv.idx]);
+        rv.next();
+        if (b < n) k_used(b);
       }
-      // Every phase of o_free is waited for, a stream without blocks' too.
-      if (!dual && n == 1 && nseg > 0) wait(&sm.o_free[1], (nseg - 1) & 1, kFaultWaitSoftmax);
       ++nseg;
     }
     commit(&sm.drain);
@@ -1038,11 +1047,6 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           // Rows that see nothing here are masked too where columns may hold anything.
           hides = all != ~0u && (mem || tail < 128);
         }
-        ok = wait_on(&sm.qk_done[st], nqk & 1, fault, kFaultWaitMma, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        ++nqk;
-        tc_fence_after();
         const bool warp_mem = __any_sync(0xffffffffu, mem);
         const bool warp_hides = __any_sync(0xffffffffu, hides);
         if (!FP8 && tail < 128 && (st == 0 || !s.dual)) {
@@ -1061,6 +1065,10 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         for (int half = 0; half < 2; ++half) {
           const uint32_t vis0 = half == 0 ? vis[0] : vis[2], vis1 = half == 0 ? vis[1] : vis[3];
           const uint32_t hcol = scol + half * 64;  // P over the first half of its own S
+          ok = wait_on(&sm.qk_done[st][half], nqk & 1, fault, kFaultWaitMma, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          tc_fence_after();
           if (warp_mem) {
             if (warp_hides) {
               // Few blocks: eight columns at a time, written back to S.
@@ -1089,15 +1097,13 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
             bool rescale = false;
             update_max(on, mx, scale, m_ref, l, alpha, rescale);
             if (__any_sync(0xffffffffu, rescale)) {
-              // Before the first half O holds every block up to here (the S
-              // was committed after the PV before it); before the second, the
-              // first half's PV has to end.
-              if (half == 1) {
-                ok = wait_on(&sm.pva_done[st], (nqk - 1) & 1, fault, kFaultWaitMma, abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_fence_after();
-              }
+              // O has to hold the half before (the second halves' PVs complete
+              // odd phases of pv_done, the first halves' even ones); the half
+              // before that is complete, as this S was issued after it.
+              ok = wait_on(&sm.pv_done[st], half ^ 1, fault, kFaultWaitMma, abort);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
 #pragma unroll 1
               for (int q = 0; q < 4; ++q) {
                 const uint32_t ocol = lanes + kColO + st * 128 + q * 32;
@@ -1139,6 +1145,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           if (lane == 0) mbar_arrive(&sm.p_full[st][half]);
         }
         if (!ok) break;
+        ++nqk;
       }
       if (!ok) break;
       g0 += n;
