@@ -7,13 +7,22 @@
 // b s, b c + a s). The backward with dy: u = R^T dy, dw = sum over tokens and
 // heads of u x r, and with g = u w, dx = r (g - x r^2 mean(g x)).
 //
-// A team of 16 lanes holds a row in registers, eight elements a lane in two
-// groups of four, placed so that both elements of a pair are the lane's own:
-// with paired halves lane l of the rotary / 8 turned lanes takes elements 4l..
-// and rotary / 2 + 4l.., otherwise (adjacent pairs, or elements past the
-// rotary ones) 8l.. and 8l + 4... Either way a turned lane's cosines are
+// A team of 16 lanes holds a row in registers, eight elements a lane: the first
+// and second elements A[0..3], B[0..3] of four pairs. With paired halves lane
+// l of the rotary / 8 turned lanes takes elements 4l.. as A and rotary / 2 +
+// 4l.. as B; with adjacent pairs 8l, 8l + 2, .. and 8l + 1, 8l + 3, ..; lanes
+// past the rotary elements take 8l.. and 8l + 4... A turned lane's cosines are
 // entries 4l..4l+3 of the position's table row, and only the sums over a row
-// cross lanes.
+// cross lanes. The weight is taken into the cosines and sines once for the
+// heads of a token that a team turns: y = r (A wc - B ws', B wc' + A ws).
+//
+// The kernels are bound by memory, if the arithmetic is kept down (one
+// operation at a time instead of pairs: 17 instructions an element, 58% of the
+// issue slots, 221 us and 313 us) and loads are not held up: forward 65536
+// tokens of 32 + 4 heads (1.24 GB in and out) take 199 us, 92% of the measured
+// copy bandwidth; backward 32768 of 64 + 8 (1.82 GB) 291 us, 92%. 16-byte
+// accesses by 8 lanes a row were slower (225, 307), as were loads one unit
+// ahead in the backward (350: its registers).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -26,79 +35,127 @@ namespace {
 constexpr int kTeam = 16;             // lanes per row
 constexpr int kThreads = 256;
 constexpr int kTeams = kThreads / kTeam;
+constexpr int kBwdResident = 2;  // backward blocks an SM holds
 
-struct Row {
-  float e[8];
+// A lane's eight elements: A and B of pairs 0, 1 and of pairs 2, 3.
+struct Own {
+  float2 a0, a1, b0, b1;
 };
 
+MSA_DEV float2 mul2(float2 x, float2 y) { return __fmul2_rn(x, y); }
+MSA_DEV float2 fma2(float2 x, float2 y, float2 z) { return __ffma2_rn(x, y, z); }
+MSA_DEV float2 neg2(float2 x) { return make_float2(-x.x, -x.y); }
+MSA_DEV float2 both(float x) { return make_float2(x, x); }
+
 template <bool F16>
-MSA_DEV void unpack4(uint2 w, float* e) {
-  if (F16) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
-    e[0] = a.x, e[1] = a.y, e[2] = b.x, e[3] = b.y;
+MSA_DEV float2 unpack2(uint32_t w) {
+  if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+// Two groups of four elements as they lie in memory, to and from pairs.
+template <bool F16, bool ADJ>
+MSA_DEV Own unpack(uint2 lo, uint2 hi, bool adj) {
+  const float2 x0 = unpack2<F16>(lo.x), x1 = unpack2<F16>(lo.y), x2 = unpack2<F16>(hi.x), x3 = unpack2<F16>(hi.y);
+  if (ADJ && adj)
+    return {make_float2(x0.x, x1.x), make_float2(x2.x, x3.x), make_float2(x0.y, x1.y), make_float2(x2.y, x3.y)};
+  return {x0, x1, x2, x3};
+}
+template <bool ADJ>
+MSA_DEV void groups(const Own& y, bool adj, float2 (&g)[4]) {
+  if (ADJ && adj) {
+    g[0] = make_float2(y.a0.x, y.b0.x), g[1] = make_float2(y.a0.y, y.b0.y);
+    g[2] = make_float2(y.a1.x, y.b1.x), g[3] = make_float2(y.a1.y, y.b1.y);
   } else {
-    e[0] = __uint_as_float(w.x << 16), e[1] = __uint_as_float(w.x & 0xffff0000u);
-    e[2] = __uint_as_float(w.y << 16), e[3] = __uint_as_float(w.y & 0xffff0000u);
+    g[0] = y.a0, g[1] = y.a1, g[2] = y.b0, g[3] = y.b1;
   }
 }
 template <bool F16>
-MSA_DEV uint2 pack4(const float* e) {
-  return make_uint2(pack_x2<F16>(e[0], e[1]), pack_x2<F16>(e[2], e[3]));
+MSA_DEV uint2 pack4(float2 x, float2 y) {
+  return make_uint2(pack_x2<F16>(x.x, x.y), pack_x2<F16>(y.x, y.y));
 }
 // Four values as E4M3 codes, round to nearest even, magnitudes above 448 as
 // 448 (NaN stays NaN).
-MSA_DEV uint32_t pack4_e4m3(const float* e) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(e[0], e[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(e[2], e[3]), __NV_SATFINITE, __NV_E4M3);
+MSA_DEV uint32_t pack4_e4m3(float2 x, float2 y) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
   return lo | (hi << 16);
 }
 
 MSA_DEV float team_sum(float v) {
 #pragma unroll
-  for (int s = 8; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
+  for (int s = kTeam / 2; s > 0; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
   return v;
 }
-
-// Where a lane's two groups of four elements lie, and whether they turn.
-struct Place {
-  int o0, o1;
-  bool turned;
-};
-MSA_DEV Place place_of(int l, int rotary, int interleaved) {
-  const bool turned = 8 * l < rotary;
-  if (turned && !interleaved) return {4 * l, rotary / 2 + 4 * l, true};
-  return {8 * l, 8 * l + 4, turned};
+MSA_DEV float dot_of(const Own& x, const Own& y) {
+  const float2 s = fma2(x.a0, y.a0, fma2(x.a1, y.a1, fma2(x.b0, y.b0, mul2(x.b1, y.b1))));
+  return s.x + s.y;
+}
+MSA_DEV Own scaled(const Own& x, float f) {
+  const float2 g = both(f);
+  return {mul2(x.a0, g), mul2(x.a1, g), mul2(x.b0, g), mul2(x.b1, g)};
+}
+MSA_DEV Own product(const Own& x, const Own& y) {
+  return {mul2(x.a0, y.a0), mul2(x.a1, y.a1), mul2(x.b0, y.b0), mul2(x.b1, y.b1)};
 }
 
-// Turns the lane's four pairs by (c, s).
-MSA_DEV void turn(Row& y, float4 c, float4 s, int interleaved) {
-  const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-  auto pair = [&](int ia, int ib, int j) {
-    const float p = y.e[ia], q = y.e[ib];
-    y.e[ia] = p * cc[j] - q * ss[j];
-    y.e[ib] = q * cc[j] + p * ss[j];
-  };
-  if (interleaved) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) pair(2 * j, 2 * j + 1, j);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) pair(j, j + 4, j);
-  }
+// Where a lane's two groups of four elements lie, whether they turn, and
+// whether their pairs are adjacent.
+struct Place {
+  int o0, o1;
+  bool turned, adj;
+};
+template <bool ADJ>
+MSA_DEV Place place_of(int l, int rotary) {
+  const bool turned = 8 * l < rotary;
+  if (turned && !ADJ) return {4 * l, rotary / 2 + 4 * l, true, false};
+  return {8 * l, 8 * l + 4, turned, ADJ};
+}
+// The weight's elements, in pairs.
+template <bool ADJ>
+MSA_DEV Own weight_of(const float* w, const Place& at) {
+  const float4 x = __ldg(reinterpret_cast<const float4*>(w + at.o0));
+  const float4 y = __ldg(reinterpret_cast<const float4*>(w + at.o1));
+  if (ADJ && at.adj)
+    return {make_float2(x.x, x.z), make_float2(y.x, y.z), make_float2(x.y, x.w), make_float2(y.y, y.w)};
+  return {make_float2(x.x, x.y), make_float2(x.z, x.w), make_float2(y.x, y.y), make_float2(y.z, y.w)};
+}
+// Cosines and sines of the lane's four pairs.
+struct Angles {
+  float2 c0, c1, s0, s1;
+};
+template <class Args>
+MSA_DEV Angles angles_of(const Args& a, int l, int pos, bool turned) {
+  if (!turned) return {both(1.f), both(1.f), both(0.f), both(0.f)};
+  const float* row = a.cos_sin + (size_t)pos * a.rotary + 4 * l;
+  const float4 c = __ldg(reinterpret_cast<const float4*>(row));
+  const float4 s = __ldg(reinterpret_cast<const float4*>(row + a.rotary / 2));
+  return {make_float2(c.x, c.y), make_float2(c.z, c.w), make_float2(s.x, s.y), make_float2(s.z, s.w)};
 }
 
 // Cache row of token t (right-aligned in its sequence): its page, row within
 // the page, or page -1 where it has none. Tokens at or past cu_q[batch]
-// belong to no sequence.
-MSA_DEV int cache_page(const RopeArgs& a, int t, int& row) {
-  int lo = 0, hi = a.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(a.cu_q + mid) <= t) lo = mid; else hi = mid - 1;
+// belong to no sequence. The team's lanes probe together: first the place
+// that equal lengths would give, then kTeam places a step.
+MSA_DEV int cache_page(const RopeArgs& a, int l, int t, bool live, int& row) {
+  const unsigned lane0 = (threadIdx.x & 31) & ~(kTeam - 1);
+  const unsigned mask = ((1u << kTeam) - 1u) << lane0;
+  int lo = min(a.batch - 1, (int)((long long)t * a.batch / a.tokens));
+  int begin = __ldg(a.cu_q + lo), end = __ldg(a.cu_q + lo + 1);
+  if (!(begin <= t && t < end)) {
+    // The last lo with cu_q[lo] <= t (0 where there is none).
+    int hi = a.batch;
+    lo = 0;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + kTeam) / (kTeam + 1);
+      const int at = lo + (l + 1) * step;
+      const bool below = at < hi && __ldg(a.cu_q + min(at, a.batch)) <= t;
+      const int n = __popc(__ballot_sync(mask, below) & mask);
+      lo += n * step;
+      hi = min(hi, lo + step);
+    }
+    begin = __ldg(a.cu_q + lo), end = __ldg(a.cu_q + lo + 1);
   }
-  const int end = __ldg(a.cu_q + lo + 1);
-  if (t < __ldg(a.cu_q + lo) || t >= end) return -1;
+  if (!live || t < begin || t >= end) return -1;
   const long long pos = (long long)__ldg(a.seqused_k + lo) - end + t;
   if (pos < 0 || pos >= (long long)a.max_pages * kBlk) return -1;
   row = (int)(pos % kBlk);
@@ -109,24 +166,34 @@ MSA_DEV int cache_page(const RopeArgs& a, int t, int& row) {
 // KV: 0 K to a dense output, 1 K and V to 16-bit pools, 2 to E4M3 pools.
 // A team takes up to R heads of one token, all of Q, of K or of V, with every
 // row's loads issued before the first is used.
-template <bool F16, int KV, int R>
+template <bool F16, bool ADJ, int KV, int R>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
   const int l = threadIdx.x % kTeam;
-  const int cq = (a.hq + R - 1) / R, ck = (a.hkv + R - 1) / R;
-  const int per_token = cq + (KV ? 2 : 1) * ck;
+  const unsigned cq = (a.hq + R - 1) / R, ck = (a.hkv + R - 1) / R;
   const unsigned id = blockIdx.x * kTeams + threadIdx.x / kTeam;
-  const unsigned t_u = id / (unsigned)per_token;
+  unsigned t_u, c;  // the token, and the team within it: Q's, then K's and V's
+  if (KV) {
+    // All tokens' K and V first: where they go takes several loads one after
+    // the other to find, which then is under the work on Q.
+    const unsigned kv = a.tokens * 2u * ck;
+    const bool q = id >= kv;
+    const unsigned per = q ? cq : 2u * ck, rest = q ? id - kv : id;
+    t_u = rest / per;
+    c = rest - t_u * per + (q ? 0u : cq);
+  } else {
+    t_u = id / (cq + ck);
+    c = id - t_u * (cq + ck);
+  }
   const bool live = t_u < (unsigned)a.tokens;
   const int t = live ? (int)t_u : 0;
-  const int c = live ? (int)(id - t_u * per_token) : 0;
-  const int side = c < cq ? 0 : c < cq + ck ? 1 : 2;
-  const int h0 = (side == 0 ? c : side == 1 ? c - cq : c - cq - ck) * R;
+  const int side = !live || c < cq ? 0 : c < cq + ck ? 1 : 2;
+  const int h0 = (int)(side == 0 ? (live ? c : 0u) : side == 1 ? c - cq : c - cq - ck) * R;
   const int n = live ? min(R, (side == 0 ? a.hq : a.hkv) - h0) : 0;
   const uint16_t* src = static_cast<const uint16_t*>(side == 0 ? a.q : side == 1 ? a.k : a.v) +
                         (long long)t * (side == 0 ? a.q_stride : side == 1 ? a.k_stride : a.v_stride) +
                         h0 * kHeadDim;
-  Place at = place_of(l, a.rotary, a.interleaved);
-  if (side == 2) at = {8 * l, 8 * l + 4, false};
+  Place at = place_of<ADJ>(l, a.rotary);
+  if (KV && side == 2) at = {8 * l, 8 * l + 4, false, ADJ};
   uint2 raw[R][2];
 #pragma unroll
   for (int i = 0; i < R; ++i) {
@@ -139,19 +206,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   }
   const int pos = __ldg(a.positions + t);
   const bool known = pos >= 0 && pos < a.max_position;
-  float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (at.turned && known) {
-    const float* tab = a.cos_sin + (size_t)pos * a.rotary + 4 * l;
-    cs = __ldg(reinterpret_cast<const float4*>(tab));
-    sn = __ldg(reinterpret_cast<const float4*>(tab + a.rotary / 2));
-  }
-  float w[8];
+  const Angles g = angles_of(a, l, pos, at.turned && known);
+  // The weight times cosines, and times sines (of the other element's term).
+  Own wc, ws;
   if (side < 2) {
-    const float* wp = side == 0 ? a.wq : a.wk;
-    const float4 w0 = __ldg(reinterpret_cast<const float4*>(wp + at.o0));
-    const float4 w1 = __ldg(reinterpret_cast<const float4*>(wp + at.o1));
-    w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w;
-    w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
+    const Own w = weight_of<ADJ>(side == 0 ? a.wq : a.wk, at);
+    wc = {mul2(w.a0, g.c0), mul2(w.a1, g.c1), mul2(w.b0, g.c0), mul2(w.b1, g.c1)};
+    ws = {mul2(w.a0, g.s0), mul2(w.a1, g.s1), neg2(mul2(w.b0, g.s0)), neg2(mul2(w.b1, g.s1))};
   }
   // Destination: a dense row, or the cache row's address for head 0.
   int page = 0, crow = 0;
@@ -160,46 +221,43 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     if (side == 0) {
       write = live && t < __ldg(a.cu_q + a.batch);
     } else {
-      page = live && known ? cache_page(a, t, crow) : -1;
+      page = cache_page(a, l, t, live && known, crow);
       write = page >= 0;
     }
   }
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    Row y;
-    unpack4<F16>(raw[i][0], y.e);
-    unpack4<F16>(raw[i][1], y.e + 4);
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(y.e[j], y.e[j], ss);
-    ss = team_sum(ss);
-    if (side < 2) {
-      const float r = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y.e[j] = y.e[j] * r * w[j];
-      if (at.turned) turn(y, cs, sn, a.interleaved);
-      if (!known) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y.e[j] = 0.f;
+    const Own x = unpack<F16, ADJ>(raw[i][0], raw[i][1], at.adj);
+    const float r = rsqrtf(team_sum(dot_of(x, x)) * (1.f / kHeadDim) + a.eps);
+    Own y = x;
+    if (!KV || side < 2) {
+      if (at.turned) {
+        y = scaled({fma2(x.a0, wc.a0, mul2(x.b0, ws.b0)), fma2(x.a1, wc.a1, mul2(x.b1, ws.b1)),
+                    fma2(x.b0, wc.b0, mul2(x.a0, ws.a0)), fma2(x.b1, wc.b1, mul2(x.a1, ws.a1))}, r);
+      } else {
+        y = scaled(product(x, wc), r);
       }
     }
     if (i >= n || !write) continue;
+    float2 e[4];
+    groups<ADJ>(y, at.adj, e);
+    if (side < 2 && !known) e[0] = e[1] = e[2] = e[3] = both(0.f);
     if (side == 0 || KV == 0) {
       uint16_t* dst = static_cast<uint16_t*>(side == 0 ? a.q_out : a.k_out) +
                       ((size_t)t * (side == 0 ? a.hq : a.hkv) + h0 + i) * kHeadDim;
-      *reinterpret_cast<uint2*>(dst + at.o0) = pack4<F16>(y.e);
-      *reinterpret_cast<uint2*>(dst + at.o1) = pack4<F16>(y.e + 4);
+      __stcs(reinterpret_cast<uint2*>(dst + at.o0), pack4<F16>(e[0], e[1]));
+      __stcs(reinterpret_cast<uint2*>(dst + at.o1), pack4<F16>(e[2], e[3]));
     } else {
       const size_t row = ((size_t)page * a.hkv + h0 + i) * kBlk + crow;
       void* pool = side == 1 ? a.k_pool : a.v_pool;
       if (KV == 2) {
         uint8_t* dst = static_cast<uint8_t*>(pool) + row * kHeadDim;
-        *reinterpret_cast<uint32_t*>(dst + at.o0) = pack4_e4m3(y.e);
-        *reinterpret_cast<uint32_t*>(dst + at.o1) = pack4_e4m3(y.e + 4);
+        *reinterpret_cast<uint32_t*>(dst + at.o0) = pack4_e4m3(e[0], e[1]);
+        *reinterpret_cast<uint32_t*>(dst + at.o1) = pack4_e4m3(e[2], e[3]);
       } else {
         uint16_t* dst = static_cast<uint16_t*>(pool) + row * kHeadDim;
-        *reinterpret_cast<uint2*>(dst + at.o0) = side == 2 ? raw[i][0] : pack4<F16>(y.e);
-        *reinterpret_cast<uint2*>(dst + at.o1) = side == 2 ? raw[i][1] : pack4<F16>(y.e + 4);
+        *reinterpret_cast<uint2*>(dst + at.o0) = side == 2 ? raw[i][0] : pack4<F16>(e[0], e[1]);
+        *reinterpret_cast<uint2*>(dst + at.o1) = side == 2 ? raw[i][1] : pack4<F16>(e[2], e[3]);
       }
     }
   }
@@ -209,37 +267,29 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 // thread's eight weight sums belong to one weight. Units are R heads of one
 // token; a block strides over its side's units and leaves one row of 128
 // partial sums, summed over its teams in a fixed order.
-template <bool F16, int R>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a) {
+template <bool F16, bool ADJ, int R>
+__global__ void __launch_bounds__(kThreads, kBwdResident) rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a) {
   const int l = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
   const bool kside = (int)blockIdx.x >= a.q_blocks;
   const int heads = kside ? a.hkv : a.hq;
-  const int chunks = (heads + R - 1) / R;
-  const long long units = (long long)a.tokens * chunks;
-  const int blk = kside ? (int)blockIdx.x - a.q_blocks : (int)blockIdx.x;
-  const int blocks = kside ? (int)gridDim.x - a.q_blocks : a.q_blocks;
+  const unsigned chunks = (heads + R - 1) / R;
+  const unsigned units = (unsigned)a.tokens * chunks;  // below 2^31, as tokens * heads are
+  const unsigned blk = kside ? blockIdx.x - a.q_blocks : blockIdx.x;
+  const unsigned blocks = kside ? gridDim.x - a.q_blocks : a.q_blocks;
   const uint16_t* x = static_cast<const uint16_t*>(kside ? a.k : a.q);
   const uint16_t* dy = static_cast<const uint16_t*>(kside ? a.dk_out : a.dq_out);
   uint16_t* dx = static_cast<uint16_t*>(kside ? a.dk : a.dq);
   const long long xs = kside ? a.k_stride : a.q_stride, ds = kside ? a.dk_stride : a.dq_stride;
-  const Place at = place_of(l, a.rotary, a.interleaved);
-  float w[8], dw[8];
-  {
-    const float* wp = kside ? a.wk : a.wq;
-    const float4 w0 = __ldg(reinterpret_cast<const float4*>(wp + at.o0));
-    const float4 w1 = __ldg(reinterpret_cast<const float4*>(wp + at.o1));
-    w[0] = w0.x, w[1] = w0.y, w[2] = w0.z, w[3] = w0.w;
-    w[4] = w1.x, w[5] = w1.y, w[6] = w1.z, w[7] = w1.w;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) dw[j] = 0.f;
+  const Place at = place_of<ADJ>(l, a.rotary);
+  const Own w = weight_of<ADJ>(kside ? a.wk : a.wq, at);
+  Own dw = {both(0.f), both(0.f), both(0.f), both(0.f)};
   // Both teams of a warp walk the same number of units (the sums over a row
   // are warp shuffles).
-  for (long long u0 = (long long)blk * kTeams; u0 < units; u0 += (long long)blocks * kTeams) {
-    const long long u = u0 + team;
+  for (unsigned u0 = blk * kTeams; u0 < units; u0 += blocks * kTeams) {
+    const unsigned u = u0 + team;
     const bool live = u < units;
-    const int t = live ? (int)(u / chunks) : 0;
-    const int h0 = live ? (int)(u - (long long)t * chunks) * R : 0;
+    const unsigned t = live ? u / chunks : 0u;
+    const int h0 = live ? (int)(u - t * chunks) * R : 0;
     const int n = live ? min(R, heads - h0) : 0;
     const uint16_t* xp = x + t * xs + h0 * kHeadDim;
     const uint16_t* dp = dy + ((size_t)t * heads + h0) * kHeadDim;
@@ -257,48 +307,55 @@ __global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const __grid_constan
     }
     const int pos = __ldg(a.positions + t);
     const bool known = pos >= 0 && pos < a.max_position;
-    float4 cs = make_float4(1.f, 1.f, 1.f, 1.f), sn = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (at.turned && known) {
-      const float* tab = a.cos_sin + (size_t)pos * a.rotary + 4 * l;
-      cs = __ldg(reinterpret_cast<const float4*>(tab));
-      sn = __ldg(reinterpret_cast<const float4*>(tab + a.rotary / 2));
-      sn = make_float4(-sn.x, -sn.y, -sn.z, -sn.w);
-    }
+    const Angles g = angles_of(a, l, pos, at.turned && known);
+    // The rows' sums first, all of them under way together.
+    Own v[R];
+    float ss[R], dot[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      Row f, g;
-      unpack4<F16>(rx[i][0], f.e);
-      unpack4<F16>(rx[i][1], f.e + 4);
-      unpack4<F16>(rd[i][0], g.e);
-      unpack4<F16>(rd[i][1], g.e + 4);
-      if (at.turned) turn(g, cs, sn, a.interleaved);
-      float ss = 0.f, dot = 0.f;
+      const Own f = unpack<F16, ADJ>(rx[i][0], rx[i][1], at.adj);
+      v[i] = unpack<F16, ADJ>(rd[i][0], rd[i][1], at.adj);
+      if (at.turned)
+        v[i] = {fma2(v[i].a0, g.c0, mul2(v[i].b0, g.s0)), fma2(v[i].a1, g.c1, mul2(v[i].b1, g.s1)),
+                fma2(v[i].b0, g.c0, neg2(mul2(v[i].a0, g.s0))), fma2(v[i].b1, g.c1, neg2(mul2(v[i].a1, g.s1)))};
+      ss[i] = dot_of(f, f);
+      dot[i] = dot_of(product(v[i], f), w);
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ss = fmaf(f.e[j], f.e[j], ss);
-        dot = fmaf(g.e[j] * w[j], f.e[j], dot);
-      }
-      ss = team_sum(ss);
-      dot = team_sum(dot);
-      const float r = rsqrtf(ss * (1.f / kHeadDim) + a.eps);
-      const float k = r * r * dot * (1.f / kHeadDim);
-      const bool counts = known && i < n;
+    for (int d = kTeam / 2; d > 0; d >>= 1)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (counts) dw[j] = fmaf(g.e[j] * r, f.e[j], dw[j]);
-        g.e[j] = known ? r * (g.e[j] * w[j] - f.e[j] * k) : 0.f;
+      for (int i = 0; i < R; ++i) {
+        ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], d);
+        dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], d);
       }
-      if (i >= n) continue;
-      uint16_t* out = dx + t * ds + (h0 + i) * kHeadDim;
-      *reinterpret_cast<uint2*>(out + at.o0) = pack4<F16>(g.e);
-      *reinterpret_cast<uint2*>(out + at.o1) = pack4<F16>(g.e + 4);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const Own f = unpack<F16, ADJ>(rx[i][0], rx[i][1], at.adj);
+      const float r = rsqrtf(ss[i] * (1.f / kHeadDim) + a.eps);
+      const float k = -r * r * r * dot[i] * (1.f / kHeadDim);
+      if (known && i < n) {
+        const Own fr = scaled(f, r);
+        dw = {fma2(v[i].a0, fr.a0, dw.a0), fma2(v[i].a1, fr.a1, dw.a1), fma2(v[i].b0, fr.b0, dw.b0),
+              fma2(v[i].b1, fr.b1, dw.b1)};
+      }
+      if (i < n) {
+        const Own h = scaled(product(v[i], w), r);
+        const float2 k2 = both(k);
+        float2 e[4];
+        groups<ADJ>({fma2(f.a0, k2, h.a0), fma2(f.a1, k2, h.a1), fma2(f.b0, k2, h.b0), fma2(f.b1, k2, h.b1)}, at.adj, e);
+        if (!known) e[0] = e[1] = e[2] = e[3] = both(0.f);
+        uint16_t* out = dx + t * ds + (h0 + i) * kHeadDim;
+        __stcs(reinterpret_cast<uint2*>(out + at.o0), pack4<F16>(e[0], e[1]));
+        __stcs(reinterpret_cast<uint2*>(out + at.o1), pack4<F16>(e[2], e[3]));
+      }
     }
   }
   __shared__ float sums[kTeams][kHeadDim];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    sums[team][at.o0 + j] = dw[j];
-    sums[team][at.o1 + j] = dw[j + 4];
+  {
+    float2 e[4];
+    groups<ADJ>(dw, at.adj, e);
+    *reinterpret_cast<float4*>(&sums[team][at.o0]) = make_float4(e[0].x, e[0].y, e[1].x, e[1].y);
+    *reinterpret_cast<float4*>(&sums[team][at.o1]) = make_float4(e[2].x, e[2].y, e[3].x, e[3].y);
   }
   __syncthreads();
   if (threadIdx.x < kHeadDim) {
@@ -317,6 +374,7 @@ __global__ void __launch_bounds__(1024) rope_bwd_sum_kernel(const __grid_constan
   const int col = (blockIdx.x & 3) * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
   const int first = kside ? a.q_blocks : 0, last = kside ? blocks : a.q_blocks;
   float s = 0.f;
+#pragma unroll 8
   for (int i = first + g; i < last; i += 32) s += a.partials[(size_t)i * kHeadDim + col];
   __shared__ float sums[32][32];
   sums[g][threadIdx.x & 31] = s;
@@ -329,15 +387,28 @@ __global__ void __launch_bounds__(1024) rope_bwd_sum_kernel(const __grid_constan
   }
 }
 
-constexpr int kBwdRows = 2;  // heads of a token in flight per team
+// Heads of a token in flight per team. Forward 4 / 6 / 8: 203 / 199 / 202 us on
+// the size above. Backward, with the blocks an SM holds: 1 row 373, 2 rows 329
+// (4 blocks), 4 rows 292 (2 blocks); more blocks than an SM holds gain nothing.
+constexpr int kFwdRows = 6, kAppendRows = 4;
+constexpr int kBwdRows = 4;
 
-template <bool F16, int KV>
-cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
-  constexpr int R = 4;
+template <bool F16, bool ADJ, int KV>
+cudaError_t launch_rope_r(const RopeArgs& a, cudaStream_t s) {
+  constexpr int R = KV ? kAppendRows : kFwdRows;
   const long long per_token = (a.hq + R - 1) / R + (KV ? 2 : 1) * (long long)((a.hkv + R - 1) / R);
   const long long teams = (long long)a.tokens * per_token;
-  rope_kernel<F16, KV, R><<<(unsigned)((teams + kTeams - 1) / kTeams), kThreads, 0, s>>>(a);
+  rope_kernel<F16, ADJ, KV, R><<<(unsigned)((teams + kTeams - 1) / kTeams), kThreads, 0, s>>>(a);
   return cudaGetLastError();
+}
+template <bool F16, int KV>
+cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
+  return a.interleaved ? launch_rope_r<F16, true, KV>(a, s) : launch_rope_r<F16, false, KV>(a, s);
+}
+template <bool F16>
+void launch_rope_bwd_t(const RopeBwdArgs& a, int blocks, cudaStream_t s) {
+  if (a.interleaved) rope_bwd_kernel<F16, true, kBwdRows><<<blocks, kThreads, 0, s>>>(a);
+  else rope_bwd_kernel<F16, false, kBwdRows><<<blocks, kThreads, 0, s>>>(a);
 }
 
 }  // namespace
@@ -350,9 +421,9 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
 }
 
 RopeBwdGrid rope_bwd_grid(long long tokens, int hq, int hkv) {
-  // Enough blocks to fill the GPU (8 of 256 threads fit an SM), shared between the sides by their rows, but no
-  // more than have a unit each.
-  constexpr long long kMost = 152 * 8;
+  // Enough blocks to fill the GPU, shared between the sides by their rows, but
+  // no more than have a unit each.
+  constexpr long long kMost = 152 * kBwdResident;
   const long long uq = tokens * ((hq + kBwdRows - 1) / kBwdRows), uk = tokens * ((hkv + kBwdRows - 1) / kBwdRows);
   const long long bq = (uq + kTeams - 1) / kTeams, bk = (uk + kTeams - 1) / kTeams;
   RopeBwdGrid g{(int)bq, (int)bk};
@@ -366,8 +437,8 @@ RopeBwdGrid rope_bwd_grid(long long tokens, int hq, int hkv) {
 cudaError_t launch_rope_bwd(const RopeBwdArgs& a, int k_blocks, cudaStream_t s) {
   const int blocks = a.q_blocks + k_blocks;
   if (blocks > 0) {
-    if (a.f16) rope_bwd_kernel<true, kBwdRows><<<blocks, kThreads, 0, s>>>(a);
-    else rope_bwd_kernel<false, kBwdRows><<<blocks, kThreads, 0, s>>>(a);
+    if (a.f16) launch_rope_bwd_t<true>(a, blocks, s);
+    else launch_rope_bwd_t<false>(a, blocks, s);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
