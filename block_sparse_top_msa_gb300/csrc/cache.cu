@@ -149,6 +149,7 @@ MSA_DEV int block_exclusive(int v, int* s, int& total) {
 // tables here, forks by the kernel after this one.
 template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_constant__ CacheTableArgs a) {
+  grid_dependents_launch();
   extern __shared__ int smem[];
   int* claim = smem;                   // num_rows: the first request for the row
   int* need = claim + a.num_rows;      // n: pages wanted, or -1 refused
@@ -162,37 +163,55 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     if (r >= 0 && r < a.num_rows) atomicMin(&claim[r], i);
   }
   __syncthreads();
-  for (int i = warp; i < a.n; i += kPlanThreads / 32) {
-    const int r = a.rows[i];
+  // What can be told without reading whole rows, a thread per request.
+  for (int i = tid; i < a.n; i += kPlanThreads) {
+    const int r = a.rows[i], src = FORK ? a.src_rows[i] : 0, len = FORK ? 0 : a.lengths[i];
     bool ok = r >= 0 && r < a.num_rows && claim[r] == i;
     int want = 0;
     if (FORK) {
-      const int src = a.src_rows[i];
       ok = ok && src >= 0 && src < a.num_rows && claim[src] == INT_MAX;
-      if (ok) {
-        const int len = a.seqused_k[src];
-        ok = len >= 0 && (long long)len <= (long long)a.max_pages * kBlk && a.seqused_k[r] == 0;
-        // The row forked to holds no page.
-        const int32_t* row = a.page_table + (size_t)r * a.max_pages;
-        bool held = false;
-        for (int t = lane; t < a.max_pages; t += 32) held |= row[t] >= 0;
-        ok = ok && !__any_sync(0xffffffffu, held);
-        if (ok && len % kBlk != 0) {
-          const int p = a.page_table[(size_t)src * a.max_pages + len / kBlk];
-          want = p >= 0 && p < a.num_pages;
-        }
+      const int n = ok ? a.seqused_k[src] : 0, own = ok ? a.seqused_k[r] : 0;
+      ok = ok && n >= 0 && (long long)n <= (long long)a.max_pages * kBlk && own == 0;
+      if (ok && n % kBlk != 0) {
+        const int p = a.page_table[(size_t)src * a.max_pages + n / kBlk];
+        want = p >= 0 && p < a.num_pages;
       }
     } else {
-      const int len = a.lengths[i];
-      ok = ok && len >= a.seqused_k[r] && (long long)len <= (long long)a.max_pages * kBlk;
-      if (ok) {
+      const int own = ok ? a.seqused_k[r] : 0;
+      ok = ok && len >= own && (long long)len <= (long long)a.max_pages * kBlk;
+      // Room for up to four more blocks is counted here, for more below.
+      const int first = max(0, own) / kBlk, last = (int)(((long long)len + kBlk - 1) / kBlk);
+      if (ok && last - first > 4) {
+        want = INT_MAX;
+      } else if (ok) {
         const int32_t* row = a.page_table + (size_t)r * a.max_pages;
-        const int last = (len + kBlk - 1) / kBlk;
-        for (int t0 = max(0, a.seqused_k[r]) / kBlk; t0 < last; t0 += 32)
-          want += __popc(__ballot_sync(0xffffffffu, t0 + lane < last && row[min(t0 + lane, last - 1)] < 0));
+#pragma unroll
+        for (int t = 0; t < 4; ++t) want += first + t < last && row[first + t] < 0;
       }
     }
-    if (lane == 0) need[i] = ok ? want : -1;
+    need[i] = ok ? want : -1;
+  }
+  __syncthreads();
+  // Whole rows, a warp per request: a row forked to holds no page; the pages
+  // that a long extension lacks.
+  for (int i = warp; i < a.n; i += kPlanThreads / 32) {
+    if (FORK ? need[i] < 0 : need[i] != INT_MAX) continue;
+    const int r = a.rows[i];
+    const int32_t* row = a.page_table + (size_t)r * a.max_pages;
+    int t0 = 0, last = a.max_pages;
+    if (!FORK) {
+      t0 = max(0, a.seqused_k[r]) / kBlk;
+      last = (int)(((long long)a.lengths[i] + kBlk - 1) / kBlk);
+    }
+    int count = 0;
+#pragma unroll 8
+    for (int t = t0 + lane; t < last; t += 32) count += FORK ? row[t] >= 0 : row[t] < 0;
+    count = __reduce_add_sync(0xffffffffu, count);
+    __syncwarp();
+    if (lane == 0) {
+      if (!FORK) need[i] = count;
+      else if (count > 0) need[i] = -1;
+    }
   }
   __syncthreads();
   // Pages wanted before each request.
@@ -204,26 +223,42 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     if (i < a.n) offset[i] = sum + before;
     sum += total;
   }
-  // The first `sum` free pages, ascending.
+  // The first `sum` free pages, ascending: the next step's counts are on their
+  // way while this one's free pages are numbered.
   int found = 0;
   const int wanted = min(sum, a.num_pages);
-  for (int p0 = 0; p0 < a.num_pages && found < wanted; p0 += kPlanThreads * kScanPerThread) {
-    const int p = p0 + tid * kScanPerThread;
-    unsigned freed = 0;
-    if (p + kScanPerThread <= a.num_pages && (reinterpret_cast<uintptr_t>(a.page_refs) & 15) == 0) {
+  const bool quads = (reinterpret_cast<uintptr_t>(a.page_refs) & 15) == 0;
+  int4 held[kScanPerThread / 4];
+  const unsigned pages = (unsigned)a.num_pages;
+  auto fetch = [&](unsigned p) {
 #pragma unroll
-      for (int q = 0; q < kScanPerThread; q += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(a.page_refs + p + q);
-        freed |= (unsigned)((v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3) << q;
+    for (int q = 0; q < kScanPerThread; q += 4) {
+      int4& v = held[q / 4];
+      if (quads && p + q + 4 <= pages) {
+        v = *reinterpret_cast<const int4*>(a.page_refs + p + q);
+      } else {
+        v.x = p + q < pages ? a.page_refs[p + q] : 1;
+        v.y = p + q + 1 < pages ? a.page_refs[p + q + 1] : 1;
+        v.z = p + q + 2 < pages ? a.page_refs[p + q + 2] : 1;
+        v.w = p + q + 3 < pages ? a.page_refs[p + q + 3] : 1;
       }
-    } else {
-      for (int q = 0; q < kScanPerThread; ++q)
-        if (p + q < a.num_pages && a.page_refs[p + q] == 0) freed |= 1u << q;
     }
+  };
+  constexpr unsigned step = kPlanThreads * kScanPerThread;
+  if (wanted > 0) fetch(tid * kScanPerThread);
+  for (unsigned p0 = 0; p0 < pages && found < wanted; p0 += step) {
+    const unsigned p = p0 + tid * kScanPerThread;
+    unsigned freed = 0;
+#pragma unroll
+    for (int q = 0; q < kScanPerThread; q += 4) {
+      const int4 v = held[q / 4];
+      freed |= (unsigned)((v.x == 0) | (v.y == 0) << 1 | (v.z == 0) << 2 | (v.w == 0) << 3) << q;
+    }
+    if (p0 + step < pages) fetch(p + step);
     int total;
     int at = found + block_exclusive(__popc(freed), scan, total);
     while (freed != 0u && at < wanted) {
-      a.list[at++] = p + __ffs(freed) - 1;
+      a.list[at++] = (int)p + __ffs(freed) - 1;
       freed &= freed - 1;
     }
     found += total;
@@ -261,30 +296,6 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   }
 }
 
-// The table row of each granted fork: the source's whole pages, each with one
-// more holder, then the fresh page, then nothing.
-__global__ void __launch_bounds__(kFreeThreads) cache_fork_table_kernel(const __grid_constant__ CacheTableArgs a) {
-  const int i = blockIdx.x;
-  const int page = a.plan[i];
-  if (page == -2) return;
-  const int src = a.src_rows[i], dst = a.rows[i];
-  const int len = a.seqused_k[src], whole = len / kBlk;
-  const int32_t* from = a.page_table + (size_t)src * a.max_pages;
-  int32_t* to = a.page_table + (size_t)dst * a.max_pages;
-  for (int t = threadIdx.x; t < a.max_pages; t += kFreeThreads) {
-    int p = -1;
-    if (t < whole) {
-      p = from[t];
-      if (p >= 0 && p < a.num_pages) atomicAdd(a.page_refs + p, 1);
-      else p = -1;
-    } else if (t == whole) {
-      p = page;
-    }
-    to[t] = p;
-  }
-  if (threadIdx.x == 0) a.seqused_k[dst] = len;
-}
-
 // -------------------------------------------------------------------- copies
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnroll = 8;
@@ -305,17 +316,40 @@ MSA_DEV void copy_chunk(const uint8_t* src, uint8_t* dst, long long bytes) {
       *reinterpret_cast<uint4*>(dst + o + i * kCopyThreads * 16ll) = v[i];
 }
 
+// A granted fork: in block (.., num_pools, i), if there is one, the table row:
+// the source's whole pages, each with one more holder, then the fresh page,
+// then nothing; in the others the begun page, a chunk of a pool each.
 __global__ void __launch_bounds__(kCopyThreads)
-    cache_fork_copy_kernel(const __grid_constant__ CachePools pools, long long page_bytes,
-                           const __grid_constant__ CacheTableArgs a) {
+    cache_fork_kernel(const __grid_constant__ CachePools pools, int num_pools, long long page_bytes,
+                      const __grid_constant__ CacheTableArgs a) {
+  grid_dependency_wait();  // the plan
   const int i = blockIdx.z;
   const int page = a.plan[i];
-  if (page < 0) return;
   const int src = a.src_rows[i];
-  const int from = a.page_table[(size_t)src * a.max_pages + a.seqused_k[src] / kBlk];
+  if (page == -2) return;
+  const int len = a.seqused_k[src], whole = len / kBlk;
+  const int32_t* from = a.page_table + (size_t)src * a.max_pages;
+  if ((int)blockIdx.y == num_pools) {
+    const int dst = a.rows[i];
+    int32_t* to = a.page_table + (size_t)dst * a.max_pages;
+    for (int t = blockIdx.x * kCopyThreads + threadIdx.x; t < a.max_pages; t += gridDim.x * kCopyThreads) {
+      int p = -1;
+      if (t < whole) {
+        p = from[t];
+        if (p >= 0 && p < a.num_pages) atomicAdd(a.page_refs + p, 1);
+        else p = -1;
+      } else if (t == whole) {
+        p = page;
+      }
+      to[t] = p;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.seqused_k[dst] = len;
+    return;
+  }
+  if (page < 0) return;
   uint8_t* base = static_cast<uint8_t*>(pools.base[blockIdx.y]);
   const long long o = (long long)blockIdx.x * kCopyChunk;
-  copy_chunk(base + (long long)from * page_bytes + o, base + (long long)page * page_bytes + o,
+  copy_chunk(base + (long long)from[whole] * page_bytes + o, base + (long long)page * page_bytes + o,
              min((long long)kCopyChunk, page_bytes - o));
 }
 
@@ -368,17 +402,20 @@ cudaError_t launch_cache_free(const CacheTableArgs& a, cudaStream_t s) {
 
 cudaError_t launch_cache_extend(const CacheTableArgs& a, cudaStream_t s) { return launch_plan<false>(a, s); }
 
-cudaError_t launch_cache_fork(const CacheTableArgs& a, cudaStream_t s) {
-  const cudaError_t e = launch_plan<true>(a, s);
-  if (e != cudaSuccess) return e;
-  cache_fork_table_kernel<<<a.n, kFreeThreads, 0, s>>>(a);
-  return cudaGetLastError();
-}
+cudaError_t launch_cache_fork(const CacheTableArgs& a, cudaStream_t s) { return launch_plan<true>(a, s); }
 
-cudaError_t launch_cache_fork_copy(const CachePools& p, int num_pools, long long page_bytes,
+cudaError_t launch_cache_fork_copy(const CachePools& p, int num_pools, long long page_bytes, bool tables,
                                    const CacheTableArgs& a, cudaStream_t s) {
-  cache_fork_copy_kernel<<<copy_grid(num_pools, page_bytes, a.n), kCopyThreads, 0, s>>>(p, page_bytes, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = copy_grid(num_pools + (tables ? 1 : 0), page_bytes, a.n);
+  cfg.blockDim = dim3(kCopyThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = tables ? 1 : 0;  // right behind the plan
+  return cudaLaunchKernelEx(&cfg, cache_fork_kernel, p, num_pools, page_bytes, a);
 }
 
 cudaError_t launch_cache_copy_pages(const CachePools& p, int num_pools, long long page_bytes,

@@ -372,9 +372,10 @@ struct CacheTableArgs {
 };
 cudaError_t launch_cache_free(const CacheTableArgs& a, cudaStream_t s);
 cudaError_t launch_cache_extend(const CacheTableArgs& a, cudaStream_t s);
-// The plan and the tables; the begun pages' copies follow for each group of pools.
+// The plan; then, for each group of pools, the begun pages' copies, with the
+// first group (tables) the rows too.
 cudaError_t launch_cache_fork(const CacheTableArgs& a, cudaStream_t s);
-cudaError_t launch_cache_fork_copy(const CachePools& p, int num_pools, long long page_bytes,
+cudaError_t launch_cache_fork_copy(const CachePools& p, int num_pools, long long page_bytes, bool tables,
                                    const CacheTableArgs& a, cudaStream_t s);
 cudaError_t launch_cache_copy_pages(const CachePools& p, int num_pools, long long page_bytes,
                                     int num_pages, const int32_t* src, const int32_t* dst, int n,

@@ -208,9 +208,12 @@ msa_status_t msa_cache_fork(void* const* pools, int num_pools, long long page_by
   st = place_plan(&a, workspace, workspace_bytes);
   if (st != MSA_OK) return st;
   cudaError_t e = launch_cache_fork(a, stream);
+  bool tables = true;
   if (e == cudaSuccess)
     e = for_pools(pools, num_pools, [&](const CachePools& p, int count) {
-      return launch_cache_fork_copy(p, count, page_bytes, a, stream);
+      const cudaError_t r = launch_cache_fork_copy(p, count, page_bytes, tables, a, stream);
+      tables = false;
+      return r;
     });
   return from_cuda(e);
 }
