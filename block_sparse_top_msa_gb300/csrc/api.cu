@@ -652,7 +652,7 @@ msa_status_t build_forward(
 // cut.
 struct TreeLayout {
   int W, unit_tokens, max_tiles, cap, words, grid, rows_part;
-  size_t off_info, off_len, off_blocks, off_member, off_part_o, off_part_ml, off_cut, total;
+  size_t off_info, off_len, off_blocks, off_member, off_part_o, off_part_ml, off_cut, off_odd, total;
 };
 
 // Most tokens of a unit and pages of a sequence: what the union kernel's
@@ -697,6 +697,7 @@ TreeLayout tree_layout(int batch, int total_q, int hq, int hkv, int topk, int ma
   L.off_part_o = place(2 * (size_t)L.grid * L.rows_part * 128 * sizeof(float));
   L.off_part_ml = place(2 * (size_t)L.grid * L.rows_part * sizeof(float2));
   L.off_cut = place((size_t)L.grid * sizeof(int2));
+  L.off_odd = place((1 + (size_t)total_q * hq) * sizeof(int32_t));
   L.total = off;
   return L;
 }
@@ -785,6 +786,8 @@ msa_status_t build_tree(
   a.part_m = reinterpret_cast<float*>(ws + L.off_part_ml);
   a.part_l = a.part_m + 2 * (size_t)L.grid * L.rows_part;
   a.cut = reinterpret_cast<int2*>(ws + L.off_cut);
+  a.odd = reinterpret_cast<int32_t*>(ws + L.off_odd);
+  a.q = q;
   a.out = out;
   a.lse = lse;
   return MSA_OK;

@@ -147,6 +147,7 @@ struct TreeArgs {
   CUtensorMap tmap_q;  // (d, Hq, Tq) 16-bit, box (64, G, tile_tokens)
   CUtensorMap tmap_k;  // (.., 128, Hkv, pages), 16-bit caches
   CUtensorMap tmap_v;
+  const void* q;
   const uint8_t* k_pool;
   const uint8_t* v_pool;
   int e4m3, f16;       // the cache's type, else bf16
@@ -178,6 +179,7 @@ struct TreeArgs {
   float* part_l;
   int2* cut;        // (grid): the unit that begins in the CTA's range and goes on after it, and the
                     // one that began before it (of the CTA's first segment); -1: none
+  int32_t* odd;     // (1 + Tq * Hq): how many rows were not finite, and which
   void* out;
   float* lse;
 };

@@ -31,14 +31,19 @@
 // Keys past a sequence's end are masked in S, and their V rows zeroed in
 // shared memory, as P = 0 times what a page may hold there need not be 0.
 //
-// E4M3 is decoded to f16 by moving bits (sign to sign, the seven others below
-// it): that is the value times 2^-8, exactly, subnormal codes included, in
-// four integer instructions a pair. Conversions to bf16 took the unit that
-// the softmax's exponentials run on and bound the kernel (6000 to 8000 clocks
-// a block against 3500 here). Q then is f16 too, each bf16 row scaled by the
-// power of two that puts its largest value just below f16's largest (what
-// falls below f16's range is under 2^-39 of that); the powers of two come
-// back with the softmax scale and the output.
+// E4M3 is decoded to f16, exactly, NaN codes included, by one conversion a
+// pair (moving the bits by integer instructions: 372 us against 352 for 128
+// requests; on to bf16, two more conversions a pair: 646 in the kernel before
+// this one). Q then is f16 too, each bf16 row scaled by the power of two that
+// puts its largest value just below f16's largest (what falls below f16's
+// range is under 2^-39 of that); the power of two comes back with the softmax
+// scale.
+//
+// A tile's rows share the products, so a row also multiplies, by P = 0, what
+// it must not see: values of another row's drafts or blocks, which may be
+// infinite or NaN. Rows whose l or O is not finite are left to odd_row, which
+// computes them anew from the row's own keys alone.
+#include <cuda_fp16.h>
 #include <math.h>
 
 #include <climits>
@@ -236,32 +241,26 @@ struct Ring {
     }
   }
 };
-// Sixteen E4M3 codes as eight packed pairs of f16, times 2^-8.
-MSA_DEV void e4m3x16_to_f16(uint4 raw, uint32_t (&o)[8]) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const uint32_t v = __byte_perm(w[i], 0u, p == 0 ? 0x1404 : 0x3424);
-      o[2 * i + p] = (v & 0x80008000u) | ((v >> 1) & 0x3f803f80u);
-    }
-  }
+// The largest of three, NaN if one is: a NaN among keys that are masked
+// otherwise has to show.
+MSA_DEV float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
-
 template <int N>
 MSA_DEV float row_max(const float* v) {
   float m0 = v[0], m1 = v[1], m2 = v[2], m3 = v[3];
 #pragma unroll
   for (int c = 4; c + 8 <= N; c += 8) {
-    m0 = fmax3(m0, v[c], v[c + 1]);
-    m1 = fmax3(m1, v[c + 2], v[c + 3]);
-    m2 = fmax3(m2, v[c + 4], v[c + 5]);
-    m3 = fmax3(m3, v[c + 6], v[c + 7]);
+    m0 = max3_nan(m0, v[c], v[c + 1]);
+    m1 = max3_nan(m1, v[c + 2], v[c + 3]);
+    m2 = max3_nan(m2, v[c + 4], v[c + 5]);
+    m3 = max3_nan(m3, v[c + 6], v[c + 7]);
   }
-  m0 = fmax3(m0, v[N - 4], v[N - 3]);
-  m1 = fmax3(m1, v[N - 2], v[N - 1]);
-  return fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
+  m0 = max3_nan(m0, v[N - 4], v[N - 3]);
+  m1 = max3_nan(m1, v[N - 2], v[N - 1]);
+  return max3_nan(max3_nan(m0, m1, m2), m3, m3);
 }
 
 // Inclusive sum over the warp.
@@ -287,7 +286,10 @@ __global__ void __launch_bounds__(kUnionThreads) tree_union_kernel(const __grid_
   __shared__ int s_warp[kUnionThreads / 32];
   __shared__ int s_b, s_t0;
   grid_dependents_launch();
-  if (tid == 0) s_b = -1;
+  if (tid == 0) {
+    s_b = -1;
+    if (tile == 0 && h == 0) *a.odd = 0;
+  }
   int carry = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kUnionThreads) {
     const int b = b0 + tid;
@@ -923,7 +925,10 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       for (int c = 0; c < 8; ++c) {
         const int r = r0 + c * 16;
         uint32_t o[8];
-        e4m3x16_to_f16(raw[c], o);
+        e4m3x4_to_f16(raw[c].x, o[0], o[1]);
+        e4m3x4_to_f16(raw[c].y, o[2], o[3]);
+        e4m3x4_to_f16(raw[c].z, o[4], o[5]);
+        e4m3x4_to_f16(raw[c].w, o[6], o[7]);
         uint8_t* half = dst + (q >> 2) * kHalf;
         const int c16 = (q & 3) * 2;
         *reinterpret_cast<uint4*>(half + sw128_offset(r, c16)) = make_uint4(o[0], o[1], o[2], o[3]);
@@ -988,7 +993,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           const int e = (int)(big >> 7);  // exponent field of the row's largest value
           const int k = e == 255 ? 0 : min(120, 142 - e);
           const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-          scale = a.scale_log2 * __uint_as_float((uint32_t)(127 + 8 - k) << 23);
+          scale = a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
 #pragma unroll 4
           for (int c = 0; c < 16; ++c) {
             uint4* at = reinterpret_cast<uint4*>(qt + (c >> 3) * kHalf + sw128_offset(row, c & 7));
@@ -1090,7 +1095,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
             for (int c0q = 0; c0q < 64; c0q += kCols) {
               if constexpr (kCols == 64) tmem_ld64(hcol, sv);
               else tmem_ld32(hcol + c0q, sv);
-              mx = fmaxf(mx, row_max<kCols>(sv));
+              mx = max3_nan(mx, mx, row_max<kCols>(sv));
             }
             const bool on = mem && mx != -INFINITY;
             float alpha = 1.f;
@@ -1196,10 +1201,10 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       tc_fence_after();
       const bool joins = !s.dual && n > 1;
       const bool has = l > 0.f;
-      const float os = FP8 ? 256.f : 1.f;  // V's powers of two
-      const float inv = has ? os / l : 0.f;
+      const float inv = has ? 1.f / l : 0.f;
       const size_t slot = s.slot < 0 ? 0 : s.slot;
       const int prow_out = (s.dual ? st * W * G : 0) + row;
+      float2 odd = make_float2(0.f, 0.f);  // NaN once an element of O is not finite
 #pragma unroll 1
       for (int c0q = 0; c0q < 128; c0q += 32) {
         float o[32];
@@ -1220,6 +1225,9 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           }
         }
         if (active && s.slot < 0) {
+#pragma unroll
+          for (int c = 0; c < 32; c += 2)
+            odd = __ffma2_rn(make_float2(o[c], o[c + 1]), make_float2(0.f, 0.f), odd);
           uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * kHeadDim + c0q);
 #pragma unroll
           for (int c = 0; c < 32; c += 8)
@@ -1232,7 +1240,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           // Column by column, so that a warp's rows are one piece of memory.
           float* dst = a.part_o + (slot * kHeadDim + c0q) * a.rows_part + prow_out;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) dst[(size_t)c * a.rows_part] = o[c] * os;
+          for (int c = 0; c < 32; ++c) dst[(size_t)c * a.rows_part] = o[c];
         }
         __syncwarp();
       }
@@ -1240,7 +1248,10 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         if (s.slot >= 0) {
           a.part_m[slot * a.rows_part + prow_out] = m_ref;
           a.part_l[slot * a.rows_part + prow_out] = l;
-        } else if (a.lse != nullptr) a.lse[orow] = has ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        } else {
+          if (a.lse != nullptr) a.lse[orow] = has ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          if (l != 0.f && !(odd.x + odd.y == 0.f && l < INFINITY)) a.odd[1 + atomicAdd(a.odd, 1)] = (int)orow;
+        }
       }
     }
   }
@@ -1253,24 +1264,107 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
   }
 }
 
+// Output row (token, query head) from its own visible keys, in fp32, by a
+// warp: a lane takes a key of 32, and then four columns of their V. For rows
+// that are not finite above; as slow as it is short.
+__device__ __noinline__ void odd_row(const TreeArgs& a, size_t orow, int lane) {
+  const int t = (int)(orow / a.num_qo_heads), hq = (int)(orow - (size_t)t * a.num_qo_heads);
+  const int h = hq / (a.num_qo_heads / a.num_kv_heads);
+  int b = 0;  // the last sequence that begins at or before t
+  for (int hi = a.batch; hi - b > 1;) {
+    const int mid = (b + hi) >> 1;
+    if (__ldg(a.cu_q + mid) <= t) b = mid; else hi = mid;
+  }
+  const int lq = __ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b), lk = __ldg(a.seqused_k + b);
+  const int nblk = min((int)(((long long)lk + kBlk - 1) / kBlk), a.max_pages);
+  auto value = [&](const uint8_t* rows, int i, bool e4m3) {
+    if (e4m3) {
+      uint32_t lo, hi;
+      e4m3x4_to_f16(__ldg(rows + i), lo, hi);
+      return __low2float(*reinterpret_cast<const __half2*>(&lo));
+    }
+    const uint16_t w = __ldg(reinterpret_cast<const uint16_t*>(rows) + i);
+    return a.f16 ? __half2float(__ushort_as_half(w)) : __uint_as_float((uint32_t)w << 16);
+  };
+  const uint8_t* q = static_cast<const uint8_t*>(a.q) + orow * kHeadDim * 2;
+  const int32_t* ids = a.q2k + ((size_t)h * a.total_q + t) * a.topk;
+  const int id0 = lane < a.topk ? __ldg(ids + lane) : -1, id1 = lane + 32 < a.topk ? __ldg(ids + lane + 32) : -1;
+  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < a.topk; ++i) {
+    const int id = __shfl_sync(0xffffffffu, i < 32 ? id0 : id1, i & 31);
+    // A block listed twice counts once.
+    const bool again = (lane < i && id0 == id) || (lane + 32 < i && id1 == id);
+    if (__any_sync(0xffffffffu, again) || id < 0 || id >= nblk) continue;
+    const int page = __ldg(a.page_table + (size_t)b * a.max_pages + id);
+    if (page < 0 || page >= a.num_pages) continue;
+    const size_t at = ((size_t)page * a.num_kv_heads + h) * kBlk * kHeadDim * (a.e4m3 ? 1 : 2);
+    const long long left = (long long)lk - (long long)id * kBlk;
+    const int tail = left < kBlk ? (int)left : kBlk;
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t see = tree_bits(a.tree_mask + (size_t)t * a.mask_words, a.mask_words,
+                                     (long long)id * kBlk - ((long long)lk - lq), k, tail - 1);
+      if (see == 0u) continue;
+      float s = -INFINITY;
+      if ((see >> lane) & 1u) {
+        s = 0.f;
+#pragma unroll 8
+        for (int c = 0; c < kHeadDim; ++c)
+          s = fmaf(value(q, c, false), value(a.k_pool + at, (32 * k + lane) * kHeadDim + c, a.e4m3), s);
+        s *= a.scale_log2;
+      }
+      float top = s;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+      top = fmaxf(top, m);
+      const bool nan = __any_sync(0xffffffffu, s != s);
+      if (top == -INFINITY && !nan) continue;
+      const float alpha = m == -INFINITY ? 0.f : ex2(m - top);
+      const float p = s == -INFINITY ? 0.f : ex2(s - top);
+      m = top;
+      l *= alpha;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[c] *= alpha;
+      for (int x = 0; x < 32; ++x) {
+        const float px = __shfl_sync(0xffffffffu, p, x);
+        if (!((see >> x) & 1u)) continue;
+        l += px;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          acc[c] = fmaf(px, value(a.v_pool + at, (32 * k + x) * kHeadDim + 4 * lane + c, a.e4m3), acc[c]);
+      }
+    }
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  auto pack = [&](float x, float y) { return a.f16 ? pack_f16x2(x, y) : pack_bf16x2(x, y); };
+  reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * kHeadDim)[lane] =
+      make_uint2(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv));
+  if (lane == 0 && a.lse != nullptr) a.lse[orow] = l != 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+}
+
 // Joins the partials of the unit that is cut at the end of CTA k's range and
 // begins within it (the CTAs after it whose first segment is of that unit hold
 // the others): with M = max m_i and L = sum 2^(m_i - M) l_i, out = sum
 // 2^(m_i - M) O_i / L and lse = (M + log2 L) ln 2, the sums in the order of
 // the ranges. A block takes kMergeRows of the unit's rows, a thread four rows
 // of four columns; kMergeChunk partials at a time, whose weights go through
-// shared memory while their O are on the way.
+// shared memory while their O are on the way. Odd rows are computed here too:
+// those that whole units listed, and those that joining finds.
 constexpr int kMergeRows = 64, kMergeThreads = 512, kMergeAhead = 4, kMergeChunk = 16;
 __global__ void __launch_bounds__(kMergeThreads)
-    merge_tree_kernel(const __grid_constant__ TreeArgs a, int grid, int f16) {
+    merge_tree_kernel(const __grid_constant__ TreeArgs a) {
   __shared__ uint32_t s_out[kMergeRows][kHeadDim / 2 + 1];
   __shared__ float s_m[kMergeChunk][kMergeRows], s_l[kMergeChunk][kMergeRows];
   __shared__ int s_end;
-  const int k = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ uint32_t s_odd[kMergeRows / 32];
+  const int k = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, grid = gridDim.x;
   if (tid == 0) s_end = grid;
+  if (tid < kMergeRows / 32) s_odd[tid] = 0u;
   __syncthreads();
   grid_dependency_wait();
-  const int unit = __ldcg(a.cut + k).x;
+  const int unit = __ldcg(a.cut + k).x, odd = __ldcg(a.odd);
+  for (int i = (blockIdx.y * grid + k) * (kMergeThreads / 32) + warp; i < odd;
+       i += gridDim.y * grid * (kMergeThreads / 32))
+    odd_row(a, (size_t)__ldcg(a.odd + 1 + i), lane);
   if (unit < 0) return;
   for (int i = k + 1 + tid; i < grid; i += kMergeThreads)
     if (__ldcg(a.cut + i).y != unit) atomicMin(&s_end, i);
@@ -1345,10 +1439,14 @@ __global__ void __launch_bounds__(kMergeThreads)
     __syncthreads();
   }
   // Through shared memory to whole rows.
-  auto pack = [&](float x, float y) { return f16 ? pack_f16x2(x, y) : pack_bf16x2(x, y); };
+  auto pack = [&](float x, float y) { return a.f16 ? pack_f16x2(x, y) : pack_bf16x2(x, y); };
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const float inv = L[r] > 0.f ? 1.f / L[r] : 0.f;
+    float sum = 0.f;  // NaN where an element is not finite
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sum = fmaf(acc[c][r], 0.f, sum);
+    if (L[r] != 0.f && !(sum == 0.f && L[r] < INFINITY)) atomicOr(&s_odd[(q + r) >> 5], 1u << ((q + r) & 31));
     s_out[q + r][c4 * 2] = pack(acc[0][r] * inv, acc[1][r] * inv);
     s_out[q + r][c4 * 2 + 1] = pack(acc[2][r] * inv, acc[3][r] * inv);
     const int row = row0 + q + r, token = row / G;
@@ -1360,8 +1458,11 @@ __global__ void __launch_bounds__(kMergeThreads)
   for (int r = warp; r < rows; r += kMergeThreads / 32) {
     const int row = row0 + r, token = row / G;
     const size_t orow = (size_t)(info.x + token) * a.num_qo_heads + (size_t)h * G + (row - token * G);
-    reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * kHeadDim)[lane] =
-        make_uint2(s_out[r][2 * lane], s_out[r][2 * lane + 1]);
+    if ((s_odd[r >> 5] >> (r & 31)) & 1u)
+      odd_row(a, orow, lane);
+    else
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * kHeadDim)[lane] =
+          make_uint2(s_out[r][2 * lane], s_out[r][2 * lane + 1]);
   }
 }
 
@@ -1392,7 +1493,7 @@ cudaError_t launch_t(const TreeArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const int rows = a.unit_tokens * (a.num_qo_heads / a.num_kv_heads);
   return launch_dependent(merge_tree_kernel, dim3(a.grid, (rows + kMergeRows - 1) / kMergeRows), kMergeThreads,
-                          0, s, a, a.grid, F16 ? 1 : 0);
+                          0, s, a);
 }
 
 }  // namespace

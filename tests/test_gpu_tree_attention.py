@@ -206,3 +206,95 @@ def test_other_routes_leave_it_alone(msa):
         check(c, *run(msa, c))
     finally:
         msa.msa_set_prefill_route(0)
+
+
+ODD = [
+    ([9, 17], [1000, 140], 32, 2, 5, "fp16"),
+    ([33, 2, 64], [290, 400, 64], 16, 2, 6, "bf16"),
+    ([5, 1, 12], [1200, 300, 140], 16, 2, 4, "e4m3"),
+    ([70, 64], [190, 640], 16, 2, 2, "e4m3"),
+    ([1, 1], [3000, 129], 8, 8, 20, "bf16"),
+    # blocks of one unit over several ranges
+    ([20], [5000], 32, 2, 36, "bf16"),
+    ([20], [5000], 32, 2, 36, "e4m3"),
+]
+
+
+@pytest.mark.parametrize("where", ["k", "v", "block"])
+@pytest.mark.parametrize("lens,used,hq,hkv,topk,kv", ODD)
+def test_what_a_row_does_not_see_may_be_anything(msa, lens, used, hq, hkv, topk, kv, where):
+    """Keys and values that are not finite, in a draft's row or in a block that one token lists: whoever does not see them is as
+    near its 64-bit result as ever, whoever does gets the formula's NaN or infinity."""
+    c = make(lens, used, hq, hkv, topk, kv, seed=5, garbage=False)
+    nan, inf = float("nan"), float("nan") if kv == "e4m3" else float("inf")
+    kf, vf = c["k"].float(), c["v"].float()
+    for b, n in enumerate(lens):
+        lo, first = int(c["cu"][b]), used[b] - n
+        if where == "block":
+            blk = 0
+            c["q2k"][:, lo + 1 : lo + n] = torch.where(c["q2k"][:, lo + 1 : lo + n] == blk, -1, c["q2k"][:, lo + 1 : lo + n])
+            page = int(c["table"][b, blk])
+            kf[page, :, 3] = nan
+            vf[page, :, 5, 7] = inf
+        else:
+            p = first + n // 2
+            page, row = int(c["table"][b, p // 128]), p % 128
+            if where == "k":
+                kf[page, :, row] = nan
+                vf[page, :, row] = -inf
+            else:
+                vf[page, :, row, 9] = inf
+                vf[page, :, row, 64:] = nan
+    c["k"], c["v"] = kf.to(DT[kv]), vf.to(DT[kv])
+    out, lse = (x.double().cpu() for x in run(msa, c))
+    ref, rl, size = tree_attention(c["q"], c["k"].float(), c["v"].float(), c["q2k"], c["cu"], c["mask"], c["table"], c["used"], SCALE)
+    finite = ref.isfinite()
+    assert not finite.all() and (finite.any() or max(lens) == 1)
+    assert torch.equal(out.isnan(), ref.isnan()) and torch.equal(out.isinf(), ref.isinf()) and torch.equal(lse.isnan(), rl.isnan())
+    assert torch.equal(out[ref.isinf()], ref[ref.isinf()])
+    tol = half_step(c["q"].dtype) * (size + ref.abs()) * 1.01 + 2.0**-13 * size
+    if kv == "fp16":
+        tol += topk * 128 * 2.0**-25 * 6 + 2.0**-25
+    assert ((out - ref).abs() <= tol)[finite].all()
+    ok = rl.isfinite()
+    assert ((lse - rl).abs()[ok] <= 2.0**-13 + rl.abs()[ok] * 2.0**-21).all()
+
+
+GROWN = [
+    ([9, 17], [1000, 640], 32, 2, 7, "fp16"),
+    ([33, 64], [1290, 900], 16, 2, 9, "bf16"),
+    ([5, 1, 12], [1200, 900, 640], 16, 2, 8, "e4m3"),
+    ([20], [5000], 32, 2, 36, "bf16"),
+    ([70], [3000], 16, 2, 20, "e4m3"),
+    # lists of the greatest length, 128 tokens a tile and one
+    ([30], [9000], 2, 2, 64, "bf16"),
+    ([3], [9000], 128, 1, 64, "fp16"),
+]
+
+
+@pytest.mark.parametrize("down", [False, True])
+@pytest.mark.parametrize("lens,used,hq,hkv,topk,kv", GROWN)
+def test_logits_that_grow_and_fall(msa, lens, used, hq, hkv, topk, kv, down):
+    """Keys that grow with their place, so that the running maximum moves from half a block to the next (or never after the
+    first), with a row of Q of zeros and one below every normal f16. The logits' error grows with L = max sum |q k| scale: 128 roundings of 2^-24
+    of the sum, and three of the exponent's argument, below 2 L log2(e): a probability is off by 2 (2^-17 + 9 2^-24) L < 2^-15.8 L
+    over numerator and denominator."""
+    c = make(lens, used, hq, hkv, topk, kv, seed=9, garbage=False)
+    kf = c["k"].float()
+    for b, n in enumerate(used):
+        for i in range((n + 127) // 128):
+            at = (torch.arange(128) + 128 * i) / n
+            kf[c["table"][b, i]] *= (6 * (1 - at if down else at)).clamp(min=0)[None, :, None]
+    c["k"] = kf.to(DT[kv])
+    c["q"][0] = 0
+    c["q"][1] *= 2.0**-24 if kv == "fp16" else 2.0**-60
+    out, lse = (x.double().cpu() for x in run(msa, c))
+    ref, rl, size = tree_attention(c["q"], c["k"].float(), c["v"].float(), c["q2k"], c["cu"], c["mask"], c["table"], c["used"], SCALE)
+    big = max((c["q"].float().abs().reshape(-1, hkv, hq // hkv, 128).amax(2)[:, h] @ c["k"].float()[:, h].abs().reshape(-1, 128).T).max().item() for h in range(hkv)) * SCALE
+    off = 2.0**-15.8 * big
+    tol = half_step(c["q"].dtype) * (size + ref.abs()) * 1.01 + off * size
+    if kv == "fp16":
+        tol += topk * 128 * 2.0**-25 * 6 + 2.0**-25
+    bad = (out - ref).abs() > tol
+    assert not bad.any(), (int(bad.sum()), ((out - ref).abs() / tol.clamp(min=1e-30)).max().item())
+    assert ((lse - rl).abs() <= off + rl.abs() * 2.0**-21 + 2.0**-20).all()
