@@ -30,6 +30,8 @@ __global__ void __launch_bounds__(kAcceptThreads)
                         const __grid_constant__ CacheAcceptArgs a) {
   __shared__ long long s_src[kAcceptChunk], s_dst[kAcceptChunk];  // row offsets; -1: no move
   __shared__ int s_len;
+  grid_dependency_wait();
+  grid_dependents_launch();
   const int b = blockIdx.y;
   const int lq = __ldg(a.cu_q + b + 1) - __ldg(a.cu_q + b);
   const int lk = __ldg(a.seqused_k + b);
@@ -91,6 +93,8 @@ __global__ void __launch_bounds__(kAcceptThreads)
 constexpr int kFreeThreads = 256;
 
 __global__ void __launch_bounds__(kFreeThreads) cache_free_kernel(const __grid_constant__ CacheTableArgs a) {
+  grid_dependency_wait();
+  grid_dependents_launch();
   const int i = blockIdx.x;
   const int r = __ldg(a.rows + i);
   if (r < 0 || r >= a.num_rows) return;
@@ -149,6 +153,7 @@ MSA_DEV int block_exclusive(int v, int* s, int& total) {
 // tables here, forks by the kernel after this one.
 template <bool FORK>
 __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_constant__ CacheTableArgs a) {
+  grid_dependency_wait();
   grid_dependents_launch();
   extern __shared__ int smem[];
   int* claim = smem;                   // num_rows: the first request for the row
@@ -322,7 +327,8 @@ MSA_DEV void copy_chunk(const uint8_t* src, uint8_t* dst, long long bytes) {
 __global__ void __launch_bounds__(kCopyThreads)
     cache_fork_kernel(const __grid_constant__ CachePools pools, int num_pools, long long page_bytes,
                       const __grid_constant__ CacheTableArgs a) {
-  grid_dependency_wait();  // the plan
+  grid_dependency_wait();
+  grid_dependents_launch();
   const int i = blockIdx.z;
   const int page = a.plan[i];
   const int src = a.src_rows[i];
@@ -359,6 +365,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 __global__ void __launch_bounds__(kCopyThreads)
     cache_copy_kernel(const __grid_constant__ CachePools pools, long long page_bytes, int num_pages,
                       const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n) {
+  grid_dependency_wait();
+  grid_dependents_launch();
   const int i = blockIdx.z;
   const int from = __ldg(src + i), to = __ldg(dst + i);
   if (from < 0 || from >= num_pages || to < 0 || to >= num_pages || from == to) return;
@@ -383,21 +391,19 @@ cudaError_t launch_plan(const CacheTableArgs& a, cudaStream_t s) {
   const int bytes = (a.num_rows + 2 * a.n + 33) * (int)sizeof(int);
   const cudaError_t e = set_smem_limit((const void*)cache_plan_kernel<FORK>, bytes);
   if (e != cudaSuccess) return e;
-  cache_plan_kernel<FORK><<<1, kPlanThreads, bytes, s>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(cache_plan_kernel<FORK>, dim3(1), kPlanThreads, bytes, s, a);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_accept(const CachePools& p, const CacheAcceptArgs& a, cudaStream_t s) {
   const int columns = a.num_pools * a.hkv * (a.row_bytes / 16);
-  cache_accept_kernel<<<dim3((columns + kAcceptThreads - 1) / kAcceptThreads, a.batch), kAcceptThreads, 0, s>>>(p, a);
-  return cudaGetLastError();
+  return launch_dependent(cache_accept_kernel, dim3((columns + kAcceptThreads - 1) / kAcceptThreads, a.batch),
+                          kAcceptThreads, 0, s, p, a);
 }
 
 cudaError_t launch_cache_free(const CacheTableArgs& a, cudaStream_t s) {
-  cache_free_kernel<<<a.n, kFreeThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(cache_free_kernel, dim3(a.n), kFreeThreads, 0, s, a);
 }
 
 cudaError_t launch_cache_extend(const CacheTableArgs& a, cudaStream_t s) { return launch_plan<false>(a, s); }
@@ -406,23 +412,15 @@ cudaError_t launch_cache_fork(const CacheTableArgs& a, cudaStream_t s) { return 
 
 cudaError_t launch_cache_fork_copy(const CachePools& p, int num_pools, long long page_bytes, bool tables,
                                    const CacheTableArgs& a, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = copy_grid(num_pools + (tables ? 1 : 0), page_bytes, a.n);
-  cfg.blockDim = dim3(kCopyThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = tables ? 1 : 0;  // right behind the plan
-  return cudaLaunchKernelEx(&cfg, cache_fork_kernel, p, num_pools, page_bytes, a);
+  return launch_dependent(cache_fork_kernel, copy_grid(num_pools + (tables ? 1 : 0), page_bytes, a.n), kCopyThreads, 0,
+                          s, p, num_pools, page_bytes, a);
 }
 
 cudaError_t launch_cache_copy_pages(const CachePools& p, int num_pools, long long page_bytes,
                                     int num_pages, const int32_t* src, const int32_t* dst, int n,
                                     cudaStream_t s) {
-  cache_copy_kernel<<<copy_grid(num_pools, page_bytes, n), kCopyThreads, 0, s>>>(p, page_bytes, num_pages, src, dst, n);
-  return cudaGetLastError();
+  return launch_dependent(cache_copy_kernel, copy_grid(num_pools, page_bytes, n), kCopyThreads, 0, s, p, page_bytes,
+                          num_pages, src, dst, n);
 }
 
 }  // namespace msa

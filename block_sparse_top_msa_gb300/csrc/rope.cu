@@ -168,6 +168,8 @@ MSA_DEV int cache_page(const RopeArgs& a, int l, int t, bool live, int& row) {
 // row's loads issued before the first is used.
 template <bool F16, bool ADJ, int KV, int R>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  grid_dependency_wait();
+  grid_dependents_launch();
   const int l = threadIdx.x % kTeam;
   const unsigned cq = (a.hq + R - 1) / R, ck = (a.hkv + R - 1) / R;
   const unsigned id = blockIdx.x * kTeams + threadIdx.x / kTeam;
@@ -269,6 +271,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 // partial sums, summed over its teams in a fixed order.
 template <bool F16, bool ADJ, int R>
 __global__ void __launch_bounds__(kThreads, kBwdResident) rope_bwd_kernel(const __grid_constant__ RopeBwdArgs a) {
+  grid_dependency_wait();
+  grid_dependents_launch();
   const int l = threadIdx.x % kTeam, team = threadIdx.x / kTeam;
   const bool kside = (int)blockIdx.x >= a.q_blocks;
   const int heads = kside ? a.hkv : a.hq;
@@ -370,6 +374,8 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) rope_bwd_kernel(const 
 // group of 32), 32 rows of threads each taking every 32nd partial, then those
 // 32 sums one after the other.
 __global__ void __launch_bounds__(1024) rope_bwd_sum_kernel(const __grid_constant__ RopeBwdArgs a, int blocks) {
+  grid_dependency_wait();
+  grid_dependents_launch();
   const bool kside = blockIdx.x >= 4;
   const int col = (blockIdx.x & 3) * 32 + (threadIdx.x & 31), g = threadIdx.x >> 5;
   const int first = kside ? a.q_blocks : 0, last = kside ? blocks : a.q_blocks;
@@ -398,17 +404,17 @@ cudaError_t launch_rope_r(const RopeArgs& a, cudaStream_t s) {
   constexpr int R = KV ? kAppendRows : kFwdRows;
   const long long per_token = (a.hq + R - 1) / R + (KV ? 2 : 1) * (long long)((a.hkv + R - 1) / R);
   const long long teams = (long long)a.tokens * per_token;
-  rope_kernel<F16, ADJ, KV, R><<<(unsigned)((teams + kTeams - 1) / kTeams), kThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(rope_kernel<F16, ADJ, KV, R>, dim3((unsigned)((teams + kTeams - 1) / kTeams)), kThreads, 0, s,
+                          a);
 }
 template <bool F16, int KV>
 cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t s) {
   return a.interleaved ? launch_rope_r<F16, true, KV>(a, s) : launch_rope_r<F16, false, KV>(a, s);
 }
 template <bool F16>
-void launch_rope_bwd_t(const RopeBwdArgs& a, int blocks, cudaStream_t s) {
-  if (a.interleaved) rope_bwd_kernel<F16, true, kBwdRows><<<blocks, kThreads, 0, s>>>(a);
-  else rope_bwd_kernel<F16, false, kBwdRows><<<blocks, kThreads, 0, s>>>(a);
+cudaError_t launch_rope_bwd_t(const RopeBwdArgs& a, int blocks, cudaStream_t s) {
+  return launch_dependent(a.interleaved ? rope_bwd_kernel<F16, true, kBwdRows> : rope_bwd_kernel<F16, false, kBwdRows>,
+                          dim3(blocks), kThreads, 0, s, a);
 }
 
 }  // namespace
@@ -437,13 +443,10 @@ RopeBwdGrid rope_bwd_grid(long long tokens, int hq, int hkv) {
 cudaError_t launch_rope_bwd(const RopeBwdArgs& a, int k_blocks, cudaStream_t s) {
   const int blocks = a.q_blocks + k_blocks;
   if (blocks > 0) {
-    if (a.f16) launch_rope_bwd_t<true>(a, blocks, s);
-    else launch_rope_bwd_t<false>(a, blocks, s);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = a.f16 ? launch_rope_bwd_t<true>(a, blocks, s) : launch_rope_bwd_t<false>(a, blocks, s);
     if (e != cudaSuccess) return e;
   }
-  rope_bwd_sum_kernel<<<8, 1024, 0, s>>>(a, blocks);
-  return cudaGetLastError();
+  return launch_dependent(rope_bwd_sum_kernel, dim3(8), 1024, 0, s, a, blocks);
 }
 
 }  // namespace msa

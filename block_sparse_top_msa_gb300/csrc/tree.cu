@@ -285,6 +285,7 @@ __global__ void __launch_bounds__(kUnionThreads) tree_union_kernel(const __grid_
   const int tile = blockIdx.x, h = blockIdx.y, unit = tile * a.num_kv_heads + h;
   __shared__ int s_warp[kUnionThreads / 32];
   __shared__ int s_b, s_t0;
+  grid_dependency_wait();
   grid_dependents_launch();
   if (tid == 0) {
     s_b = -1;
@@ -1466,21 +1467,6 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
 }
 
-template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <bool FP8, bool F16>
 cudaError_t launch_t(const TreeArgs& a, cudaStream_t s) {
   const int optin = device_smem_optin();
@@ -1503,8 +1489,7 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s) {
   const int smem = (int)sizeof(uint32_t) * (2 * maps + a.unit_tokens * a.words);
   cudaError_t e = set_smem_limit((const void*)tree_union_kernel, smem);
   if (e != cudaSuccess) return e;
-  tree_union_kernel<<<dim3(a.max_tiles, a.num_kv_heads), kUnionThreads, smem, s>>>(a);
-  e = cudaGetLastError();
+  e = launch_dependent(tree_union_kernel, dim3(a.max_tiles, a.num_kv_heads), kUnionThreads, smem, s, a);
   if (e != cudaSuccess) return e;
   if (a.e4m3) return launch_t<true, false>(a, s);
   return a.f16 ? launch_t<false, true>(a, s) : launch_t<false, false>(a, s);
