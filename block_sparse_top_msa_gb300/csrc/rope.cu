@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, kBwdResident) rope_bwd_kernel(const 
     for (int i = 0; i < R; ++i) {
       const Own f = unpack<F16, ADJ>(rx[i][0], rx[i][1], at.adj);
       const float r = rsqrtf(ss[i] * (1.f / kHeadDim) + a.eps);
-      const float k = -r * r * r * dot[i] * (1.f / kHeadDim);
+      const float k = -(r * dot[i]) * r * r * (1.f / kHeadDim);  // a row of zeros has dot 0, however large r
       if (known && i < n) {
         const Own fr = scaled(f, r);
         dw = {fma2(v[i].a0, fr.a0, dw.a0), fma2(v[i].a1, fr.a1, dw.a1), fma2(v[i].b0, fr.b0, dw.b0),

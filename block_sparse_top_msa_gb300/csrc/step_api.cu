@@ -257,6 +257,10 @@ msa_status_t msa_cache_accept(void* const* pools, int num_pools, int row_bytes, 
       !aligned(path_len, 4) || !aligned(seqused_out, 4) || seqused_out == seqused_k)
     return MSA_INVALID_ARG;
   if (batch > kMaxCacheRows || num_kv_heads > 1024 || row_bytes > 4096) return MSA_UNSUPPORTED;
+  // A pool's rows move once: a pool given twice would read moved rows.
+  for (int i = 1; i < num_pools; ++i)
+    for (int j = 0; j < i; ++j)
+      if (pools[i] == pools[j]) return MSA_INVALID_ARG;
   CacheAcceptArgs a{};
   a.row_bytes = row_bytes, a.hkv = num_kv_heads;
   a.page_table = page_table, a.max_pages = max_pages, a.num_pages = num_pages, a.batch = batch;

@@ -242,8 +242,9 @@ msa_status_t msa_sparse_attention_nvfp4_prepare(
  *               past 32 * mask_words are not seen
  *   workspace   msa_tree_attention_workspace_size(...) bytes, 256-byte aligned,
  *               uninitialised; calls that share one must be ordered on the device
- * K and V of the keys below seqused_k have to be finite; what the pages hold
- * past them does not matter. A NULL or misaligned tree_mask, a NULL
+ * What a token does not see may hold anything, infinities and NaN included:
+ * rows past seqused_k, blocks that it does not list, other drafts. A token
+ * that sees a NaN gets NaN. A NULL or misaligned tree_mask, a NULL
  * page_table or too few words: MSA_INVALID_ARG; max_pages above 2^18:
  * MSA_UNSUPPORTED; otherwise as the forward.
  * msa_tree_attention_prepare binds the call into a plan that
@@ -382,8 +383,9 @@ msa_status_t msa_qk_norm_rope_bwd(
  *   are not moved. Pools are (num_pages, Hkv, 128, row_bytes) with row_bytes a
  *   multiple of 16 (256 for 16-bit and 128 for E4M3 caches of head_dim 128;
  *   planar NVFP4 pages are not made of rows and cannot be given here).
- *   seqused_out is another array than seqused_k. The request's last pages must
- *   be its own (as extend and fork leave them).
+ *   seqused_out is another array than seqused_k, and no pool is given twice
+ *   (MSA_INVALID_ARG). The request's last pages must be its own (as extend and
+ *   fork leave them).
  * workspace of msa_cache_fork and msa_cache_extend: as their size query says,
  * 256-byte aligned, uninitialised; calls that share one, or the same tables,
  * must be ordered on the device. MSA_INVALID_ARG for a NULL or misaligned

@@ -229,3 +229,22 @@ def test_captured_and_on_another_stream(msa):
     want, grads_want = msa.msa_qk_norm_rope(*a), msa.msa_qk_norm_rope_bwd(*d, *a)
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(again + grads, want + grads_want))
+
+
+def test_rows_of_zeros_and_a_tiny_eps(msa):
+    """r = eps^(-1/2) is 2^50 for a row of zeros, r^3 beyond float32: the gradient is r g all the same."""
+    x, q, k, v, w, table, pos = inputs(6, 4, 2, 64, "bf16")
+    eps, pos = 2.0**-100, pos.clamp(0, 49)
+    x[2] = 0
+    x[4, 1] = 0
+    gq, gk, _ = on_gpu(x, 4, 2, True)
+    dq, dk = (torch.randn(6, n, 128, generator=torch.Generator().manual_seed(n)).to(torch.bfloat16) for n in (4, 2))
+    args = gq, gk, w[0].to(DEV), w[1].to(DEV), gpu(table), pos.to(DEV)
+    oq, ok = msa.msa_qk_norm_rope(*args, eps=eps)
+    gdq, gdk, gwq, gwk = msa.msa_qk_norm_rope_bwd(dq.to(DEV), dk.to(DEV), *args, eps=eps)
+    for y, src, wt, dx, dy, dw in ((oq, q, w[0], gdq, dq, gwq), (ok, k, w[1], gdk, dk, gwk)):
+        ref, mag = norm_rope(src, wt, table, pos, False, eps)
+        near(y, ref, mag, torch.bfloat16, CHAIN)
+        rx, xm, rw, wm = norm_rope_bwd(src, wt, dy, table, pos, False, eps)
+        near(dx, rx, xm, torch.bfloat16, CHAIN_BWD)
+        assert ((dw.double().cpu() - rw).abs() <= SUMS * wm).all()

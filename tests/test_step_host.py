@@ -132,3 +132,9 @@ def test_binding_refuses_before_the_library():
         msa.msa_cache_copy_pages([], pos, pos)
     with pytest.raises(ValueError):
         msa.msa_tree_attention(x, x, x, pos, pos, pos, page_table=pos, seqused_k=pos)
+
+
+def test_accept_refuses_a_pool_given_twice(L):
+    names = "pools n row hkv pt mp np b su cu path len most out s".split()
+    good = dict(pools=(C.c_void_p * 3)(0x10000, 0x20000, 0x10000), n=3, row=256, hkv=2, pt=P, mp=1, np=1, b=1, su=P, cu=P, path=P, len=P, most=1, out=C.c_void_p(0x30000), s=None)
+    assert call(L.msa_cache_accept, names, good) == INVALID
