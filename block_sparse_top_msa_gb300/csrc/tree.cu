@@ -1057,9 +1057,13 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         const bool warp_hides = __any_sync(0xffffffffu, hides);
         if (!FP8 && tail < 128 && (st == 0 || !s.dual)) {
           // V rows past the end, before the first PV that reads the block (in
-          // a unit of two tiles stream 0's, which is issued first).
+          // a unit of two tiles stream 0's, which is issued first). The wait
+          // for the slot's phase needs the phase before it complete: V of the
+          // block kVSlots earlier is, once this block's S is, whose product
+          // is issued behind the PV of the block two earlier.
           const int g = g0 + j, vs = g % kVSlots;
-          ok = wait_on(&sm.v_full[vs], (g / kVSlots) & 1, fault, kFaultWaitTma, abort);
+          ok = wait_on(&sm.qk_done[st][0], nqk & 1, fault, kFaultWaitMma, abort) &&
+               wait_on(&sm.v_full[vs], (g / kVSlots) & 1, fault, kFaultWaitTma, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           for (int i = tail * 16 + row; i < 128 * 16; i += 128)

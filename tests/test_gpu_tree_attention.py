@@ -298,3 +298,22 @@ def test_logits_that_grow_and_fall(msa, lens, used, hq, hkv, topk, kv, down):
     bad = (out - ref).abs() > tol
     assert not bad.any(), (int(bad.sum()), ((out - ref).abs() / tol.clamp(min=1e-30)).max().item())
     assert ((lse - rl).abs() <= off + rl.abs() * 2.0**-21 + 2.0**-20).all()
+
+
+@pytest.mark.parametrize("kv,hq,hkv", [("fp16", 40, 4), ("bf16", 64, 4), ("e4m3", 32, 2)])
+def test_slow_caches_change_nothing(msa, kv, hq, hkv):
+    """Long lists read from memory and not from L2, so that blocks arrive later than their place in the pipeline: the bits of a
+    call whose caches are warm, in units of one tile and of two."""
+    lens = [4 + (7 * i) % 13 for i in range(24)]
+    used = [2200 + 61 * i for i in range(24)]
+    c = make(lens, used, hq, hkv, 16, kv, seed=3)
+    warm = run(msa, c)
+    check(c, *warm)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    d = {n: t.to(DEV) for n, t in c.items()}
+    for i in range(6):
+        flush.fill_(i)
+        out, lse = msa.msa_tree_attention(d["q"], d["k"], d["v"], d["q2k"], d["cu"], d["mask"], page_table=d["table"], seqused_k=d["used"],
+                                          max_seqlen_q=max(lens), return_softmax_lse=True)
+        assert torch.equal(out, warm[0]) and torch.equal(lse, warm[1])
+    fault_clear(msa)
