@@ -386,7 +386,7 @@ def _own(s):
         q, k, _ = _split(s)
         return dict(zip(("q", "k", "wq", "wk"), msa.msa_qk_norm_rope_bwd(s["dq"], s["dk"], q, k, s["wq"], s["wk"], s["cos_sin"], s["positions"], **rope)))
     if s["op"] == "tree":
-        return dict(zip(("out", "lse"), msa.msa_tree_attention(s["q"], s["k"], s["v"], s["lists"], s["cu"], s["mask"], page_table=s["table"], seqused_k=s["used"], max_seqlen_q=s["nq_hi"],
+        return dict(zip(("out", "lse"), msa.msa_tree_attention(s["q"], s["k"], s["v"], s["lists"], s["cu"], s["mask"], page_table=s["table"], seqused_k=s["used"], max_seqlen_q=min(s["nq_hi"], 32 * s["mask"].shape[1]),
                                                               return_softmax_lse=True)))
     if s["op"] == "fork":
         msa.msa_cache_free(s["table"], s["used"], s["refs"], s["dst"])
