@@ -4,19 +4,28 @@
 // tokens fill the 128 rows of an MMA tile) with one KV head; it attends over
 // the union of its tokens' listed blocks, each row to its own blocks and to
 // the drafts its mask names. Drafts of one request choose much the same
-// blocks, so a block is brought to shared memory once for both tiles: against
-// one tile per unit that halves the cache traffic and the E4M3 conversions.
+// blocks, so a block is brought to shared memory once for both tiles: that
+// halves the cache traffic and the E4M3 conversions (units of one tile: 84 us
+// against 73 for 32 requests of 16 tokens with 64 query heads, 4 KV heads and
+// 16 listed blocks, 376 against 351 for 128 E4M3 requests of 8 to 32 tokens;
+// the figures below are of these two).
 //
 // The units' blocks, laid end to end, are cut into equal ranges, one per CTA
 // (one CTA per SM): a CTA works through the segments its range cuts out of
 // the units. A segment that is a whole unit writes its output, the others
 // leave (m, l, O) partials that merge_tree_kernel joins. Where whole units
 // load the CTAs nearly as evenly (within cut_cost blocks), a unit goes whole
-// to the CTA whose range it begins in: partials and their joining took 20 us
-// of the 87 that 32 requests of 16 tokens (64 query heads, 4 KV heads, top 16)
-// took with ranges cut. The unions' lengths are known on the device only:
-// every CTA sums them (tree_union_kernel leaves one per unit), comes to the
-// same choice and finds its own range.
+// to the CTA whose range it begins in: the 32 requests take 73 us so, and 89
+// with ranges cut. The unions' lengths are known on the device only: every CTA
+// sums them (tree_union_kernel leaves one per unit), comes to the same choice
+// and finds its own range.
+//
+// What bounds it: neither memory nor the tensor cores alone (their work on the
+// unions is 132 us of the 351, on the 32 requests 27 of the 73, where random
+// pages take 42), but a block's chain of products and softmax by two streams
+// of four warps, and the issue slots these share with the decoding: a block
+// of two tiles takes 4300 clocks, its products 2350. Waits are by
+// mbar_wait_sleep, as spinning takes issue slots too (354 us).
 //
 // Two streams of (QK^T, softmax, PV) keep the tensor cores busy: while one
 // stream's softmax warps turn its S into P, the other's products run. With
@@ -32,9 +41,7 @@
 // shared memory, as P = 0 times what a page may hold there need not be 0.
 //
 // E4M3 is decoded to f16, exactly, NaN codes included, by one conversion a
-// pair (moving the bits by integer instructions: 372 us against 352 for 128
-// requests; on to bf16, two more conversions a pair: 646 in the kernel before
-// this one). Q then is f16 too, each bf16 row scaled by the power of two that
+// pair (moving the bits by integer instructions: 372 us against 352). Q then is f16 too, each bf16 row scaled by the power of two that
 // puts its largest value just below f16's largest (what falls below f16's
 // range is under 2^-39 of that); the power of two comes back with the softmax
 // scale.
@@ -117,27 +124,6 @@ struct __align__(1024) Smem {
   int abort;
 };
 
-// mbar_wait of common.cuh with its limit kept in SM clocks: reading the global
-// timer, as that does once a first test fails, takes longer than most waits
-// here.
-constexpr long long kWaitLimitClocks = 4000000000ll;  // about 2 s
-MSA_DEV bool wait_on(uint64_t* bar, uint32_t parity, unsigned* fault, unsigned code,
-                     volatile int* abort = nullptr) {
-  if (mbar_test(bar, parity)) return true;
-  const long long t0 = clock64();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_test(bar, parity)) return true;
-    if (abort != nullptr && *abort) return false;
-    if (clock64() - t0 > kWaitLimitClocks) {
-      if (fault) atomicOr(fault, code);
-      if (abort) *abort = 1;
-      return false;
-    }
-  }
-}
-
 // The partition of [0, total) into the CTAs' ranges.
 struct Ranges {
   long long total;
@@ -157,8 +143,8 @@ MSA_DEV int first_block(long long p0, long long c, int w, int len) {
 }
 
 // What a block costs a CTA, by the unit's tiles: bringing and decoding it is
-// the same, but two tiles multiply twice (4500 clocks against 3300 with E4M3,
-// about as much apart with 16-bit caches).
+// the same, but two tiles multiply twice (128 E4M3 requests: 351 us with 3 to
+// 4, 366 with equal weights, 365 with 2 to 4).
 constexpr int kOneTileWeight = 3, kTwoTileWeight = 4;
 MSA_DEV int unit_weight(const TreeArgs& a, int tokens) {
   return tokens > a.tile_tokens ? kTwoTileWeight : kOneTileWeight;
@@ -534,7 +520,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
   // The n-th segment of this CTA; false at the end (or when a wait gave up).
   auto read_seg = [&](int n, Segment& s) -> bool {
     const int slot = n % kSegRing;
-    if (!wait_on(&sm.seg_full[slot], (n / kSegRing) & 1, fault, kFaultWaitOther, abort)) {
+    if (!mbar_wait_sleep(&sm.seg_full[slot], (n / kSegRing) & 1, fault, kFaultWaitOther, abort)) {
       s.unit = -2;
       return false;
     }
@@ -557,7 +543,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     auto publish = [&](const Segment& s) {
       const int slot = n_pub % kSegRing;
       if (n_pub >= kSegRing &&
-          !wait_on(&sm.seg_empty[slot], ((n_pub / kSegRing) - 1) & 1, fault, kFaultWaitOther, abort)) {
+          !mbar_wait_sleep(&sm.seg_empty[slot], ((n_pub / kSegRing) - 1) & 1, fault, kFaultWaitOther, abort)) {
         ok = false;
         return;
       }
@@ -567,7 +553,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     };
     auto load_q = [&]() {
       if (!ok || pend.unit < 0) return;
-      if (n_q > 0 && !wait_on(&sm.q_empty, (n_q - 1) & 1, fault, kFaultWaitMma, abort)) {
+      if (n_q > 0 && !mbar_wait_sleep(&sm.q_empty, (n_q - 1) & 1, fault, kFaultWaitMma, abort)) {
         ok = false;
         return;
       }
@@ -643,7 +629,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       }
       a.cut[cta] = make_int2(cut_unit, head_unit);
       // A copy in flight lands before the CTA's shared memory is given back.
-      if (!ok && q_flight) wait_on(&sm.q_full, (n_q - 1) & 1, fault, kFaultWaitTma);
+      if (!ok && q_flight) mbar_wait_sleep(&sm.q_full, (n_q - 1) & 1, fault, kFaultWaitTma);
     }
   } else if (warp == R::kMma) {
     // -------------------------------------------------------------- MMA issue
@@ -666,7 +652,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     int nseg = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase, unsigned code) {
-      ok = ok && wait_on(bar, phase, fault, code, abort);
+      ok = ok && mbar_wait_sleep(bar, phase, fault, code, abort);
     };
     auto commit = [&](uint64_t* bar) { commit_if(el, bar); };
     // S of stream st = tile `tile` of Q times K, for the block's 64-key half h.
@@ -754,7 +740,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       ++nseg;
     }
     commit(&sm.drain);
-    wait_on(&sm.drain, 0, fault, kFaultWaitMma);
+    mbar_wait_sleep(&sm.drain, 0, fault, kFaultWaitMma);
     __syncwarp();
   } else if (warp == R::kKv) {
     // ---------------------------------------------------------------- K and V
@@ -816,7 +802,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       // Waits until the tile's slot may be written.
       auto slot_free = [&](const Tile& t) -> bool {
         const int ring = t.is_v ? kVSlots : kKSlots, slot = t.g % ring, round = t.g / ring;
-        return round == 0 || wait_on(t.is_v ? &sm.v_empty[slot] : &sm.k_empty[slot], (round - 1) & 1, fault,
+        return round == 0 || mbar_wait_sleep(t.is_v ? &sm.v_empty[slot] : &sm.k_empty[slot], (round - 1) & 1, fault,
                                      kFaultWaitMma, abort);
       };
       int last_k[kKSlots], last_v[kVSlots];  // last block issued into each slot
@@ -845,9 +831,9 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       }
       if (!ok && lane == 0) {
         for (int i = 0; i < kKSlots; ++i)
-          if (last_k[i] >= 0) wait_on(&sm.k_full[i], (last_k[i] / kKSlots) & 1, fault, kFaultWaitTma);
+          if (last_k[i] >= 0) mbar_wait_sleep(&sm.k_full[i], (last_k[i] / kKSlots) & 1, fault, kFaultWaitTma);
         for (int i = 0; i < kVSlots; ++i)
-          if (last_v[i] >= 0) wait_on(&sm.v_full[i], (last_v[i] / kVSlots) & 1, fault, kFaultWaitTma);
+          if (last_v[i] >= 0) mbar_wait_sleep(&sm.v_full[i], (last_v[i] / kVSlots) & 1, fault, kFaultWaitTma);
       }
     } else {
       // E4M3: the blocks as they are into the raw ring, 16 KB of contiguous
@@ -856,7 +842,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       auto put = [&](const RawTile& r, const uint8_t* src) -> bool {
         const int slot = y % kRawSlots;
         if (y >= kRawSlots &&
-            !wait_on(&sm.raw_empty[slot], ((y / kRawSlots) - 1) & 1, fault, kFaultWaitOther, abort))
+            !mbar_wait_sleep(&sm.raw_empty[slot], ((y / kRawSlots) - 1) & 1, fault, kFaultWaitOther, abort))
           return false;
         sm.raw_tile[slot] = r;
         if (r.rows > 0) {
@@ -887,7 +873,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         // Copies in flight land before the CTA's shared memory is given back.
         if (!ok)
           for (int i = y < kRawSlots ? 0 : y - kRawSlots; i < y; ++i)
-            wait_on(&sm.raw_full[i % kRawSlots], (i / kRawSlots) & 1, fault, kFaultWaitTma);
+            mbar_wait_sleep(&sm.raw_full[i % kRawSlots], (i / kRawSlots) & 1, fault, kFaultWaitTma);
       }
     }
   } else if (FP8 && warp >= R::kDecode) {
@@ -903,7 +889,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     bool ok = true;
     for (int y = 0;; ++y) {
       const int rs = y % kRawSlots;
-      ok = wait_on(&sm.raw_full[rs], (y / kRawSlots) & 1, fault, kFaultWaitTma, abort);
+      ok = mbar_wait_sleep(&sm.raw_full[rs], (y / kRawSlots) & 1, fault, kFaultWaitTma, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const RawTile t = sm.raw_tile[rs];
@@ -917,7 +903,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       if (lane == 0) mbar_arrive(&sm.raw_empty[rs]);
       if (t.g < 0) break;
       const int ring = t.is_v ? kVSlots : kKSlots, slot = t.g % ring, round = t.g / ring;
-      ok = round == 0 || wait_on(t.is_v ? &sm.v_empty[slot] : &sm.k_empty[slot], (round - 1) & 1, fault,
+      ok = round == 0 || mbar_wait_sleep(t.is_v ? &sm.v_empty[slot] : &sm.k_empty[slot], (round - 1) & 1, fault,
                                  kFaultWaitMma, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -979,7 +965,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       if constexpr (FP8) {
         if (s.dual || st == 0) {
           // The row of Q, in place: bf16 to f16 times 2^k.
-          ok = wait_on(&sm.q_full, nseg & 1, fault, kFaultWaitTma, abort);
+          ok = mbar_wait_sleep(&sm.q_full, nseg & 1, fault, kFaultWaitTma, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           uint8_t* qt = &sm.q[s.dual ? st : 0][0][0];
@@ -1012,7 +998,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         }
         if (lane == 0) mbar_arrive(&sm.q_ready);
         if (!s.dual && st == 1) {
-          ok = wait_on(&sm.q_ready, nseg & 1, fault, kFaultWaitSoftmax, abort);
+          ok = mbar_wait_sleep(&sm.q_ready, nseg & 1, fault, kFaultWaitSoftmax, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           scale = sm.q_scale[row];
@@ -1062,8 +1048,8 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           // block kVSlots earlier is, once this block's S is, whose product
           // is issued behind the PV of the block two earlier.
           const int g = g0 + j, vs = g % kVSlots;
-          ok = wait_on(&sm.qk_done[st][0], nqk & 1, fault, kFaultWaitMma, abort) &&
-               wait_on(&sm.v_full[vs], (g / kVSlots) & 1, fault, kFaultWaitTma, abort);
+          ok = mbar_wait_sleep(&sm.qk_done[st][0], nqk & 1, fault, kFaultWaitMma, abort) &&
+               mbar_wait_sleep(&sm.v_full[vs], (g / kVSlots) & 1, fault, kFaultWaitTma, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           for (int i = tail * 16 + row; i < 128 * 16; i += 128)
@@ -1075,7 +1061,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         for (int half = 0; half < 2; ++half) {
           const uint32_t vis0 = half == 0 ? vis[0] : vis[2], vis1 = half == 0 ? vis[1] : vis[3];
           const uint32_t hcol = scol + half * 64;  // P over the first half of its own S
-          ok = wait_on(&sm.qk_done[st][half], nqk & 1, fault, kFaultWaitMma, abort);
+          ok = mbar_wait_sleep(&sm.qk_done[st][half], nqk & 1, fault, kFaultWaitMma, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -1110,7 +1096,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
               // O has to hold the half before (the second halves' PVs complete
               // odd phases of pv_done, the first halves' even ones); the half
               // before that is complete, as this S was issued after it.
-              ok = wait_on(&sm.pv_done[st], half ^ 1, fault, kFaultWaitMma, abort);
+              ok = mbar_wait_sleep(&sm.pv_done[st], half ^ 1, fault, kFaultWaitMma, abort);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               tc_fence_after();
@@ -1166,7 +1152,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         if (st == 1) {
           // Stream 0's warps join the two.
           if (nml > 0)
-            ok = wait_on(&sm.ml_empty, (nml - 1) & 1, fault, kFaultWaitSoftmax, abort);
+            ok = mbar_wait_sleep(&sm.ml_empty, (nml - 1) & 1, fault, kFaultWaitSoftmax, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           ++nml;
@@ -1177,7 +1163,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           if (lane == 0) mbar_arrive(&sm.ml_full);
           continue;
         }
-        ok = wait_on(&sm.ml_full, nml & 1, fault, kFaultWaitSoftmax, abort);
+        ok = mbar_wait_sleep(&sm.ml_full, nml & 1, fault, kFaultWaitSoftmax, abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++nml;
@@ -1190,14 +1176,14 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         l = f[0] * l + f[1] * other.y;
         m_ref = m;
         from[1] = lanes + kColO + 128;
-        ok = wait_on(&sm.o_done[0], no[0] & 1, fault, kFaultWaitMma, abort);
+        ok = mbar_wait_sleep(&sm.o_done[0], no[0] & 1, fault, kFaultWaitMma, abort);
         ++no[0];
         if (ok && n > 1) {
-          ok = wait_on(&sm.o_done[1], no[1] & 1, fault, kFaultWaitMma, abort);
+          ok = mbar_wait_sleep(&sm.o_done[1], no[1] & 1, fault, kFaultWaitMma, abort);
           ++no[1];
         }
       } else {
-        ok = wait_on(&sm.o_done[st], no[st] & 1, fault, kFaultWaitMma, abort);
+        ok = mbar_wait_sleep(&sm.o_done[st], no[st] & 1, fault, kFaultWaitMma, abort);
         ++no[0];
         ++no[1];
       }
