@@ -41,10 +41,10 @@
 // shared memory, as P = 0 times what a page may hold there need not be 0.
 //
 // E4M3 is decoded to f16, exactly, NaN codes included, by one conversion a
-// pair (moving the bits by integer instructions: 372 us against 352). Q then is f16 too, each bf16 row scaled by the power of two that
-// puts its largest value just below f16's largest (what falls below f16's
-// range is under 2^-39 of that); the power of two comes back with the softmax
-// scale.
+// pair (moving the bits by integer instructions: 372 us against 352). Q then
+// is f16 too, each bf16 row scaled by the power of two that puts its largest
+// value just below f16's largest (what falls below f16's range is under 2^-39
+// of that); the power of two comes back with the softmax scale.
 //
 // A tile's rows share the products, so a row also multiplies, by P = 0, what
 // it must not see: values of another row's drafts or blocks, which may be
