@@ -317,3 +317,43 @@ def test_slow_caches_change_nothing(msa, kv, hq, hkv):
                                           max_seqlen_q=max(lens), return_softmax_lse=True)
         assert torch.equal(out, warm[0]) and torch.equal(lse, warm[1])
     fault_clear(msa)
+
+
+def test_hundreds_of_requests(msa):
+    """More sequences than a block of the union kernel reads at once, some of them empty."""
+    lens = [(5 * i) % 3 for i in range(600)]
+    used = [n + (37 * i) % 200 for i, n in enumerate(lens)]
+    c = make(lens, used, 4, 2, 2, "bf16", seed=6)
+    check(c, *run(msa, c))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_offsets_past_32_bits(msa, kv):
+    """Pages whose elements lie past 2^32, written by the append and read by the attention."""
+    g = torch.Generator().manual_seed(8)
+    hkv, hq, num, lens, used = 4, 16, 70000, [6, 9], [300, 140]
+    assert (num - 10) * hkv * 128 * 128 > 2**32
+    k, v = (torch.empty(num, hkv, 128, 128, dtype=DT[kv], device=DEV) for _ in range(2))
+    table = torch.tensor([[num - 1, num - 5, num - 2], [num - 7, num - 3, -1]], dtype=torch.int32)
+    small = torch.tensor([[0, 1, 2], [3, 4, -1]], dtype=torch.int32)
+    pages = table[small >= 0].long().to(DEV)
+    fill = torch.randn(2, 5, hkv, 128, 128, generator=g).to(DT[kv])
+    k[pages], v[pages] = fill[0].to(DEV), fill[1].to(DEV)
+    c = make(lens, used, hq, hkv, 3, kv, seed=8, garbage=False)
+    x = torch.randn(sum(lens), hq + 2 * hkv, 128, generator=g).to(torch.bfloat16).to(DEV)
+    w = torch.ones(128, device=DEV)
+    pos = torch.zeros(sum(lens), dtype=torch.int32, device=DEV)
+    c["table"] = table
+    q = msa.msa_qk_norm_rope_append(x[:, :hq], x[:, hq : hq + hkv], x[:, hq + hkv :], w, w, None, pos, c["cu"].to(DEV), k, v, page_table=table.to(DEV),
+                                    seqused_k=c["used"].to(DEV))
+    d = {n: t.to(DEV) for n, t in c.items()}
+    out, lse = msa.msa_tree_attention(q, k, v, d["q2k"], d["cu"], d["mask"], page_table=d["table"], seqused_k=d["used"], max_seqlen_q=9, return_softmax_lse=True)
+    fault_clear(msa)
+    kept, near = (t[pages].cpu() for t in (k, v)), x[:, hq + hkv :].float().cpu()
+    c["k"], c["v"] = kept
+    for b in range(2):
+        for t in range(int(c["cu"][b]), int(c["cu"][b + 1])):
+            p = used[b] - int(c["cu"][b + 1]) + t
+            assert torch.equal(c["v"][small[b, p // 128], :, p % 128].float(), near[t].to(DT[kv]).float())
+    c["q"], c["table"] = q.cpu(), small
+    check(c, out, lse)
