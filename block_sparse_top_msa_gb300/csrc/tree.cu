@@ -20,11 +20,12 @@
 // sums them (tree_union_kernel leaves one per unit), comes to the same choice
 // and finds its own range.
 //
-// What bounds it: neither memory nor the tensor cores alone (their work on the
-// unions is 132 us of the 348, on the 32 requests 27 of the 73, where random
-// pages take 42), but a block's chain of products and softmax by two streams
-// of four warps, and the issue slots these share with the decoding: a block
-// of two tiles takes 4300 clocks, its products 2350. Waits are by
+// What bounds it: no unit, but the latency of a block's chain (S, its maxima,
+// P, the products) by two streams of four warps, and what passes between two
+// units. A block of two tiles takes 4100 to 4400 clocks, its products 2350; with
+// E4M3 the tensor cores are busy 38% of the time, the issue slots 42%, memory
+// 22%. The products of the unions would take 132 us of the 348, on the 32
+// requests 27 of the 73, where random pages take 42. Waits are by
 // mbar_wait_sleep, as spinning takes issue slots too (354 us against 351).
 //
 // Two streams of (QK^T, softmax, PV) keep the tensor cores busy: while one
