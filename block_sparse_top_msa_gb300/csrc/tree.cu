@@ -24,7 +24,7 @@
 // P, the products) by two streams of four warps, and what passes between two
 // units. A block of two tiles takes 4100 to 4400 clocks, its products 2350; with
 // E4M3 the tensor cores are busy 38% of the time, the issue slots 42%, memory
-// 22%. The products of the unions would take 132 us of the 348, on the 32
+// 22%. The products of the unions would take 132 us of the 343, on the 32
 // requests 27 of the 73, where random pages take 42. Waits are by
 // mbar_wait_sleep, as spinning takes issue slots too (354 us against 351).
 //
@@ -1347,9 +1347,12 @@ __device__ __noinline__ void odd_row(const TreeArgs& a, size_t orow, int lane) {
 // the ranges. A block takes kMergeRows of the unit's rows, a thread four rows
 // of four columns; kMergeChunk partials at a time, whose weights go through
 // shared memory while their O are on the way. Odd rows are computed here too:
-// those that whole units listed, and those that joining finds.
-constexpr int kMergeRows = 64, kMergeThreads = 512, kMergeAhead = 4, kMergeChunk = 16;
-__global__ void __launch_bounds__(kMergeThreads)
+// those that whole units listed, and those that joining finds. Two blocks an
+// SM, two partials ahead: 343.5, 72.6 and 23.7 us for 128 E4M3 requests, 32 and
+// one, against 347.3, 73.0 and 24.8 with blocks of 64 rows, one an SM, and four
+// partials ahead.
+constexpr int kMergeRows = 32, kMergeThreads = 8 * kMergeRows, kMergeAhead = 2, kMergeChunk = 16;
+__global__ void __launch_bounds__(kMergeThreads, 2)
     merge_tree_kernel(const __grid_constant__ TreeArgs a) {
   __shared__ uint32_t s_out[kMergeRows][kHeadDim / 2 + 1];
   __shared__ float s_m[kMergeChunk][kMergeRows], s_l[kMergeChunk][kMergeRows];
@@ -1374,7 +1377,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   if (rows <= 0) return;
   const int count = s_end - k;
   auto slot = [&](int i) { return (size_t)(i == 0 ? 2 * k + 1 : 2 * (k + i)); };
-  const int q = (tid & 15) * 4, c4 = tid >> 4;  // first row of four, group of four columns
+  const int q = tid % (kMergeRows / 4) * 4, c4 = tid / (kMergeRows / 4);  // first row of four, group of four columns
   const int left = rows - q;                    // rows of the thread's four that exist
   const bool quad = left >= 4 && (a.rows_part & 3) == 0;
   const float* part = a.part_o + (size_t)c4 * 4 * a.rows_part + row0 + q;
