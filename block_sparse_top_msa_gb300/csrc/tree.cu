@@ -24,8 +24,8 @@
 // P, the products) by two streams of four warps, and what passes between two
 // units. A block of two tiles takes 4100 to 4400 clocks, its products 2350; with
 // E4M3 the tensor cores are busy 38% of the time, the issue slots 42%, memory
-// 22%. The products of the unions would take 132 us of the 343, on the 32
-// requests 27 of the 73, where random pages take 42. Waits are by
+// 22%. The products of the unions would take 132 us of the 344, on the 32
+// requests 27 of the 72, where random pages take 42. Waits are by
 // mbar_wait_sleep, as spinning takes issue slots too (354 us against 351).
 //
 // Two streams of (QK^T, softmax, PV) keep the tensor cores busy: while one
@@ -37,8 +37,7 @@
 // Roles: warps 0-3 and 4-7 the softmax of stream 0 and 1 (a thread per row),
 // warp 8 hands out the segments and loads Q, warp 9 issues the MMAs, warp 10
 // brings K and V by TMA, and for E4M3 caches warps 11-14 decode them into the
-// swizzled layout the MMA reads, and convert the next segment's Q while the
-// softmax warps are in the epilogue of the last (by these: 350.5 us, not 348).
+// swizzled layout the MMA reads.
 // Keys past a sequence's end are masked in S, and their V rows zeroed in
 // shared memory, as P = 0 times what a page may hold there need not be 0.
 //
@@ -95,7 +94,6 @@ struct Segment {
 // What a raw E4M3 slot holds; g == -1: no more.
 struct RawTile {
   int g, is_v, rows;  // rows: keys of the block within the sequence (0: no page)
-  int q;              // a segment's first K: its tiles of Q
 };
 
 template <bool FP8>
@@ -119,7 +117,7 @@ struct __align__(1024) Smem {
   uint64_t ml_full, ml_empty, drain;
   uint64_t q_ready;                // E4M3: Q converted
   float2 ml[128];                  // stream 1's (m, l) for the epilogue that joins the streams
-  int8_t q_exp[2][256];            // E4M3: the rows' powers of two, of this segment and the next
+  float q_scale[128];              // E4M3, one tile: the rows' softmax scales
   long long scan[32];
   long long first_p0, total;
   int first_unit, most;  // most: of the CTAs' loads with whole units
@@ -438,7 +436,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     mbar_init(&sm.ml_full, 4);
     mbar_init(&sm.ml_empty, 4);
     mbar_init(&sm.drain, 1);
-    mbar_init(&sm.q_ready, FP8 ? R::kDecodeWarps : 1);
+    mbar_init(&sm.q_ready, 8);
     for (int s = 0; s < kRawSlots; ++s) {
       mbar_init(&sm.raw_full[s], 1);
       mbar_init(&sm.raw_empty[s], FP8 ? R::kDecodeWarps : 1);
@@ -763,7 +761,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     const int32_t *list = nullptr, *prow = nullptr;
     int page_k = -1, page_v = -1, blk_k = 0, blk_v = 0;
     struct Tile {
-      int g, page, blk, is_v, h, lk, q;
+      int g, page, blk, is_v, h, lk;
     };
     // The next tile, warp-wide; false at the end.
     auto take = [&](Tile& t) -> bool {
@@ -801,7 +799,6 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       t.is_v = is_v;
       t.h = s.h;
       t.lk = s.lk;
-      t.q = x == 1 ? 1 + s.dual : 0;
       return true;
     };
     if constexpr (!FP8) {
@@ -869,13 +866,13 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         if (lane == 0) {
           const long long left = (long long)t.lk - (long long)t.blk * kBlk;
           const int rows = t.page >= a.num_pages || left <= 0 ? 0 : left < kBlk ? (int)left : kBlk;
-          ok = put(RawTile{t.g, t.is_v, rows, t.q},
+          ok = put(RawTile{t.g, t.is_v, rows},
                    (t.is_v ? a.v_pool : a.k_pool) + ((size_t)(rows > 0 ? t.page : 0) * a.num_kv_heads + t.h) * kHalf);
         }
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       }
       if (lane == 0) {
-        if (ok) ok = put(RawTile{-1, 0, 0, 0}, nullptr);
+        if (ok) ok = put(RawTile{-1, 0, 0}, nullptr);
         // Copies in flight land before the CTA's shared memory is given back.
         if (!ok)
           for (int i = y < kRawSlots ? 0 : y - kRawSlots; i < y; ++i)
@@ -892,7 +889,6 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     // banks.
     const int ct = tid - R::kDecode * 32;
     const int q = ct & 7, r0 = (ct >> 3) ^ (q >> 2);
-    int nq = 0;  // segments whose Q is converted
     bool ok = true;
     for (int y = 0;; ++y) {
       const int rs = y % kRawSlots;
@@ -931,43 +927,6 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(t.is_v ? &sm.v_full[slot] : &sm.k_full[slot]);
-      if (t.q > 0) {
-        // The segment's Q, a thread per row, in place: bf16 to f16 times 2^k.
-        ok = mbar_wait_sleep(&sm.q_full, nq & 1, fault, kFaultWaitTma, abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-#pragma unroll 1
-        for (int i = 0; i < t.q; ++i) {
-          uint8_t* qt = &sm.q[i][0][0];
-          uint32_t big = 0u;
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(qt + (c >> 3) * kHalf + sw128_offset(ct, c & 7));
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) big = max(big, max(xs[e] & 0x7f80u, (xs[e] >> 16) & 0x7f80u));
-          }
-          const int e = (int)(big >> 7);  // exponent field of the row's largest value
-          const int k = e == 255 ? 0 : min(120, 142 - e);
-          const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-          sm.q_exp[nq & 1][i * 128 + ct] = (int8_t)k;
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(qt + (c >> 3) * kHalf + sw128_offset(ct, c & 7));
-            const uint4 x = *at;
-            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w)
-              o[w] = pack_f16x2(__uint_as_float(xs[w] << 16) * up, __uint_as_float(xs[w] & 0xffff0000u) * up);
-            *at = make_uint4(o[0], o[1], o[2], o[3]);
-          }
-        }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.q_ready);
-        ++nq;
-      }
     }
   } else {
     // ------------------------------------------------------ softmax, epilogue
@@ -1006,6 +965,49 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       const uint32_t* mask = a.tree_mask + (size_t)(s.t0 + (active ? w : 0)) * a.mask_words;
       const int32_t* prow = a.page_table + (size_t)s.b * a.max_pages;
       float scale = a.scale_log2;  // of the row's S, to log2 units
+      if constexpr (FP8) {
+        if (s.dual || st == 0) {
+          // The row of Q, in place: bf16 to f16 times 2^k.
+          ok = mbar_wait_sleep(&sm.q_full, nseg & 1, fault, kFaultWaitTma, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          uint8_t* qt = &sm.q[s.dual ? st : 0][0][0];
+          uint32_t big = 0u;
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(qt + (c >> 3) * kHalf + sw128_offset(row, c & 7));
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) big = max(big, max(xs[i] & 0x7f80u, (xs[i] >> 16) & 0x7f80u));
+          }
+          const int e = (int)(big >> 7);  // exponent field of the row's largest value
+          const int k = e == 255 ? 0 : min(120, 142 - e);
+          const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+          scale = a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) {
+            uint4* at = reinterpret_cast<uint4*>(qt + (c >> 3) * kHalf + sw128_offset(row, c & 7));
+            const uint4 x = *at;
+            const uint32_t xs[4] = {x.x, x.y, x.z, x.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[i] = pack_f16x2(__uint_as_float(xs[i] << 16) * up, __uint_as_float(xs[i] & 0xffff0000u) * up);
+            *at = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+          if (!s.dual) sm.q_scale[row] = scale;
+          fence_async_smem();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&sm.q_ready);
+        if (!s.dual && st == 1) {
+          ok = mbar_wait_sleep(&sm.q_ready, nseg & 1, fault, kFaultWaitSoftmax, abort);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          scale = sm.q_scale[row];
+        }
+        ++nseg;
+      }
       float m_ref = -INFINITY, l = 0.f;
       // Block ids two steps ahead, pages one step ahead.
       int j = s.dual ? 0 : st;
@@ -1063,12 +1065,6 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           const uint32_t vis0 = half == 0 ? vis[0] : vis[2], vis1 = half == 0 ? vis[1] : vis[3];
           const uint32_t hcol = scol + half * 64;  // P over the first half of its own S
           ok = mbar_wait_sleep(&sm.qk_done[st][half], nqk & 1, fault, kFaultWaitMma, abort);
-          // This S says that Q's powers of two are there; those of the segment
-          // after the next replace them only behind products with this one's P.
-          if (FP8 && t == 0) {
-            const int k = sm.q_exp[nseg & 1][(s.dual ? st * 128 : 0) + row];
-            scale = a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
-          }
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
@@ -1152,7 +1148,6 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       }
       if (!ok) break;
       g0 += n;
-      ++nseg;
       // ------------------------------------------------------------ epilogue
       float f[2] = {1.f, 0.f};
       uint32_t from[2] = {lanes + kColO + st * 128, 0u};
