@@ -316,7 +316,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor& q = tensor("q", a[0]);
   check_place("q", q, nullptr);
   if (!is_16bit(q.scalar_type())) wrong_dtype("q", q, "bfloat16 or float16");
-  check_shape("q", q, Shape{-1, -1, 128});
+  dense("q", a[0], nullptr, q.scalar_type(), {-1, -1, 128});
   const at::Device dev = q.device();
   const Tensor& k = tensor("k", a[1]);
   if (!is_kv(k.scalar_type())) wrong_dtype("k", k, "bfloat16, float16 or float8_e4m3fn");
