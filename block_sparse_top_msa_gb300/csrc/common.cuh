@@ -385,7 +385,9 @@ MSA_DEV void grid_dependents_launch() {
 
 // Launches a kernel that begins with grid_dependency_wait(): where the kernel
 // before it on the stream lets it, it is brought to the SMs early and waits
-// there.
+// there. A grid's wait covers the one grid before it; what that grid ran behind
+// is covered only if that grid waited too. So every kernel launched like this
+// waits on every path, those that have nothing to do or give up included.
 template <class... P, class... A>
 cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchConfig_t cfg = {};

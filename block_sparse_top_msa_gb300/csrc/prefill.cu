@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     uint32_t dyn;
     asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
     if (pad + sizeof(Smem) > dyn) {
+      grid_dependency_wait();
       if (threadIdx.x == 0) atomicOr(a.fault, (unsigned)kFaultCapacity);
       return;
     }
@@ -1224,32 +1225,37 @@ cudaError_t launch_dependent(Kernel kernel, dim3 grid, dim3 block, size_t smem, 
 __global__ void __launch_bounds__(256) merge_splits_kernel(const __grid_constant__ PrefillArgs a) {
   // The union metadata read below is final before this launch may begin: the
   // attention kernel lets it launch only after waiting for the union kernel.
-  // Only the partials need the wait, so it comes after the metadata loads.
+  // Only the partials need the wait, so it comes after the metadata loads, but
+  // it comes for warps without a row too: where no unit is split, this grid's
+  // end is all that a grid launched behind it waits for, and must not come
+  // before the attention kernel's.
   // In direct mode the attention kernel writes the metadata; a one-token tile
   // is its own query row (t0 = tile, one token), so only the union length is
   // read, after the wait, together with the first splits' partials.
   constexpr int kU = 4;
   const int warp_global = (int)((blockIdx.x * (size_t)blockDim.x + threadIdx.x) >> 5);
   const int lane = threadIdx.x & 31;
-  if (warp_global >= a.tail_units * a.rows_part) return;
   const int t = warp_global / a.rows_part, row = warp_global - t * a.rows_part;
   const int unit = a.whole_units + t;
   const int h = unit / a.max_tiles;  // same head-major order as item_at
   const int tile = a.max_tiles - 1 - (unit - h * a.max_tiles);
   const int G = a.num_qo_heads / a.num_kv_heads;
   const int w = row / G, gh = row - w * G;
-  if (row >= a.tile_tokens * G) return;
+  bool live = warp_global < a.tail_units * a.rows_part && row < a.tile_tokens * G;
   int t0 = tile, n_union = 0;
-  if (!a.direct) {
+  if (live && !a.direct) {
     t0 = __ldg(a.tile_info + 2 * tile);
-    if (t0 < 0) return;
-    n_union = __ldg(a.union_len + (size_t)h * a.max_tiles + tile);
-    if ((n_union + a.pps - 1) / a.pps <= 1) return;  // written directly by the attention kernel
-    const int b = __ldg(a.tile_info + 2 * tile + 1);
-    if (w >= min(a.tile_tokens, __ldg(a.cu_q + b + 1) - t0)) return;
+    live = t0 >= 0;
+    if (live) {
+      n_union = __ldg(a.union_len + (size_t)h * a.max_tiles + tile);
+      const int b = __ldg(a.tile_info + 2 * tile + 1);
+      // A unit that was not split is written directly by the attention kernel.
+      live = (n_union + a.pps - 1) / a.pps > 1 && w < min(a.tile_tokens, __ldg(a.cu_q + b + 1) - t0);
+    }
   }
   const size_t p0 = (size_t)t * a.splits * a.rows_part + row;
   grid_dependency_wait();  // partials (and, in direct mode, metadata) of the attention kernel
+  if (!live) return;
   if (a.direct) n_union = __ldcg(a.union_len + (size_t)h * a.max_tiles + tile);
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);

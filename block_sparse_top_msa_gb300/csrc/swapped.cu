@@ -382,6 +382,7 @@ __global__ void __launch_bounds__(kSwThreads, 1)
     uint32_t dyn;
     asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
     if (pad + sizeof(SwSmem) > dyn) {
+      grid_dependency_wait();
       if (threadIdx.x == 0) atomicOr(a.fault, (unsigned)kFaultCapacity);
       return;
     }

@@ -394,6 +394,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     uint32_t dyn;
     asm("mov.u32 %0, %%dynamic_smem_size;" : "=r"(dyn));
     if (pad + sizeof(Smem<FP8>) > dyn) {
+      grid_dependency_wait();
       if (threadIdx.x == 0) {
         atomicOr(a.fault, (unsigned)kFaultCapacity);
         a.cut[blockIdx.x] = make_int2(-1, -1);  // nothing to join

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import test_gpu_tree_attention as tree
+from parity_util import fault_clear
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -31,3 +32,51 @@ def test_tree_refuses_a_query_with_strides(msa, kv):
                 call(q, d["k"], d["v"], d["q2k"], d["cu"], d["mask"], page_table=d["table"], seqused_k=d["used"], max_seqlen_q=5)
         c["q"] = q.contiguous().cpu()
         tree.check(c, *tree.run(msa, c))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_step_behind_a_forward_whose_splits_come_to_nothing(msa, captured):
+    """A forward with room to split its units but short lists, and right behind it an append and accepted rows that overwrite what it
+    reads: every time the forward's results of the caches before."""
+    batch, lq, hq, hkv, topk = 4, 3, 64, 4, 16
+    g = torch.Generator().manual_seed(4)
+    used = [700 + 128 * b for b in range(batch)]
+    width = (max(used) + 127) // 128
+    pages = batch * width
+    table = torch.randperm(pages, generator=g).to(torch.int32).view(batch, width).to(DEV)
+    lists = torch.full((hkv, batch * lq, topk), -1, dtype=torch.int32)
+    lists[:, :, 0] = 1  # one listed block of sixteen
+    lists, cu = lists.to(DEV), torch.arange(0, batch * lq + 1, lq, dtype=torch.int32, device=DEV)
+    seq = torch.tensor(used, dtype=torch.int32, device=DEV)
+    pools = torch.randn(2, pages, hkv, 128, 128, generator=g).to(torch.bfloat16).to(DEV)
+    q = torch.randn(batch * lq, hq, 128, generator=g).to(torch.bfloat16).to(DEV)
+    x = torch.randn(batch * lq, hq + 2 * hkv, 128, generator=g).to(torch.bfloat16).to(DEV)
+    w, pos = torch.ones(128, device=DEV), torch.zeros(batch * lq, dtype=torch.int32, device=DEV)
+    # The tokens' cache rows are the listed block's, so that the append overwrites keys that the forward reads.
+    at = torch.full((batch,), 256, dtype=torch.int32, device=DEV)
+    path, plen = torch.tensor([[1, 2]] * batch, dtype=torch.int32, device=DEV), torch.full((batch,), 2, dtype=torch.int32, device=DEV)
+    work = torch.empty(msa.msa_sparse_attention_workspace_size(batch, batch * lq, hq, hkv, 128, topk, lq, True) + 256, dtype=torch.uint8, device=DEV)
+    out, kept = torch.empty_like(q), (pools.clone(), q.clone())
+
+    def step():
+        msa.msa_sparse_attention_fwd(q, pools[0], pools[1], lists, cu, causal=True, page_table=table, seqused_k=seq, max_seqlen_q=lq, out=out, workspace=work)
+        msa.msa_qk_norm_rope_append(x[:, :hq], x[:, hq : hq + hkv], x[:, hq + hkv :], w, w, None, pos, cu, pools[0], pools[1], page_table=table, seqused_k=at, q_out=q)
+        return msa.msa_cache_accept(pools, table, at, cu, path, plen)
+
+    step()
+    torch.cuda.synchronize()
+    pools.copy_(kept[0])
+    q.copy_(kept[1])
+    msa.msa_sparse_attention_fwd(q, pools[0], pools[1], lists, cu, causal=True, page_table=table, seqused_k=seq, max_seqlen_q=lq, out=out, workspace=work)
+    want = out.clone()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+    for _ in range(50):
+        pools.copy_(kept[0])
+        q.copy_(kept[1])
+        out.fill_(7)
+        graph.replay() if captured else step()
+        assert torch.equal(out, want)
+    fault_clear(msa)

@@ -1,0 +1,45 @@
+"""What can be told on the host about the serving step's operators at the edges of what their documentation allows (CPU only)."""
+import glob
+import os
+import re
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+WAIT = "grid_dependency_wait();"
+
+
+def kernels():
+    """Each kernel's source: (file, name, body)."""
+    for path in sorted(glob.glob(os.path.join(ROOT, "block_sparse_top_msa_gb300", "csrc", "*.cu"))):
+        text = open(path).read()
+        for m in re.finditer(r"__global__.*?\b(\w+_kernel)\((.*?)\n}\n", text, re.S):
+            yield os.path.basename(path), m.group(1), re.sub(r"//[^\n]*", "", m.group(2))
+
+
+def enclosing_block(text, at):
+    """What stands in the innermost braces around a place, before it."""
+    depth = 0
+    for i in range(at - 1, -1, -1):
+        depth += (text[i] == "}") - (text[i] == "{")
+        if depth < 0:
+            return text[i:at]
+    return text[:at]
+
+
+def test_dependent_kernels_wait_on_every_path():
+    """A grid launched to begin under the tail of the one before it is ordered by its wait alone, and the grid after it by its end: a
+    path that leaves before the wait orders nothing."""
+    waiting = {name: (file, body) for file, name, body in kernels() if WAIT in body}
+    launched = set()
+    for path in glob.glob(os.path.join(ROOT, "block_sparse_top_msa_gb300", "csrc", "*.cu")):
+        text = open(path).read()
+        launched |= set(re.findall(r"(?:launch_dependent|launch_pdl)\(\s*(?:a\.interleaved \? )?(\w+_kernel)\b", text))
+        launched |= set(re.findall(r"cudaLaunchKernelEx\(&cfg, (\w+_kernel)\b", text))
+    assert len(launched) >= 14 and launched <= set(waiting), launched - set(waiting)
+    for name in sorted(launched):
+        file, body = waiting[name]
+        # The wait that every thread comes to; the attention kernel has another for launches that wait late, in the work counter's claim.
+        m = re.search(r"^  (?:if \(!a\.wait_late\) )?grid_dependency_wait\(\);", body, re.M)
+        assert m, (file, name)
+        before = body[: m.start()]
+        for r in re.finditer(r"return;", before):
+            assert WAIT in enclosing_block(before, r.start()), (file, name, before[max(0, r.start() - 200) : r.end()])
