@@ -112,7 +112,7 @@ struct __align__(1024) Smem {
   uint64_t v_full[kVSlots], v_empty[kVSlots];
   uint64_t qk_done[2][2];          // per stream and 64-key half of a block: S readable
   uint64_t p_full[2][2];           // P written
-  uint64_t pv_done[2];             // per stream: a half's PV complete
+  uint64_t pv_done[2][2];          // the half's PV complete: its P read, O written
   uint64_t o_done[2], o_free[2];   // per stream: O complete at a segment's end, O read out
   uint64_t ml_full, ml_empty, drain;
   uint64_t q_ready;                // E4M3: Q converted
@@ -429,8 +429,8 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       for (int h = 0; h < 2; ++h) {
         mbar_init(&sm.qk_done[s][h], 1);
         mbar_init(&sm.p_full[s][h], 4);
+        mbar_init(&sm.pv_done[s][h], 1);
       }
-      mbar_init(&sm.pv_done[s], 1);
       mbar_init(&sm.o_done[s], 1);
       mbar_init(&sm.o_free[s], 4);
     }
@@ -652,15 +652,27 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     const uint32_t v0 = (uint32_t)sdesc_sw128(smem_u32(&sm.v[0][0][0]), kHalf, 1024);
     Ring<kKSlots> rk;
     Ring<kVSlots> rv;
-    uint32_t p_phase = 0u;  // a bit per stream
+    uint32_t p_phase = 0u;   // a bit per stream
+    uint32_t pv_phase = 0u, pv_open = 0u;  // a bit per stream and half: the PV's phase; a PV not waited for yet
     int nseg = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase, unsigned code) {
       ok = ok && mbar_wait_sleep(bar, phase, fault, code, abort);
     };
     auto commit = [&](uint64_t* bar) { commit_if(el, bar); };
-    // S of stream st = tile `tile` of Q times K, for the block's 64-key half h.
+    // S of stream st = tile `tile` of Q times K, for the block's 64-key half h:
+    // over the P of the half before, once the PV that reads it is complete.
+    // (MMAs run in the order of their issue where shape and accumulator are the
+    // same; these differ in both.)
     auto qk = [&](int st, int h, int tile) {
+      const uint32_t bit = 1u << (2 * st + h);
+      if (pv_open & bit) {
+        wait(&sm.pv_done[st][h], (pv_phase & bit) != 0u, kFaultWaitMma);
+        if (!ok) return;
+        tc_fence_after();
+        pv_open ^= bit;
+        pv_phase ^= bit;
+      }
       const uint32_t q = q0 + tile * kTile16, k = k0 + rk.idx * kTile16 + h * 512;
       const uint32_t d = tb + kColS + st * 128 + h * 64;
 #pragma unroll
@@ -676,7 +688,8 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       const uint32_t tp = tb + kColS + st * 128 + h * 64, d = tb + kColO + st * 128;
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) mma_ts_if(el, d, tp + kk * 8, v + kk * 128, hi, idO, kk > 0 || h > 0 || !first);
-      commit(&sm.pv_done[st]);
+      commit(&sm.pv_done[st][h]);
+      pv_open |= 1u << (2 * st + h);
     };
     Segment s;
     for (int ni = 0; ok; ++ni) {
@@ -1097,10 +1110,10 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
             bool rescale = false;
             update_max(on, mx, scale, m_ref, l, alpha, rescale);
             if (__any_sync(0xffffffffu, rescale)) {
-              // O has to hold the half before (the second halves' PVs complete
-              // odd phases of pv_done, the first halves' even ones); the half
-              // before that is complete, as this S was issued after it.
-              ok = mbar_wait_sleep(&sm.pv_done[st], half ^ 1, fault, kFaultWaitMma, abort);
+              // O has to hold the half before: this block's first or the last
+              // block's second (in a unit's first half no row has a maximum yet).
+              // The half before that is complete, as this S was issued after it.
+              ok = mbar_wait_sleep(&sm.pv_done[st][half ^ 1], (nqk - (half ^ 1)) & 1, fault, kFaultWaitMma, abort);
               ok = __all_sync(0xffffffffu, ok);
               if (!ok) break;
               tc_fence_after();

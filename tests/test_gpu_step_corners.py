@@ -4,6 +4,7 @@ import torch
 
 import test_gpu_tree_attention as tree
 from parity_util import fault_clear
+from step_util import DT, half_step, tree_attention
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -79,4 +80,37 @@ def test_a_step_behind_a_forward_whose_splits_come_to_nothing(msa, captured):
         out.fill_(7)
         graph.replay() if captured else step()
         assert torch.equal(out, want)
+    fault_clear(msa)
+
+
+@pytest.mark.parametrize("kv,hq,hkv,lo,hi", [("fp16", 40, 4, 4, 7), ("bf16", 64, 4, 1, 16), ("e4m3", 64, 4, 1, 16), ("e4m3", 32, 4, 1, 16)])
+def test_tree_gives_the_same_bits(msa, kv, hq, hkv, lo, hi):
+    """Units of one tile and of two in one call, keys that grow so that rows are rescaled from half a block to the next: near 64 bits,
+    and the same bits in every run, alone and with runs right behind one another."""
+    lens = [lo + (5 * i) % (hi - lo + 1) for i in range(20)]
+    used = [900 + 77 * i for i in range(20)]
+    c = tree.make(lens, used, hq, hkv, 8, kv, seed=12, garbage=False)
+    kf = c["k"].float()
+    for b, n in enumerate(used):
+        for i in range((n + 127) // 128):
+            kf[c["table"][b, i]] *= 1 + 2 * ((torch.arange(128) + 128 * i) / n).clamp(max=1)[None, :, None]
+    c["k"] = kf.to(DT[kv])
+    d = {n: t.to(DEV) for n, t in c.items()}
+
+    def run():
+        return msa.msa_tree_attention(d["q"], d["k"], d["v"], d["q2k"], d["cu"], d["mask"], page_table=d["table"], seqused_k=d["used"], max_seqlen_q=max(lens),
+                                      return_softmax_lse=True)
+
+    first = run()
+    ref, rl, size = tree_attention(c["q"], c["k"].float(), c["v"].float(), c["q2k"], c["cu"], c["mask"], c["table"], c["used"], tree.SCALE)
+    # A logit is off by at most 128 roundings of 2^-24 of L = max sum |q k| scale, a probability by twice that and by the
+    # exponent's argument's three roundings: 2 (2^-17 + 9 2^-24) L < 2^-15.8 L.
+    most = max((c["q"].float().abs().reshape(-1, hkv, hq // hkv, 128).amax(2)[:, h] @ c["k"].float()[:, h].abs().reshape(-1, 128).T).max().item() for h in range(hkv)) * tree.SCALE
+    tol = half_step(c["q"].dtype) * (size + ref.abs()) * 1.01 + 2.0**-15.8 * most * size
+    if kv == "fp16":
+        tol += 8 * 128 * 2.0**-25 * 6 + 2.0**-25
+    assert ((first[0].double().cpu() - ref).abs() <= tol).all()
+    for _ in range(20):
+        runs = [run() for _ in range(10)]
+        assert all(torch.equal(o, first[0]) and torch.equal(l, first[1]) for o, l in runs)
     fault_clear(msa)
