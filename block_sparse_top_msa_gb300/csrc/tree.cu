@@ -35,9 +35,12 @@
 // the epilogue joins the two. TMEM holds S (P over it) and O of each stream.
 //
 // Roles: warps 0-3 and 4-7 the softmax of stream 0 and 1 (a thread per row),
-// warp 8 hands out the segments and loads Q, warp 9 issues the MMAs, warp 10
-// brings K and V by TMA, and for E4M3 caches warps 11-14 decode them into the
-// swizzled layout the MMA reads.
+// warp 8 hands out the segments and loads Q, warp 10 brings K and V by TMA,
+// warp 11 issues the products of Q and K, warp 9 those of P and V, and for E4M3
+// caches warps 12-15 decode K and V into the swizzled layout the MMA reads. Two
+// warps issue, as one that does both, waiting for each PV before the S that
+// takes its P's place, spends 1050 clocks a product and is the slowest of all
+// (128 E4M3 requests 393 us against 302, 32 bf16 requests 83 against 63).
 // Keys past a sequence's end are masked in S, and their V rows zeroed in
 // shared memory, as P = 0 times what a page may hold there need not be 0.
 //
@@ -73,12 +76,13 @@ constexpr uint32_t kColS = 0, kColO = 256;  // TMEM: S of stream s at 128 s, O a
 template <bool FP8>
 struct Roles {
   static constexpr int kSched = 8;  // segments and Q
-  static constexpr int kMma = 9;
+  static constexpr int kMma = 9;    // issues the products of P and V
   static constexpr int kKv = 10;    // K and V by TMA
-  static constexpr int kDecode = 11;  // E4M3: first of the decoding warps
+  static constexpr int kQk = 11;    // issues the products of Q and K
+  static constexpr int kDecode = 12;  // E4M3: first of the decoding warps
   static constexpr int kDecodeWarps = FP8 ? 4 : 0;
   static constexpr int kThreads = (kDecode + kDecodeWarps) * 32;
-  static constexpr int kReaders = 1 + 8 + 1;  // of the segment ring
+  static constexpr int kReaders = 2 + 8 + 1;  // of the segment ring
   static constexpr int kVSlots = FP8 ? 2 : 3;  // V ring (a slot frees when its last PV completes)
 };
 
@@ -114,7 +118,7 @@ struct __align__(1024) Smem {
   uint64_t p_full[2][2];           // P written
   uint64_t pv_done[2][2];          // the half's PV complete: its P read, O written
   uint64_t o_done[2], o_free[2];   // per stream: O complete at a segment's end, O read out
-  uint64_t ml_full, ml_empty, drain;
+  uint64_t ml_full, ml_empty, drain[2];
   uint64_t q_ready;                // E4M3: Q converted
   float2 ml[128];                  // stream 1's (m, l) for the epilogue that joins the streams
   float q_scale[128];              // E4M3, one tile: the rows' softmax scales
@@ -171,7 +175,7 @@ MSA_DEV uint32_t tree_bits(const uint32_t* mask, int words, long long base, int 
   return left >= 31 ? bits : left < 0 ? 0u : bits & ((2u << left) - 1u);
 }
 
-// Tile x of the 2 n tiles of a segment, in the order the MMAs want them:
+// Tile x of the 2 n tiles of a segment, in the order the products want them:
 // K0, K1, V0, K2, V1, ... V(n-1). Returns the block, and whether it is V.
 MSA_DEV int tile_order(int x, int n, bool& is_v) {
   if (x == 0) {
@@ -436,7 +440,8 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     }
     mbar_init(&sm.ml_full, 4);
     mbar_init(&sm.ml_empty, 4);
-    mbar_init(&sm.drain, 1);
+    mbar_init(&sm.drain[0], 1);
+    mbar_init(&sm.drain[1], 1);
     mbar_init(&sm.q_ready, 8);
     for (int s = 0; s < kRawSlots; ++s) {
       mbar_init(&sm.raw_full[s], 1);
@@ -635,129 +640,134 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       // A copy in flight lands before the CTA's shared memory is given back.
       if (!ok && q_flight) mbar_wait_sleep(&sm.q_full, (n_q - 1) & 1, fault, kFaultWaitTma);
     }
-  } else if (warp == R::kMma) {
+  } else if (warp == R::kQk || warp == R::kMma) {
     // -------------------------------------------------------------- MMA issue
-    // The whole warp runs this, so that what an MMA needs stays in uniform
-    // registers; one elected lane issues. (A single lane's branch spent about
-    // 100 clocks on each MMA, which takes 73.)
+    // One warp issues the products of Q and K, another those of P and V: a wait
+    // takes about 100 clocks even where it has nothing to wait for. A whole warp
+    // runs this, so that what an MMA needs stays in uniform registers; one
+    // elected lane issues. (A single lane's branch spent about 100 clocks on
+    // each MMA, which takes 73.)
+    // Two tiles: both streams take every block. One tile: block j is stream
+    // j & 1's. Either way the products go by halves of a block's keys, under
+    // the softmax of the other half. (By whole blocks a stream's softmax and
+    // products ran one after the other, 3700 clocks a block of two tiles
+    // where the products take 2350.)
+    const bool is_qk = warp == R::kQk;
     const uint32_t el = elect_one();
     const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
-    constexpr uint32_t idS = idesc_16bit_f32(128, 64, false, false, kF16Ops);
-    constexpr uint32_t idO = idesc_16bit_f32(128, 128, false, true, kF16Ops);
     constexpr uint32_t kTile16 = (2 * kHalf) >> 4, kHalf16 = kHalf >> 4;
-    // Descriptors differ in the start address, in their low words.
-    const uint64_t dq = sdesc_sw128(smem_u32(&sm.q[0][0][0]), 16, 1024);
-    const uint32_t hi = (uint32_t)(dq >> 32), q0 = (uint32_t)dq;
-    const uint32_t k0 = (uint32_t)sdesc_sw128(smem_u32(&sm.k[0][0][0]), 16, 1024);
-    const uint32_t v0 = (uint32_t)sdesc_sw128(smem_u32(&sm.v[0][0][0]), kHalf, 1024);
-    Ring<kKSlots> rk;
-    Ring<kVSlots> rv;
-    uint32_t p_phase = 0u;   // a bit per stream
-    uint32_t pv_phase = 0u, pv_open = 0u;  // a bit per stream and half: the PV's phase; a PV not waited for yet
     int nseg = 0;
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t phase, unsigned code) {
       ok = ok && mbar_wait_sleep(bar, phase, fault, code, abort);
     };
     auto commit = [&](uint64_t* bar) { commit_if(el, bar); };
-    // S of stream st = tile `tile` of Q times K, for the block's 64-key half h:
-    // over the P of the half before, once the PV that reads it is complete.
-    // (MMAs run in the order of their issue where shape and accumulator are the
-    // same; these differ in both.)
-    auto qk = [&](int st, int h, int tile) {
-      const uint32_t bit = 1u << (2 * st + h);
-      if (pv_open & bit) {
-        wait(&sm.pv_done[st][h], (pv_phase & bit) != 0u, kFaultWaitMma);
-        if (!ok) return;
-        tc_fence_after();
-        pv_open ^= bit;
-        pv_phase ^= bit;
-      }
-      const uint32_t q = q0 + tile * kTile16, k = k0 + rk.idx * kTile16 + h * 512;
-      const uint32_t d = tb + kColS + st * 128 + h * 64;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
-        mma_ss_if(el, d, q + off, k + off, hi, idS, kk > 0);
-      }
-      commit(&sm.qk_done[st][h]);
-    };
-    // O of stream st = (+=) P V for half h.
-    auto pv = [&](int st, int h, bool first) {
-      const uint32_t v = v0 + rv.idx * kTile16 + h * 512;
-      const uint32_t tp = tb + kColS + st * 128 + h * 64, d = tb + kColO + st * 128;
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk) mma_ts_if(el, d, tp + kk * 8, v + kk * 128, hi, idO, kk > 0 || h > 0 || !first);
-      commit(&sm.pv_done[st][h]);
-      pv_open |= 1u << (2 * st + h);
-    };
     Segment s;
-    for (int ni = 0; ok; ++ni) {
-      const bool more = read_seg(ni, s);
-      __syncwarp();
-      if (!more) break;
-      if (lane == 0) release_seg(ni);
-      const int n = __shfl_sync(0xffffffffu, s.n, 0);
-      const bool dual = __shfl_sync(0xffffffffu, s.dual, 0) != 0;
-      if (n == 0) continue;
-      if (FP8) wait(&sm.q_ready, nseg & 1, kFaultWaitSoftmax);
-      else wait(&sm.q_full, nseg & 1, kFaultWaitTma);
-      // Two tiles: both streams take every block, K and V going with stream 1.
-      // One tile: block j is stream j & 1's. Either way the products go by
-      // halves of a block's keys: as soon as a half's P has been consumed, the
-      // S of the same half of the stream's next block takes its place, under
-      // the softmax of the other half. (By whole blocks a stream's softmax and
-      // products ran one after the other, 3700 clocks a block of two tiles
-      // where the products take 2350.)
-      const int ahead = dual ? 1 : 2;
-      auto k_used = [&](int b) {
-        commit(&sm.k_empty[rk.idx]);
-        rk.next();
-        if (b == n - 1) commit(&sm.q_empty);  // the segment's last
-      };
-#pragma unroll 1
-      for (int x = 0; ok && x < 4; ++x) {  // the first S of each stream
-        const int st = x >> 1, h = x & 1, b = dual ? 0 : st;
-        if (b >= n) break;
-        if (h == 0) wait(&sm.k_full[rk.idx], rk.phase, kFaultWaitTma);
-        if (!ok) break;
-        tc_fence_after();
-        qk(st, h, dual ? st : 0);
-        if (h == 1 && (!dual || st == 1)) k_used(b);
+    // The next segment with blocks; false at the end.
+    int ni = 0, n = 0;
+    bool dual = false;
+    auto next_seg = [&]() -> bool {
+      n = 0;
+      while (ok && n == 0) {
+        const bool more = read_seg(ni, s);
+        __syncwarp();
+        if (!more) return false;
+        if (lane == 0) release_seg(ni);
+        ++ni;
+        n = __shfl_sync(0xffffffffu, s.n, 0);
+        dual = __shfl_sync(0xffffffffu, s.dual, 0) != 0;
       }
+      return ok;
+    };
+    if (is_qk) {
+      // S of a half takes the place of the P of the stream's half before, once
+      // the PV that reads it is complete. (MMAs run in the order of their issue
+      // where shape and accumulator are the same; these differ in both.)
+      constexpr uint32_t idS = idesc_16bit_f32(128, 64, false, false, kF16Ops);
+      // Descriptors differ in the start address, in their low words.
+      const uint64_t dq = sdesc_sw128(smem_u32(&sm.q[0][0][0]), 16, 1024);
+      const uint32_t hi = (uint32_t)(dq >> 32), q0 = (uint32_t)dq;
+      const uint32_t k0 = (uint32_t)sdesc_sw128(smem_u32(&sm.k[0][0][0]), 16, 1024);
+      Ring<kKSlots> rk;
+      uint32_t used = 0u, pv_phase = 0u;  // a bit per stream and half: whether it held a P, and its PV's phase
+      while (next_seg()) {
+        if (FP8) wait(&sm.q_ready, nseg & 1, kFaultWaitSoftmax);
+        else wait(&sm.q_full, nseg & 1, kFaultWaitTma);
 #pragma unroll 1
-      for (int t = 0; ok && t < n; ++t) {
-        const int b = t + ahead;  // the stream's next block
-        if (t < ahead && nseg > 0) {
-          // O has been read: of both streams, every phase of each.
-          if (dual || t == 0) wait(&sm.o_free[0], (nseg - 1) & 1, kFaultWaitSoftmax);
-          if (dual || t == 1 || n == 1) wait(&sm.o_free[1], (nseg - 1) & 1, kFaultWaitSoftmax);
-        }
-        wait(&sm.v_full[rv.idx], rv.phase, kFaultWaitTma);
-        if (b < n) wait(&sm.k_full[rk.idx], rk.phase, kFaultWaitTma);
-        const int x_end = dual ? 4 : 2;
+        for (int b = 0; ok && b < n; ++b) {
+          wait(&sm.k_full[rk.idx], rk.phase, kFaultWaitTma);
+          const int x_end = dual ? 4 : 2;
 #pragma unroll 1
-        for (int x = 0; ok && x < x_end; ++x) {
-          const int st = dual ? x & 1 : t & 1, h = dual ? x >> 1 : x;
-          wait(&sm.p_full[st][h], (p_phase >> st) & 1u, kFaultWaitSoftmax);
-          if (!ok) break;
-          tc_fence_after();
-          pv(st, h, t < ahead);
-          if (b < n) qk(st, h, dual ? st : 0);
-          if (h == 1) {
-            p_phase ^= 1u << st;
-            if (b >= n) commit(&sm.o_done[st]);
+          for (int x = 0; ok && x < x_end; ++x) {
+            const int st = dual ? x & 1 : b & 1, h = dual ? x >> 1 : x;
+            const uint32_t bit = 1u << (2 * st + h);
+            if (used & bit) {
+              wait(&sm.pv_done[st][h], (pv_phase & bit) != 0u, kFaultWaitMma);
+              if (!ok) break;
+              pv_phase ^= bit;
+            }
+            used |= bit;
+            tc_fence_after();
+            const uint32_t q = q0 + (dual ? st : 0) * kTile16, k = k0 + rk.idx * kTile16 + h * 512;
+            const uint32_t d = tb + kColS + st * 128 + h * 64;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
+              mma_ss_if(el, d, q + off, k + off, hi, idS, kk > 0);
+            }
+            commit(&sm.qk_done[st][h]);
           }
+          if (!ok) break;
+          commit(&sm.k_empty[rk.idx]);
+          rk.next();
         }
-        if (!ok) break;
-        commit(&sm.v_empty[rv.idx]);
-        rv.next();
-        if (b < n) k_used(b);
+        if (ok) commit(&sm.q_empty);
+        ++nseg;
       }
-      ++nseg;
+    } else {
+      constexpr uint32_t idO = idesc_16bit_f32(128, 128, false, true, kF16Ops);
+      const uint64_t dv = sdesc_sw128(smem_u32(&sm.v[0][0][0]), kHalf, 1024);
+      const uint32_t hi = (uint32_t)(dv >> 32), v0 = (uint32_t)dv;
+      Ring<kVSlots> rv;
+      uint32_t p_phase = 0u;  // a bit per stream
+      while (next_seg()) {
+        const int ahead = dual ? 1 : 2;  // blocks that are the streams' first, and last
+#pragma unroll 1
+        for (int t = 0; ok && t < n; ++t) {
+          if (t < ahead && nseg > 0) {
+            // O has been read: of both streams, every phase of each.
+            if (dual || t == 0) wait(&sm.o_free[0], (nseg - 1) & 1, kFaultWaitSoftmax);
+            if (dual || t == 1 || n == 1) wait(&sm.o_free[1], (nseg - 1) & 1, kFaultWaitSoftmax);
+          }
+          wait(&sm.v_full[rv.idx], rv.phase, kFaultWaitTma);
+          const int x_end = dual ? 4 : 2;
+#pragma unroll 1
+          for (int x = 0; ok && x < x_end; ++x) {
+            const int st = dual ? x & 1 : t & 1, h = dual ? x >> 1 : x;
+            wait(&sm.p_full[st][h], (p_phase >> st) & 1u, kFaultWaitSoftmax);
+            if (!ok) break;
+            tc_fence_after();
+            // O of the stream = (+=) P V for the half.
+            const uint32_t v = v0 + rv.idx * kTile16 + h * 512;
+            const uint32_t tp = tb + kColS + st * 128 + h * 64, d = tb + kColO + st * 128;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_ts_if(el, d, tp + kk * 8, v + kk * 128, hi, idO, kk > 0 || h > 0 || t >= ahead);
+            commit(&sm.pv_done[st][h]);
+            if (h == 1) {
+              p_phase ^= 1u << st;
+              if (t + ahead >= n) commit(&sm.o_done[st]);
+            }
+          }
+          if (!ok) break;
+          commit(&sm.v_empty[rv.idx]);
+          rv.next();
+        }
+        ++nseg;
+      }
     }
-    commit(&sm.drain);
-    mbar_wait_sleep(&sm.drain, 0, fault, kFaultWaitMma);
+    commit(&sm.drain[is_qk]);
+    mbar_wait_sleep(&sm.drain[is_qk], 0, fault, kFaultWaitMma);
     __syncwarp();
   } else if (warp == R::kKv) {
     // ---------------------------------------------------------------- K and V
@@ -1062,8 +1072,8 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           // V rows past the end, before the first PV that reads the block (in
           // a unit of two tiles stream 0's, which is issued first). The wait
           // for the slot's phase needs the phase before it complete: V of the
-          // block kVSlots earlier is, once this block's S is, whose product
-          // is issued behind the PV of the block two earlier.
+          // block kVSlots earlier is there once this block's S is, as S of a
+          // stream waits for the PV of its block before: one of the last three.
           const int g = g0 + j, vs = g % kVSlots;
           ok = mbar_wait_sleep(&sm.qk_done[st][0], nqk & 1, fault, kFaultWaitMma, abort) &&
                mbar_wait_sleep(&sm.v_full[vs], (g / kVSlots) & 1, fault, kFaultWaitTma, abort);
