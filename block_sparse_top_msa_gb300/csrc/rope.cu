@@ -26,6 +26,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -427,14 +429,14 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t s) {
 }
 
 RopeBwdGrid rope_bwd_grid(long long tokens, int hq, int hkv) {
-  // Enough blocks to fill the GPU, shared between the sides by their rows, but
-  // no more than have a unit each.
+  // Enough blocks to fill the GPU, shared between the sides by their rows (each
+  // side with rows has one), but no more than have a unit each.
   constexpr long long kMost = 152 * kBwdResident;
   const long long uq = tokens * ((hq + kBwdRows - 1) / kBwdRows), uk = tokens * ((hkv + kBwdRows - 1) / kBwdRows);
   const long long bq = (uq + kTeams - 1) / kTeams, bk = (uk + kTeams - 1) / kTeams;
   RopeBwdGrid g{(int)bq, (int)bk};
   if (bq + bk > kMost) {
-    g.k_blocks = (int)((kMost * uk + uq + uk - 1) / (uq + uk));
+    g.k_blocks = (int)std::min((kMost * uk + uq + uk - 1) / (uq + uk), kMost - 1);
     g.q_blocks = (int)(kMost - g.k_blocks);
   }
   return g;

@@ -2,9 +2,10 @@
 import pytest
 import torch
 
+import test_gpu_qk_norm_rope as rope
 import test_gpu_tree_attention as tree
 from parity_util import fault_clear
-from step_util import DT, half_step, tree_attention
+from step_util import DT, half_step, norm_rope_bwd, tree_attention
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -114,3 +115,17 @@ def test_tree_gives_the_same_bits(msa, kv, hq, hkv, lo, hi):
         runs = [run() for _ in range(10)]
         assert all(torch.equal(o, first[0]) and torch.equal(l, first[1]) for o, l in runs)
     fault_clear(msa)
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 2048), (2048, 1), (4, 1300)])
+def test_gradient_of_unlike_head_counts(msa, hq, hkv):
+    """Both sides' gradients, where nearly all rows are of one side."""
+    tokens = 13
+    _, q, k, _, w, table, pos = rope.inputs(tokens, hq, hkv, 64, "bf16", seed=3, packed=False)
+    g = torch.Generator().manual_seed(8)
+    dq, dk = (torch.randn(t.shape, generator=g).to(t.dtype) for t in (q, k))
+    got = msa.msa_qk_norm_rope_bwd(*(t.to(DEV) for t in (dq, dk, q, k, w[0], w[1], table, pos)))
+    for i, (x, d) in enumerate(((q, dq), (k, dk))):
+        dx, mag, dw, terms = norm_rope_bwd(x, w[i], d, table, pos, False)
+        rope.near(got[i], dx, mag, x.dtype, rope.CHAIN_BWD)
+        assert ((got[2 + i].double().cpu() - dw).abs() <= rope.SUMS * terms).all()

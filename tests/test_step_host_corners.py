@@ -1,4 +1,5 @@
 """What can be told on the host about the serving step's operators at the edges of what their documentation allows (CPU only)."""
+import ctypes as C
 import glob
 import os
 import re
@@ -43,3 +44,24 @@ def test_dependent_kernels_wait_on_every_path():
         before = body[: m.start()]
         for r in re.finditer(r"return;", before):
             assert WAIT in enclosing_block(before, r.start()), (file, name, before[max(0, r.start() - 200) : r.end()])
+
+
+class Grid(C.Structure):
+    _fields_ = [("q_blocks", C.c_int), ("k_blocks", C.c_int)]
+
+
+def test_the_gradient_has_blocks_for_both_sides():
+    """However unlike the head counts: a side with tokens has a block, and the two no more than the workspace has rows for."""
+    import block_sparse_top_msa_gb300 as msa
+    msa.build()
+    L = msa.lib()
+    grid = getattr(L, "_ZN3msa13rope_bwd_gridExii")  # msa::rope_bwd_grid(long long, int, int)
+    grid.restype, grid.argtypes = Grid, [C.c_longlong, C.c_int, C.c_int]
+    for tokens in (1, 12, 100, 1000, 65536, 10**6):
+        for hq in (1, 4, 5, 64, 1300, 2048, 8192):
+            for hkv in (1, 2, 8, 1300, 2048, 8192):
+                g = grid(tokens, hq, hkv)
+                assert g.q_blocks >= 1 and g.k_blocks >= 1 and g.q_blocks + g.k_blocks <= 304, (tokens, hq, hkv, g.q_blocks, g.k_blocks)
+                assert L.msa_qk_norm_rope_bwd_workspace_size(tokens, hq, hkv) >= (g.q_blocks + g.k_blocks) * 512
+    g = grid(0, 64, 8)
+    assert g.q_blocks == 0 and g.k_blocks == 0
