@@ -117,24 +117,25 @@ constexpr int kScanPerThread = 16;  // page counts a thread reads per step of th
 
 enum { kDone = 0, kRefused = 1, kNoPage = 2 };
 
-// Exclusive sum over the block's threads and the total; s holds 33 ints.
-MSA_DEV int block_exclusive(int v, int* s, int& total) {
+// Exclusive sum over the block's threads and the total; s holds 33.
+template <class T>
+MSA_DEV T block_exclusive(T v, T* s, T& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int inc = v;
+  T inc = v;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int o = __shfl_up_sync(0xffffffffu, inc, d);
+    const T o = __shfl_up_sync(0xffffffffu, inc, d);
     if (lane >= d) inc += o;
   }
   __syncthreads();  // s may still be read from an earlier call
   if (lane == 31) s[warp] = inc;
   __syncthreads();
   if (warp == 0) {
-    const int w = s[lane];
-    int wi = w;
+    const T w = s[lane];
+    T wi = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, wi, d);
+      const T o = __shfl_up_sync(0xffffffffu, wi, d);
       if (lane >= d) wi += o;
     }
     s[lane] = wi - w;
@@ -158,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   extern __shared__ int smem[];
   int* claim = smem;                   // num_rows: the first request for the row
   int* need = claim + a.num_rows;      // n: pages wanted, or -1 refused
-  int* offset = need + a.n;            // n: pages granted before
+  int* offset = need + a.n;            // n: pages wanted before, INT_MAX at most
   int* scan = offset + a.n;            // 33
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int r = tid; r < a.num_rows; r += kPlanThreads) claim[r] = INT_MAX;
@@ -219,19 +220,21 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     }
   }
   __syncthreads();
-  // Pages wanted before each request.
-  int sum = 0;
+  // Pages wanted before each request, in 64 bits: a table's rows together may
+  // lack more than 2^31.
+  __shared__ long long scan64[33];
+  long long sum = 0;
   for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    int total;
-    const int before = block_exclusive(i < a.n ? max(0, need[i]) : 0, scan, total);
-    if (i < a.n) offset[i] = sum + before;
+    long long total;
+    const long long before = block_exclusive(i < a.n ? (long long)max(0, need[i]) : 0ll, scan64, total);
+    if (i < a.n) offset[i] = (int)min(sum + before, (long long)INT_MAX);
     sum += total;
   }
   // The first `sum` free pages, ascending: the next step's counts are on their
   // way while this one's free pages are numbered.
   int found = 0;
-  const int wanted = min(sum, a.num_pages);
+  const int wanted = (int)min(sum, (long long)a.num_pages);
   const bool quads = (reinterpret_cast<uintptr_t>(a.page_refs) & 15) == 0;
   int4 held[kScanPerThread / 4];
   const unsigned pages = (unsigned)a.num_pages;
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
   __syncthreads();
   for (int i = warp; i < a.n; i += kPlanThreads / 32) {
     const int want = need[i], o = offset[i];
-    const int st = want < 0 ? kRefused : (want > 0 && o + want > found) ? kNoPage : kDone;
+    const int st = want < 0 ? kRefused : (want > 0 && (long long)o + want > found) ? kNoPage : kDone;
     if (lane == 0) a.status[i] = st;
     if (FORK) {
       const int page = st == kDone && want > 0 ? a.list[o] : -1;

@@ -129,3 +129,20 @@ def test_gradient_of_unlike_head_counts(msa, hq, hkv):
         dx, mag, dw, terms = norm_rope_bwd(x, w[i], d, table, pos, False)
         rope.near(got[i], dx, mag, x.dtype, rope.CHAIN_BWD)
         assert ((got[2 + i].double().cpu() - dw).abs() <= rope.SUMS * terms).all()
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+def test_rows_that_lack_more_pages_than_an_int_counts(msa):
+    """2^24 pages wanted by each of 130 rows: the sum is past 2^31. None is granted, those that need none are done."""
+    rows = 132
+    table = torch.full((rows, 1 << 24), -1, dtype=torch.int32, device=DEV)
+    used, refs = torch.zeros(rows, dtype=torch.int32, device=DEV), torch.zeros(100, dtype=torch.int32, device=DEV)
+    lengths = [0] + [2**31 - 1] * 130 + [1]
+    status = msa.msa_cache_extend(table, used, refs, i32(range(rows)), i32(lengths))
+    assert status.tolist() == [0] + [2] * 131
+    assert (used == 0).all() and (refs == 0).all() and int(table.max()) == -1
+    assert msa.msa_cache_extend(table, used, refs, i32([131, 130]), i32([1, 129])).tolist() == [0, 0]
+    assert refs[:4].tolist() == [1, 1, 1, 0] and table[131, :2].tolist() == [0, -1] and table[130, :3].tolist() == [1, 2, -1]
