@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kPlanThreads) cache_plan_kernel(const __grid_c
     } else if (st == kDone) {
       const int r = a.rows[i], len = a.lengths[i];
       int32_t* row = a.page_table + (size_t)r * a.max_pages;
-      const int last = (len + kBlk - 1) / kBlk;
+      const int last = (int)(((long long)len + kBlk - 1) / kBlk);
       int k = o;
       for (int t0 = max(0, a.seqused_k[r]) / kBlk; t0 < last; t0 += 32) {
         const bool take = t0 + lane < last && row[min(t0 + lane, last - 1)] < 0;

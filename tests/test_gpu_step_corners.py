@@ -135,6 +135,18 @@ def i32(x):
     return torch.tensor(x, dtype=torch.int32, device=DEV)
 
 
+def test_extend_to_the_longest_row(msa):
+    """A row that ends within the last 128 tokens of what an int counts gets its last pages."""
+    table = torch.full((1, 1 << 24), -1, dtype=torch.int32, device=DEV)
+    used, refs = i32([2**31 - 300]), torch.zeros(5, dtype=torch.int32, device=DEV)
+    first = (2**31 - 300) // 128
+    table[0, first] = 4
+    refs[4] = 1
+    assert msa.msa_cache_extend(table, used, refs, i32([0]), i32([2**31 - 1])).tolist() == [0]
+    assert used.tolist() == [2**31 - 1] and refs.tolist() == [1, 1, 0, 0, 1]
+    assert table[0, first - 2 :].tolist() == [-1, -1, 4, 0, 1]
+
+
 def test_rows_that_lack_more_pages_than_an_int_counts(msa):
     """2^24 pages wanted by each of 130 rows: the sum is past 2^31. None is granted, those that need none are done."""
     rows = 132
