@@ -2,6 +2,7 @@
 import pytest
 import torch
 
+import test_gpu_cache_pages as pages
 import test_gpu_qk_norm_rope as rope
 import test_gpu_tree_attention as tree
 from parity_util import fault_clear
@@ -158,3 +159,14 @@ def test_rows_that_lack_more_pages_than_an_int_counts(msa):
     assert (used == 0).all() and (refs == 0).all() and int(table.max()) == -1
     assert msa.msa_cache_extend(table, used, refs, i32([131, 130]), i32([1, 129])).tolist() == [0, 0]
     assert refs[:4].tolist() == [1, 1, 1, 0] and table[131, :2].tolist() == [0, -1] and table[130, :3].tolist() == [1, 2, -1]
+
+
+def test_fork_of_whole_pages_with_the_first_page_free(msa):
+    """A source that ends with its page has no begun one: the free page 0 goes to the first fork that needs one, and holds the copy of
+    its source's begun page."""
+    c = pages.Both(msa, 7, 4, 12)
+    c.extend([0, 1, 2, 3], [1, 256, 300, 128])
+    c.free([0])
+    assert c.plain.refs[0] == 0
+    assert c.fork([1, 2, 3, 2], [4, 5, 0, 6]) == [0, 0, 0, 0]
+    assert c.plain.table[5][2] == 0 and torch.equal(c.gpu_pools[0][0], c.gpu_pools[0][c.plain.table[2][2]])
