@@ -617,7 +617,10 @@ def _step():
     global _native
     if _native is None:
         lib()
-        from . import _binding as module
+        try:
+            from . import _binding as module
+        except ImportError as e:
+            raise RuntimeError(f"_binding.so is not built, or not for this torch ({e}); build() says why") from e
         module.set_error(MSAError)
         _native = module
     return _native
