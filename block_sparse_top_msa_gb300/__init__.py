@@ -694,6 +694,10 @@ class TreeAttentionRunner(SparseAttentionRunner):
         self._plan = C.c_void_p(plan)
         self._lib = lib()
 
+    def run(self, stream=None):
+        with torch.cuda.device(self.out.device):  # the tensors' device, current or not
+            return super().run(stream)
+
 
 def msa_cache_extend(page_table, seqused_k, page_refs, rows, lengths, *, status=None,
                      workspace=None, stream=None):

@@ -3,6 +3,7 @@ import ctypes as C
 import glob
 import os
 import re
+import types
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 WAIT = "grid_dependency_wait();"
@@ -65,3 +66,37 @@ def test_the_gradient_has_blocks_for_both_sides():
                 assert L.msa_qk_norm_rope_bwd_workspace_size(tokens, hq, hkv) >= (g.q_blocks + g.k_blocks) * 512
     g = grid(0, 64, 8)
     assert g.q_blocks == 0 and g.k_blocks == 0
+
+
+def test_a_prepared_tree_call_runs_on_its_own_device(monkeypatch):
+    """Tensors on another device than the current one: that device is made current and its stream taken."""
+    import torch
+
+    import block_sparse_top_msa_gb300 as msa
+    at, launched = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            at.append(self.device.index)
+
+        def __exit__(self, *a):
+            at.pop()
+
+    class Library:
+        msa_sparse_attention_plan_free = staticmethod(lambda plan: None)
+
+        @staticmethod
+        def msa_sparse_attention_run(plan, stream):
+            launched.append((at[-1], stream.value))
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=100 + at[-1]))
+    r = msa.TreeAttentionRunner.__new__(msa.TreeAttentionRunner)
+    r.out, r.lse, r._lib, r._plan = types.SimpleNamespace(device=torch.device("cuda", 3)), None, Library, C.c_void_p(1)
+    assert r.run() is r.out
+    r.run(stream=77)
+    assert launched == [(3, 103), (3, 77)] and at == [0]
