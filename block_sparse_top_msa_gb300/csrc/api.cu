@@ -8,8 +8,6 @@
 #include <cmath>
 #include <mutex>
 #include <new>
-#include <tuple>
-#include <vector>
 
 #include "../../include/msa.h"
 #include "internal.h"
@@ -281,20 +279,26 @@ cudaError_t set_smem_limit(const void* kernel, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  // Under the lock to its end: a call that needs less must not lower the limit
+  // that another thread has just raised for its launch.
   static std::mutex mu;
-  static std::vector<std::tuple<const void*, int, int>> done;
-  {
-    std::lock_guard<std::mutex> lk(mu);
-    for (const auto& t : done)
-      if (std::get<0>(t) == kernel && std::get<1>(t) == dev && std::get<2>(t) >= bytes)
-        return cudaSuccess;
-  }
+  static struct {
+    const void* kernel;
+    int dev, bytes;
+  } done[256];
+  static int n = 0;
+  std::lock_guard<std::mutex> lk(mu);
+  int i = 0;
+  while (i < n && !(done[i].kernel == kernel && done[i].dev == dev)) ++i;
+  if (i < n && done[i].bytes >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) {
-    std::lock_guard<std::mutex> lk(mu);
-    done.emplace_back(kernel, dev, bytes);
+  if (e != cudaSuccess) {
+    cudaGetLastError();  // reported here, not by a later call
+    return e;
   }
-  return e;
+  if (i == n && n < 256) ++n;
+  if (i < n) done[i] = {kernel, dev, bytes};
+  return cudaSuccess;
 }
 
 int device_smem_optin() {

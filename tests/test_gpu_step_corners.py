@@ -1,4 +1,7 @@
 """Calls of the serving step's operators at the edges of what their documentation allows."""
+import ctypes as C
+import threading
+
 import pytest
 import torch
 
@@ -170,3 +173,34 @@ def test_fork_of_whole_pages_with_the_first_page_free(msa):
     assert c.plain.refs[0] == 0
     assert c.fork([1, 2, 3, 2], [4, 5, 0, 6]) == [0, 0, 0, 0]
     assert c.plain.table[5][2] == 0 and torch.equal(c.gpu_pools[0][0], c.gpu_pools[0][c.plain.table[2][2]])
+
+
+def test_calls_of_several_threads_at_once(msa):
+    """Calls that need different amounts of shared memory, each thread on its stream with its own tables: none fails to launch."""
+    L = msa.lib()
+    sizes = [range(8000 + i, 16384, 7) for i in range(4)]
+    state, bad = [], []
+    for i in range(4):
+        most = 16384
+        state.append((torch.full((most, 1), -1, dtype=torch.int32, device=DEV), torch.zeros(most, dtype=torch.int32, device=DEV),
+                      torch.zeros(64, dtype=torch.int32, device=DEV), i32([3]), i32([100]), i32([9]),
+                      torch.empty(4096, dtype=torch.uint8, device=DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def calls(i):
+        table, used, refs, rows, lengths, status, ws, stream = state[i]
+        p = [C.c_void_p(t.data_ptr()) for t in (table, used, refs, rows, lengths, status, ws)]
+        for n in sizes[i]:
+            st = L.msa_cache_extend(p[0], 1, n, p[1], p[2], 64, p[3], p[4], 1, p[5], p[6], 4096, C.c_void_p(stream.cuda_stream))
+            if st != 0:
+                bad.append((i, n, st))
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad
+    for table, used, refs, _, _, status, _, _ in state:
+        assert status.tolist() == [0] and used[3].item() == 100 and table[3].tolist() == [0] and int(refs.sum()) == 1
