@@ -44,6 +44,22 @@ msa_status_t check_pools(void* const* pools, int num_pools, long long bytes, int
   return MSA_OK;
 }
 
+// What two of the pools have in common, of kApart (nothing), kSame (two are one
+// pool) and kOverlap (two share a part) the last that is found.
+enum PoolsShare { kApart, kSame, kOverlap };
+PoolsShare pools_share(void* const* pools, int num_pools, uint64_t pool_bytes) {
+  auto gap = [&](int i, int j) { return (uint64_t)(static_cast<uint8_t*>(pools[i]) - static_cast<uint8_t*>(pools[j])); };
+  int i = 1;  // ascending pools, as slices of one allocation are, need one comparison each
+  while (i < num_pools && pools[i] > pools[i - 1] && gap(i, i - 1) >= pool_bytes) ++i;
+  PoolsShare found = kApart;
+  for (; i < num_pools; ++i)
+    for (int j = 0; j < i; ++j) {
+      if (pools[i] == pools[j]) found = found == kOverlap ? kOverlap : kSame;
+      else if ((pools[i] > pools[j] ? gap(i, j) : gap(j, i)) < pool_bytes) found = kOverlap;
+    }
+  return found;
+}
+
 // Calls launch(pools, count) for the pools in groups of what one launch takes.
 template <class F>
 cudaError_t for_pools(void* const* pools, int num_pools, F launch) {
@@ -207,6 +223,7 @@ msa_status_t msa_cache_fork(void* const* pools, int num_pools, long long page_by
   a.status = status;
   st = place_plan(&a, workspace, workspace_bytes);
   if (st != MSA_OK) return st;
+  if (pools_share(pools, num_pools, (uint64_t)page_bytes * num_pages) == kOverlap) return MSA_INVALID_ARG;
   cudaError_t e = launch_cache_fork(a, stream);
   bool tables = true;
   if (e == cudaSuccess)
@@ -240,6 +257,7 @@ msa_status_t msa_cache_copy_pages(void* const* pools, int num_pools, long long p
   if (n > kMaxCopyPairs) return MSA_UNSUPPORTED;
   if (n == 0) return MSA_OK;
   if (!aligned(src_pages, 4) || !aligned(dst_pages, 4)) return MSA_INVALID_ARG;
+  if (pools_share(pools, num_pools, (uint64_t)page_bytes * num_pages) == kOverlap) return MSA_INVALID_ARG;
   return from_cuda(for_pools(pools, num_pools, [&](const CachePools& p, int count) {
     return launch_cache_copy_pages(p, count, page_bytes, num_pages, src_pages, dst_pages, n, stream);
   }));
@@ -258,9 +276,8 @@ msa_status_t msa_cache_accept(void* const* pools, int num_pools, int row_bytes, 
     return MSA_INVALID_ARG;
   if (batch > kMaxCacheRows || num_kv_heads > 1024 || row_bytes > 4096) return MSA_UNSUPPORTED;
   // A pool's rows move once: a pool given twice would read moved rows.
-  for (int i = 1; i < num_pools; ++i)
-    for (int j = 0; j < i; ++j)
-      if (pools[i] == pools[j]) return MSA_INVALID_ARG;
+  if (pools_share(pools, num_pools, (uint64_t)row_bytes * num_kv_heads * 128 * num_pages) != kApart)
+    return MSA_INVALID_ARG;
   CacheAcceptArgs a{};
   a.row_bytes = row_bytes, a.hkv = num_kv_heads;
   a.page_table = page_table, a.max_pages = max_pages, a.num_pages = num_pages, a.batch = batch;

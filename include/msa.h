@@ -350,7 +350,8 @@ msa_status_t msa_qk_norm_rope_bwd(
  *
  * `pools` is a host array of num_pools device pointers: the K and V pools of
  * every layer, which share one page numbering, each num_pages pages of
- * page_bytes contiguous bytes (a multiple of 16). Sequences are rows of
+ * page_bytes contiguous bytes (a multiple of 16); two that share only a part
+ * of their memory are MSA_INVALID_ARG. Sequences are rows of
  * page_table (num_rows, max_pages), -1 where a row has no page, with their
  * lengths seqused_k; page_refs (num_pages) counts the entries that name each
  * page, and a page whose count is 0 is free. A caller starts with -1, 0 and 0.

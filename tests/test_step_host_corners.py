@@ -100,3 +100,23 @@ def test_a_prepared_tree_call_runs_on_its_own_device(monkeypatch):
     assert r.run() is r.out
     r.run(stream=77)
     assert launched == [(3, 103), (3, 77)] and at == [0]
+
+
+def test_pools_that_share_a_part_of_their_memory_are_refused():
+    """In ascending order and in any other; the same pool twice is refused where rows move, and copied twice elsewhere."""
+    import block_sparse_top_msa_gb300 as msa
+    msa.build()
+    L = msa.lib()
+    P, INVALID = C.c_void_p(0x10000), 1
+    pages, page = 4, 1 << 20
+
+    def calls(*at):
+        pools, n = (C.c_void_p * len(at))(*at), len(at)
+        yield L.msa_cache_fork(pools, n, page, P, 4, 8, P, P, pages, P, P, 1, P, P, 1 << 20, None)
+        yield L.msa_cache_copy_pages(pools, n, page, pages, P, P, 1, None)
+        yield L.msa_cache_accept(pools, n, 256, page // 256 // 128, P, 4, pages, 1, P, P, P, P, 3, C.c_void_p(0x20000), None)
+
+    base = 1 << 32
+    for at in ([0, 3], [3, 0], [0, 4, 8, 11], [8, 0, 4, 5], [0, 4, 3], [4, 4, 7]):
+        assert list(calls(*[base + x * page for x in at])) == [INVALID] * 3, at
+    assert list(calls(base, base + 4 * page - 16)) == [INVALID] * 3
