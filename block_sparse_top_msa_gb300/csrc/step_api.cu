@@ -203,7 +203,9 @@ msa_status_t msa_cache_extend(int32_t* page_table, int max_pages, int num_rows, 
   a.page_table = page_table, a.max_pages = max_pages, a.num_rows = num_rows, a.num_pages = num_pages;
   a.seqused_k = seqused_k, a.page_refs = page_refs, a.rows = rows, a.lengths = lengths, a.n = n, a.status = status;
   st = place_plan(&a, workspace, workspace_bytes);
-  return st != MSA_OK ? st : from_cuda(launch_cache_extend(a, stream));
+  if (st != MSA_OK) return st;
+  if (status == rows || status == lengths) return MSA_INVALID_ARG;  // written while others are read
+  return from_cuda(launch_cache_extend(a, stream));
 }
 
 msa_status_t msa_cache_fork(void* const* pools, int num_pools, long long page_bytes,
@@ -223,6 +225,7 @@ msa_status_t msa_cache_fork(void* const* pools, int num_pools, long long page_by
   a.status = status;
   st = place_plan(&a, workspace, workspace_bytes);
   if (st != MSA_OK) return st;
+  if (status == src_rows || status == dst_rows) return MSA_INVALID_ARG;  // written while others are read
   if (pools_share(pools, num_pools, (uint64_t)page_bytes * num_pages) == kOverlap) return MSA_INVALID_ARG;
   cudaError_t e = launch_cache_fork(a, stream);
   bool tables = true;
@@ -272,7 +275,7 @@ msa_status_t msa_cache_accept(void* const* pools, int num_pools, int row_bytes, 
   if (st != MSA_OK) return st;
   if (num_kv_heads < 1 || max_pages < 1 || batch < 1 || max_path < 1) return MSA_INVALID_ARG;
   if (!aligned(page_table, 4) || !aligned(seqused_k, 4) || !aligned(cu_seqlens_q, 4) || !aligned(path, 4) ||
-      !aligned(path_len, 4) || !aligned(seqused_out, 4) || seqused_out == seqused_k)
+      !aligned(path_len, 4) || !aligned(seqused_out, 4) || seqused_out == seqused_k || seqused_out == path_len)
     return MSA_INVALID_ARG;
   if (batch > kMaxCacheRows || num_kv_heads > 1024 || row_bytes > 4096) return MSA_UNSUPPORTED;
   // A pool's rows move once: a pool given twice would read moved rows.

@@ -358,7 +358,8 @@ msa_status_t msa_qk_norm_rope_bwd(
  * A request that cannot be carried out changes nothing and says so in
  * status (device int32, one per request): 0 done, 1 refused, 2 no free page.
  * Free pages are handed out lowest first, in the order of the requests; once
- * one finds too few, none after it gets any. num_rows and the number of
+ * one finds too few, none after it gets any. status is another array than the
+ * requests' (MSA_INVALID_ARG). num_rows and the number of
  * requests are at most 16384 (MSA_UNSUPPORTED above).
  *
  * msa_cache_extend: row rows[i] grows to lengths[i] tokens: a page for each
@@ -384,8 +385,8 @@ msa_status_t msa_qk_norm_rope_bwd(
  *   are not moved. Pools are (num_pages, Hkv, 128, row_bytes) with row_bytes a
  *   multiple of 16 (256 for 16-bit and 128 for E4M3 caches of head_dim 128;
  *   planar NVFP4 pages are not made of rows and cannot be given here).
- *   seqused_out is another array than seqused_k, and no pool is given twice
- *   (MSA_INVALID_ARG). The request's last pages must be its own (as extend and
+ *   seqused_out is another array than seqused_k and path_len, and no pool is
+ *   given twice (MSA_INVALID_ARG). The request's last pages must be its own (as extend and
  *   fork leave them).
  * workspace of msa_cache_fork and msa_cache_extend: as their size query says,
  * 256-byte aligned, uninitialised; calls that share one, or the same tables,

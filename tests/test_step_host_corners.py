@@ -112,7 +112,7 @@ def test_pools_that_share_a_part_of_their_memory_are_refused():
 
     def calls(*at):
         pools, n = (C.c_void_p * len(at))(*at), len(at)
-        yield L.msa_cache_fork(pools, n, page, P, 4, 8, P, P, pages, P, P, 1, P, P, 1 << 20, None)
+        yield L.msa_cache_fork(pools, n, page, P, 4, 8, P, P, pages, P, P, 1, C.c_void_p(0x20000), P, 1 << 20, None)
         yield L.msa_cache_copy_pages(pools, n, page, pages, P, P, 1, None)
         yield L.msa_cache_accept(pools, n, 256, page // 256 // 128, P, 4, pages, 1, P, P, P, P, 3, C.c_void_p(0x20000), None)
 
@@ -120,3 +120,16 @@ def test_pools_that_share_a_part_of_their_memory_are_refused():
     for at in ([0, 3], [3, 0], [0, 4, 8, 11], [8, 0, 4, 5], [0, 4, 3], [4, 4, 7]):
         assert list(calls(*[base + x * page for x in at])) == [INVALID] * 3, at
     assert list(calls(base, base + 4 * page - 16)) == [INVALID] * 3
+
+
+def test_results_in_the_place_of_what_is_read_are_refused():
+    import block_sparse_top_msa_gb300 as msa
+    msa.build()
+    L = msa.lib()
+    P, Q, R, INVALID = C.c_void_p(0x10000), C.c_void_p(0x20000), C.c_void_p(0x30000), 1
+    pools = (C.c_void_p * 1)(1 << 32)
+    for status in (P, Q):
+        assert L.msa_cache_extend(R, 4, 8, R, R, 10, P, Q, 1, status, R, 1 << 20, None) == INVALID
+        assert L.msa_cache_fork(pools, 1, 64, R, 4, 8, R, R, 10, P, Q, 1, status, R, 1 << 20, None) == INVALID
+    for out in (P, Q):
+        assert L.msa_cache_accept(pools, 1, 256, 2, R, 4, 10, 1, P, R, R, Q, 3, out, None) == INVALID
