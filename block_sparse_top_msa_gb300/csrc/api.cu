@@ -742,6 +742,7 @@ msa_status_t build_tree(
   if (workspace == nullptr || workspace_bytes < L.total) return MSA_WORKSPACE_TOO_SMALL;
   plan->empty = total_q == 0;
   if (plan->empty) return MSA_OK;
+  if (out == q) return MSA_INVALID_ARG;  // rows that are not finite read Q again
   unsigned* fault = fault_word();
   if (fault == nullptr) return MSA_CUDA_ERROR;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

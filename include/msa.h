@@ -245,7 +245,7 @@ msa_status_t msa_sparse_attention_nvfp4_prepare(
  * What a token does not see may hold anything, infinities and NaN included:
  * rows past seqused_k, blocks that it does not list, other drafts. A token
  * that sees a NaN gets NaN. A NULL or misaligned tree_mask, a NULL
- * page_table or too few words: MSA_INVALID_ARG; max_pages above 2^18:
+ * page_table, too few words or q as out: MSA_INVALID_ARG; max_pages above 2^18:
  * MSA_UNSUPPORTED; otherwise as the forward.
  * msa_tree_attention_prepare binds the call into a plan that
  * msa_sparse_attention_run launches. Rows at or past cu_seqlens_q[B] are left

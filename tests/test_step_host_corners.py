@@ -133,3 +133,5 @@ def test_results_in_the_place_of_what_is_read_are_refused():
         assert L.msa_cache_fork(pools, 1, 64, R, 4, 8, R, R, 10, P, Q, 1, status, R, 1 << 20, None) == INVALID
     for out in (P, Q):
         assert L.msa_cache_accept(pools, 1, 256, 2, R, 4, 10, 1, P, R, R, Q, 3, out, None) == INVALID
+    tree = lambda out: L.msa_tree_attention(P, 0, Q, Q, 0, R, 4, R, R, 1, R, 4, 4, R, 1, 5, 8, 2, 128, 5, 0.0, out, None, R, 1 << 30, None)
+    assert tree(P) == INVALID
