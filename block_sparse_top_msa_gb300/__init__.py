@@ -607,7 +607,9 @@ def msa_selftest_wait_timeout(timeout_us, stream=None):
 # dtypes and devices that do not fit raise ValueError or TypeError before
 # anything is launched. All tensors of a call are on one device, which need
 # not be the current one; ``stream`` defaults to that device's current stream,
-# and outputs and workspaces are allocated on the stream the call runs on.
+# and outputs and workspaces are allocated on the stream the call runs on. The
+# calls take no part in autograd: an output of inputs that require a gradient
+# has none, and msa_qk_norm_rope_bwd gives the one of msa_qk_norm_rope.
 # --------------------------------------------------------------------------
 _native = None
 
@@ -634,7 +636,8 @@ def msa_qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, *, eps=1e-6, 
     ``q`` (T, Hq, 128) and ``k`` (T, Hkv, 128) may be slices of a packed
     projection. ``cos_sin`` (max_position, rotary_dim) float32 holds each
     position's cosines and then its sines; None only normalises. Returns
-    ``(q_out, k_out)``, contiguous.
+    ``(q_out, k_out)``, contiguous and without a gradient of their own
+    (``msa_qk_norm_rope_bwd`` computes it).
     """
     return (_native or _step()).qk_norm_rope(q, k, q_weight, k_weight, cos_sin, positions, eps,
                                               interleaved, q_out, k_out, stream)
@@ -668,8 +671,8 @@ def msa_tree_attention(q, k, v, q2k_indices, cu_seqlens_q, tree_mask, *, page_ta
                        lse=None, workspace=None, stream=None):
     """Attention of drafted tokens in trees over a paged cache; see
     ``msa_tree_attention`` in include/msa.h. ``tree_mask`` (Tq, words) int32
-    holds each token's visible nodes as bits. Returns ``out`` or ``(out,
-    lse)``. ``max_seqlen_q=None`` reads the device as the forward does."""
+    holds each token's visible nodes as bits. ``q`` is contiguous. Returns
+    ``out`` or ``(out, lse)``. ``max_seqlen_q=None`` reads the device as the forward does."""
     if max_seqlen_q is None:
         max_seqlen_q = _q_bound(cu_seqlens_q, q.shape[0])
     out, lse, _, _ = (_native or _step()).tree_attention(

@@ -4,8 +4,8 @@
 // takes a few microseconds on the GPU for a decode step, less than checking a
 // dozen tensors does in Python, hence a compiled binding: against the same
 // checks in Python with ctypes, an append of four tokens (64 query heads, 4 KV
-// heads) went from 52 to 19 us, slicing its inputs included, its kernel being
-// 5.5 us.
+// heads) went from 52 to 21 us, 16 of which are the caller's slicing of its
+// inputs; its kernel is 4.0 us.
 //
 // Arguments come by position from the Python functions that document them.
 #define PY_SSIZE_T_CLEAN

@@ -18,11 +18,11 @@
 //
 // The kernels are bound by memory, if the arithmetic is kept down (one
 // operation at a time instead of pairs: 17 instructions an element, 58% of the
-// issue slots, 221 us and 313 us) and loads are not held up: forward 65536
-// tokens of 32 + 4 heads (1.24 GB in and out) take 199 us, 92% of the measured
-// copy bandwidth; backward 32768 of 64 + 8 (1.82 GB) 291 us, 92%. 16-byte
-// accesses by 8 lanes a row were slower (225, 307), as were loads one unit
-// ahead in the backward (350: its registers).
+// issue slots, a tenth slower) and loads are not held up: forward 65536 tokens
+// of 32 + 4 heads (1.24 GB in and out) take 200 us, 91% of the measured copy
+// bandwidth; backward 32768 of 64 + 8 (1.82 GB) 285 us, 94%. 16-byte accesses by
+// 8 lanes a row were slower (by 12% and 5%), as were loads one unit ahead in the
+// backward (by a fifth: its registers).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -395,9 +395,9 @@ __global__ void __launch_bounds__(1024) rope_bwd_sum_kernel(const __grid_constan
   }
 }
 
-// Heads of a token in flight per team. Forward 4 / 6 / 8: 203 / 199 / 202 us on
-// the size above. Backward, with the blocks an SM holds: 1 row 373, 2 rows 329
-// (4 blocks), 4 rows 292 (2 blocks); more blocks than an SM holds gain nothing.
+// Heads of a token in flight per team. Forward 4 / 6 / 8: 208 / 200 / 204 us on
+// the size above. Backward, with the blocks an SM holds: 1 row 363, 2 rows 337
+// (4 blocks), 4 rows 285 (2 blocks); more blocks than an SM holds gain nothing.
 constexpr int kFwdRows = 6, kAppendRows = 4;
 constexpr int kBwdRows = 4;
 

@@ -5,9 +5,9 @@
 // the union of its tokens' listed blocks, each row to its own blocks and to
 // the drafts its mask names. Drafts of one request choose much the same
 // blocks, so a block is brought to shared memory once for both tiles: that
-// halves the cache traffic and the E4M3 conversions (units of one tile: 84 us
-// against 73 for 32 requests of 16 tokens with 64 query heads, 4 KV heads and
-// 16 listed blocks, 376 against 351 for 128 E4M3 requests of 8 to 32 tokens;
+// halves the cache traffic and the E4M3 conversions (units of one tile: 78 us
+// against 64 for 32 requests of 16 tokens with 64 query heads, 4 KV heads and
+// 16 listed blocks, 376 against 305 for 128 E4M3 requests of 8 to 32 tokens;
 // the figures below are of these two).
 //
 // The units' blocks, laid end to end, are cut into equal ranges, one per CTA
@@ -15,18 +15,19 @@
 // the units. A segment that is a whole unit writes its output, the others
 // leave (m, l, O) partials that merge_tree_kernel joins. Where whole units
 // load the CTAs nearly as evenly (within cut_cost blocks), a unit goes whole
-// to the CTA whose range it begins in: the 32 requests take 73 us so, and 89
+// to the CTA whose range it begins in: the 32 requests take 64 us so, and 81
 // with ranges cut. The unions' lengths are known on the device only: every CTA
 // sums them (tree_union_kernel leaves one per unit), comes to the same choice
 // and finds its own range.
 //
 // What bounds it: no unit, but the latency of a block's chain (S, its maxima,
 // P, the products) by two streams of four warps, and what passes between two
-// units. A block of two tiles takes 4100 to 4400 clocks, its products 2350; with
-// E4M3 the tensor cores are busy 38% of the time, the issue slots 42%, memory
-// 22%. The products of the unions would take 132 us of the 344, on the 32
-// requests 27 of the 72, where random pages take 42. Waits are by
-// mbar_wait_sleep, as spinning takes issue slots too (354 us against 351).
+// units. A block of two tiles takes 3500 clocks, its products 2350, and 11 to 17
+// thousand pass between the last block of a unit and the next one's first; with
+// E4M3 the tensor cores are busy 44% of the time, the issue slots 43%, memory
+// 25%. The products of the unions would take 132 us of the 305, on the 32
+// requests 27 of the 64, where random pages take 42. Waits are by
+// mbar_wait_sleep (spinning: 302 and 65 us).
 //
 // Two streams of (QK^T, softmax, PV) keep the tensor cores busy: while one
 // stream's softmax warps turn its S into P, the other's products run. With
@@ -40,12 +41,12 @@
 // caches warps 12-15 decode K and V into the swizzled layout the MMA reads. Two
 // warps issue, as one that does both, waiting for each PV before the S that
 // takes its P's place, spends 1050 clocks a product and is the slowest of all
-// (128 E4M3 requests 393 us against 302, 32 bf16 requests 83 against 63).
+// (128 E4M3 requests 393 us against 305, 32 bf16 requests 83 against 64).
 // Keys past a sequence's end are masked in S, and their V rows zeroed in
 // shared memory, as P = 0 times what a page may hold there need not be 0.
 //
 // E4M3 is decoded to f16, exactly, NaN codes included, by one conversion a
-// pair (moving the bits by integer instructions: 372 us against 352). Q then
+// pair (moving the bits by integer instructions took 6% longer). Q then
 // is f16 too, each bf16 row scaled by the power of two that puts its largest
 // value just below f16's largest (what falls below f16's range is under 2^-39
 // of that); the power of two comes back with the softmax scale.
@@ -150,8 +151,8 @@ MSA_DEV int first_block(long long p0, long long c, int w, int len) {
 }
 
 // What a block costs a CTA, by the unit's tiles: bringing and decoding it is
-// the same, but two tiles multiply twice (128 E4M3 requests: 351 us with 3 to
-// 4, 366 with equal weights, 365 with 2 to 4).
+// the same, but two tiles multiply twice (128 E4M3 requests: 305 us with 3 to
+// 4, 318 with equal weights, 320 with 2 to 4).
 constexpr int kOneTileWeight = 3, kTwoTileWeight = 4;
 MSA_DEV int unit_weight(const TreeArgs& a, int tokens) {
   return tokens > a.tile_tokens ? kTwoTileWeight : kOneTileWeight;
@@ -388,7 +389,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
   constexpr bool kF16Ops = FP8 || F16;  // the MMAs' operands are f16, else bf16
   // Columns of S a softmax thread holds: 64 are read once; in the E4M3 kernel
   // they would spill, and the smaller code matters too (its roles share the
-  // instruction cache): 32, read twice, are 6% faster there and 3% slower in
+  // instruction cache): 32, read twice, are 5% faster there and 5% slower in
   // the others.
   constexpr int kCols = FP8 ? 32 : 64;
   using R = Roles<FP8>;
@@ -650,8 +651,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     // Two tiles: both streams take every block. One tile: block j is stream
     // j & 1's. Either way the products go by halves of a block's keys, under
     // the softmax of the other half. (By whole blocks a stream's softmax and
-    // products ran one after the other, 3700 clocks a block of two tiles
-    // where the products take 2350.)
+    // products ran one after the other, and neither hid the other.)
     const bool is_qk = warp == R::kQk;
     const uint32_t el = elect_one();
     const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
@@ -1367,8 +1367,8 @@ __device__ __noinline__ void odd_row(const TreeArgs& a, size_t orow, int lane) {
 // of four columns; kMergeChunk partials at a time, whose weights go through
 // shared memory while their O are on the way. Odd rows are computed here too:
 // those that whole units listed, and those that joining finds. Two blocks an
-// SM, two partials ahead: 343.5, 72.6 and 23.7 us for 128 E4M3 requests, 32 and
-// one, against 347.3, 73.0 and 24.8 with blocks of 64 rows, one an SM, and four
+// SM, two partials ahead: 305, 63.5 and 21.8 us for 128 E4M3 requests, 32 and
+// one, against 310, 65.2 and 22.3 with blocks of 64 rows, one an SM, and four
 // partials ahead.
 constexpr int kMergeRows = 32, kMergeThreads = 8 * kMergeRows, kMergeAhead = 2, kMergeChunk = 16;
 __global__ void __launch_bounds__(kMergeThreads, 2)
