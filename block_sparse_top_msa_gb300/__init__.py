@@ -21,7 +21,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -29,7 +29,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmsa.so")
 
 MSA_OK, MSA_INVALID_ARG, MSA_UNSUPPORTED, MSA_WORKSPACE_TOO_SMALL, MSA_CUDA_ERROR = range(5)
-MSA_BF16, MSA_FP16, MSA_FP8_E4M3 = 0, 1, 2
+MSA_BF16, MSA_FP16, MSA_FP8_E4M3, MSA_FP32 = range(4)
 
 _lib = None
 
@@ -118,6 +118,16 @@ def lib():
         L.msa_cache_accept.restype = i32
         L.msa_cache_accept.argtypes = [C.POINTER(vp), i32, i32, i32, vp, i32, i32, i32, vp, vp, vp,
                                        vp, i32, vp, vp]
+        L.msa_step_tables_workspace_size.restype = sz
+        L.msa_step_tables_workspace_size.argtypes = [i32]
+        L.msa_step_tables.restype = i32
+        L.msa_step_tables.argtypes = [vp, i32, i32, vp, i32, vp, vp, i32, i32] + [vp] * 10 + [sz, vp]
+        L.msa_sample.restype = i32
+        L.msa_sample.argtypes = [vp, i32, i64, i32, i32] + [vp] * 8 + [sz, vp]
+        L.msa_sample_workspace_size.restype = sz
+        L.msa_sample_workspace_size.argtypes = [i32, i32]
+        L.msa_draft_path.restype = i32
+        L.msa_draft_path.argtypes = [vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, vp]
         L.msa_proxy_score.restype = i32
         L.msa_proxy_score.argtypes = [
             vp, i32, vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, i32, i32, i32,
@@ -740,3 +750,50 @@ def msa_cache_accept(pools, page_table, seqused_k, cu_seqlens_q, path, path_len,
     ``seqused_out`` (B,) int32, the lengths after it."""
     return (_native or _step()).cache_accept(pools, page_table, seqused_k, cu_seqlens_q, path,
                                               path_len, seqused_out, stream)
+
+
+class StepTables(NamedTuple):
+    """What ``msa_step_tables`` returns; the names are those of the arguments
+    that take them."""
+    cu_seqlens_q: torch.Tensor
+    seqused_k: torch.Tensor
+    page_table: torch.Tensor
+    token_rows: torch.Tensor
+    positions: torch.Tensor
+    slots: torch.Tensor
+    group_rows: torch.Tensor
+    cu_groups: torch.Tensor
+    group_blocks: torch.Tensor
+
+
+def msa_step_tables(page_table, seqused_k, rows, new_lens, *, total_q, num_pages, out=None,
+                    workspace=None, stream=None):
+    """The tables of a step from its requests' lengths: requests are the rows
+    ``rows`` (B,) int32 of a cache's ``page_table`` with ``new_lens`` (B,) query
+    tokens each, at most ``total_q`` in all; see ``msa_step_tables`` in
+    include/msa.h. Returns a ``StepTables``; ``out`` is one to write to."""
+    return StepTables._make((_native or _step()).step_tables(
+        page_table, seqused_k, rows, new_lens, total_q, num_pages, out, workspace, stream))
+
+
+def msa_sample(logits, uniforms, *, temperature=None, top_k=None, top_p=None, min_p=None,
+               return_logprobs=False, tokens=None, logprobs=None, workspace=None, stream=None):
+    """A token for each row of ``logits`` (rows, vocab), bfloat16, float16 or
+    float32, from given random numbers ``uniforms`` (rows,) float32 in [0, 1);
+    see ``msa_sample`` in include/msa.h. ``temperature``, ``top_p`` and ``min_p``
+    (rows,) float32 and ``top_k`` (rows,) int32 are each row's own; None leaves
+    one out. Returns ``tokens`` (rows,) int32 or ``(tokens, logprobs)``."""
+    tokens, logprobs = (_native or _step()).sample(
+        logits, uniforms, temperature, top_k, top_p, min_p, return_logprobs, tokens, logprobs,
+        workspace, stream)
+    return tokens if logprobs is None else (tokens, logprobs)
+
+
+def msa_draft_path(sampled, drafts, tree_mask, cu_seqlens_q, *, max_path=None, path=None,
+                   path_len=None, next_tokens=None, stream=None):
+    """The path that sampled tokens take through each request's tree of drafts;
+    see ``msa_draft_path`` in include/msa.h. Returns ``(path, path_len,
+    next_tokens)``: what ``msa_cache_accept`` takes, and the next step's roots.
+    ``max_path=None`` is as many nodes as ``tree_mask`` has bits for."""
+    return (_native or _step()).draft_path(sampled, drafts, tree_mask, cu_seqlens_q, max_path, path,
+                                            path_len, next_tokens, stream)

@@ -530,6 +530,115 @@ PyObject* cache_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// -------------------------------------------------------------- a step's tables
+// page_table, seqused_k, rows, new_lens, total_q, num_pages, out (or None),
+// workspace, stream: a tuple of the nine tables.
+PyObject* step_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want_args("msa_step_tables", n, 9);
+  const Tensor& t = dense("page_table", a[0], nullptr, at::kInt, {-1, -1});
+  const at::Device dev = t.device();
+  const Tensor& used = dense("seqused_k", a[1], &dev, at::kInt, {t.size(0)});
+  const Tensor& rows = dense("rows", a[2], &dev, at::kInt, {-1});
+  const Tensor& lens = dense("new_lens", a[3], &dev, at::kInt, rows.sizes());
+  const int total = as_int(a[4]), pages = as_int(a[5]);
+  if (total < 0) bad_value("total_q must not be negative");
+  const int64_t batch = rows.size(0), width = t.size(1);
+  const Place place(dev, a[8]);
+  PyObject* given[9];
+  for (auto& g : given) g = Py_None;
+  if (a[6] != Py_None) {
+    if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 9) bad_type("out must be what a call returned");
+    for (int i = 0; i < 9; ++i) given[i] = PyTuple_GET_ITEM(a[6], i);
+  }
+  const Tensor cu = output("cu_seqlens_q", given[0], dev, at::kInt, Shape{batch + 1});
+  const Tensor used_out = output("seqused_k (out)", given[1], dev, at::kInt, Shape{batch});
+  const Tensor table = output("page_table (out)", given[2], dev, at::kInt, Shape{batch, width});
+  const Tensor token_rows = output("token_rows", given[3], dev, at::kInt, Shape{total});
+  const Tensor positions = output("positions", given[4], dev, at::kInt, Shape{total});
+  const Tensor slots = output("slots", given[5], dev, at::kLong, Shape{total});
+  const Tensor group_rows = output("group_rows", given[6], dev, at::kInt, Shape{batch});
+  const Tensor cu_groups = output("cu_groups", given[7], dev, at::kInt, Shape{batch + 1});
+  const Tensor blocks = output("group_blocks", given[8], dev, at::kInt, Shape{batch});
+  const int b = size32("rows", batch);
+  const Tensor ws = workspace(a[7], dev, msa_step_tables_workspace_size(b));
+  check("msa_step_tables",
+        msa_step_tables(ptr<const int32_t>(t), size32("page_table", width), size32("page_table", t.size(0)),
+                        ptr<const int32_t>(used), pages, ptr<const int32_t>(rows), ptr<const int32_t>(lens), b, total,
+                        ptr<int32_t>(cu), ptr<int32_t>(used_out), ptr<int32_t>(table), ptr<int32_t>(token_rows),
+                        ptr<int32_t>(positions), static_cast<long long*>(slots.data_ptr()), ptr<int32_t>(group_rows),
+                        ptr<int32_t>(cu_groups), ptr<int32_t>(blocks), ws.data_ptr(), (size_t)ws.numel(),
+                        place.stream()));
+  return tuple_of({cu, used_out, table, token_rows, positions, slots, group_rows, cu_groups, blocks});
+  END_HANDLE_TH_ERRORS
+}
+
+// ------------------------------------------------------------ tokens and paths
+template <class T>
+const T* optional_rows(const char* name, PyObject* o, const at::Device& dev, at::ScalarType dtype, int64_t rows) {
+  return o == Py_None ? nullptr : ptr<const T>(dense(name, o, &dev, dtype, {rows}));
+}
+
+// logits, uniforms, temperature, top_k, top_p, min_p, return_logprobs, tokens,
+// logprobs, workspace, stream: (tokens, logprobs or None).
+PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want_args("msa_sample", n, 11);
+  const Tensor& x = tensor("logits", a[0]);
+  check_place("logits", x, nullptr);
+  if (!is_16bit(x.scalar_type()) && x.scalar_type() != at::kFloat) wrong_dtype("logits", x, "bfloat16, float16 or float32");
+  check_shape("logits", x, Shape{-1, -1});
+  const int64_t rows = x.size(0), vocab = x.size(1);
+  if (vocab > 1 && x.stride(1) != 1) bad_value("logits: each row must be contiguous");
+  const at::Device dev = x.device();
+  const Tensor& u = dense("uniforms", a[1], &dev, at::kFloat, {rows});
+  const float* t = optional_rows<float>("temperature", a[2], dev, at::kFloat, rows);
+  const int32_t* k = optional_rows<int32_t>("top_k", a[3], dev, at::kInt, rows);
+  const float* p = optional_rows<float>("top_p", a[4], dev, at::kFloat, rows);
+  const float* m = optional_rows<float>("min_p", a[5], dev, at::kFloat, rows);
+  const Place place(dev, a[10]);
+  const Tensor tokens = output("tokens", a[7], dev, at::kInt, Shape{rows});
+  Tensor logprobs;
+  if (a[8] != Py_None || as_flag(a[6])) logprobs = output("logprobs", a[8], dev, at::kFloat, Shape{rows});
+  const int count = size32("logits", rows), width = size32("logits", vocab);
+  const Tensor ws = workspace(a[9], dev, msa_sample_workspace_size(count, width));
+  check("msa_sample",
+        msa_sample(x.data_ptr(), x.scalar_type() == at::kFloat ? MSA_FP32 : code(x.scalar_type()),
+                   rows > 1 ? x.stride(0) : vocab, count, width, ptr<const float>(u), t, k, p, m, ptr<int32_t>(tokens),
+                   logprobs.defined() ? ptr<float>(logprobs) : nullptr, ws.data_ptr(), (size_t)ws.numel(),
+                   place.stream()));
+  return tuple_of({tokens, logprobs});
+  END_HANDLE_TH_ERRORS
+}
+
+// sampled, drafts, tree_mask, cu_seqlens_q, max_path (or None), path, path_len,
+// next_tokens, stream: (path, path_len, next_tokens).
+PyObject* draft_path(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want_args("msa_draft_path", n, 9);
+  const Tensor& sampled = dense("sampled", a[0], nullptr, at::kInt, {-1});
+  const at::Device dev = sampled.device();
+  const Tensor& drafts = dense("drafts", a[1], &dev, at::kInt, sampled.sizes());
+  const Tensor& mask = tensor("tree_mask", a[2]);
+  if (mask.scalar_type() != at::kInt && mask.scalar_type() != at::kUInt32) wrong_dtype("tree_mask", mask, "int32 or uint32");
+  dense("tree_mask", a[2], &dev, mask.scalar_type(), {sampled.size(0), -1});
+  const Tensor& cu = dense("cu_seqlens_q", a[3], &dev, at::kInt, {-1});
+  const int64_t batch = cu.size(0) > 0 ? cu.size(0) - 1 : 0;
+  const int words = size32("tree_mask", mask.size(1));
+  const int most = a[4] == Py_None ? size32("tree_mask", 32 * (int64_t)words) : as_int(a[4]);
+  if (most < 1) bad_value("max_path must be at least 1");
+  const Place place(dev, a[8]);
+  const Tensor path = output("path", a[5], dev, at::kInt, Shape{batch, most});
+  const Tensor len = output("path_len", a[6], dev, at::kInt, Shape{batch});
+  const Tensor next = output("next_tokens", a[7], dev, at::kInt, Shape{batch});
+  check("msa_draft_path",
+        msa_draft_path(ptr<const int32_t>(sampled), ptr<const int32_t>(drafts), ptr<const uint32_t>(mask), words,
+                       ptr<const int32_t>(cu), size32("cu_seqlens_q", batch), size32("sampled", sampled.size(0)), most,
+                       ptr<int32_t>(path), ptr<int32_t>(len), ptr<int32_t>(next), place.stream()));
+  return tuple_of({path, len, next});
+  END_HANDLE_TH_ERRORS
+}
+
 PyObject* set_error(PyObject*, PyObject* cls) {
   Py_XDECREF(g_error);
   g_error = Py_NewRef(cls);
@@ -546,6 +655,9 @@ PyMethodDef methods[] = {MSA_METHOD(qk_norm_rope),
                          MSA_METHOD(cache_free),
                          MSA_METHOD(cache_copy_pages),
                          MSA_METHOD(cache_accept),
+                         MSA_METHOD(step_tables),
+                         MSA_METHOD(sample),
+                         MSA_METHOD(draft_path),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -383,4 +383,70 @@ cudaError_t launch_cache_copy_pages(const CachePools& p, int num_pools, long lon
                                     int num_pages, const int32_t* src, const int32_t* dst, int n,
                                     cudaStream_t s);
 
+// A step's tables from its requests' lengths (step_tables.cu).
+struct StepTablesArgs {
+  const int32_t* page_table = nullptr;  // (num_rows, max_pages)
+  int max_pages = 0, num_rows = 0, num_pages = 0;
+  const int32_t* seqused_k = nullptr;  // (num_rows), the new tokens counted
+  const int32_t* rows = nullptr;       // (batch)
+  const int32_t* new_lens = nullptr;   // (batch)
+  int batch = 0, total_q = 0;
+  int32_t* cu_q = nullptr;         // (batch + 1)
+  int32_t* seqused_out = nullptr;  // (batch)
+  int32_t* table_out = nullptr;    // (batch, max_pages)
+  int32_t* token_rows = nullptr;   // (total_q)
+  int32_t* positions = nullptr;    // (total_q)
+  long long* slots = nullptr;      // (total_q)
+  int32_t* group_rows = nullptr;   // (batch)
+  int32_t* cu_groups = nullptr;    // (batch + 1)
+  int32_t* group_blocks = nullptr;  // (batch)
+  int32_t* plan = nullptr;         // workspace (4, batch): first page, leader, group, whole blocks before the new tokens
+  int hash_slots = 0;
+};
+cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t s);
+
+// The path of sampled tokens through trees of drafts (step_tables.cu).
+struct DraftPathArgs {
+  const int32_t* sampled = nullptr;  // (total_q)
+  const int32_t* drafts = nullptr;   // (total_q)
+  const uint32_t* mask = nullptr;    // (total_q, mask_words)
+  int mask_words = 0;
+  const int32_t* cu_q = nullptr;  // (batch + 1)
+  int batch = 0, total_q = 0, max_path = 0;
+  int32_t* path = nullptr;      // (batch, max_path)
+  int32_t* path_len = nullptr;  // (batch)
+  int32_t* next = nullptr;      // (batch)
+};
+cudaError_t launch_draft_path(const DraftPathArgs& a, cudaStream_t s);
+
+// Tokens from logits (sample.cu).
+constexpr int kMaxVocab = 1 << 19;
+constexpr int kSampleParts = 513;  // of a row's histogram
+constexpr int kSampleList = 256;   // tokens listed of each slice
+struct SampleArgs {
+  const void* logits = nullptr;  // (rows, vocab), `stride` values from row to row
+  long long stride = 0;
+  int type = 0;  // 0 bf16, 1 fp16, 2 fp32
+  int rows = 0, vocab = 0;
+  const float* uniforms = nullptr;     // (rows)
+  const float* temperature = nullptr;  // (rows) or NULL, as the cuts
+  const int32_t* top_k = nullptr;
+  const float* top_p = nullptr;
+  const float* min_p = nullptr;
+  int32_t* tokens = nullptr;  // (rows)
+  float* logprobs = nullptr;  // (rows) or NULL
+  // Workspace.
+  int slice = 0, slices = 0;             // values of a slice; slices of a row
+  unsigned long long* best = nullptr;    // (rows, slices)
+  uint32_t* parts_count = nullptr;       // (rows, kSampleParts)
+  unsigned long long* parts_mass = nullptr;
+  uint2* list = nullptr;                 // (rows, slices, kSampleList)
+  int2* list_info = nullptr;             // (rows, slices): tokens listed, parts they are of
+};
+struct SampleSlices {
+  int slice, slices;
+};
+SampleSlices sample_slices(int rows, int vocab);
+cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
+
 }  // namespace msa

@@ -1,7 +1,9 @@
 // C ABI of the operators around the attention of a serving step: host-side
-// validation and launches of the norm and rotation (rope.cu) and of the
-// cache's pages (cache.cu).
+// validation and launches of the norm and rotation (rope.cu), of the cache's
+// pages (cache.cu), of a step's tables and drafted paths (step_tables.cu) and
+// of sampling (sample.cu).
 #include <cmath>
+#include <initializer_list>
 
 #include "../../include/msa.h"
 #include "internal.h"
@@ -88,6 +90,18 @@ msa_status_t place_plan(CacheTableArgs* a, void* workspace, size_t bytes) {
   a->plan = static_cast<int32_t*>(workspace);
   a->list = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + up256((size_t)a->n * 4));
   return MSA_OK;
+}
+
+// Whether an output is an input, or given twice.
+bool shares(std::initializer_list<const void*> outputs, std::initializer_list<const void*> inputs) {
+  for (auto o = outputs.begin(); o != outputs.end(); ++o) {
+    if (*o == nullptr) continue;
+    for (const void* i : inputs)
+      if (*o == i) return true;
+    for (auto other = outputs.begin(); other != o; ++other)
+      if (*o == *other) return true;
+  }
+  return false;
 }
 
 }  // namespace
@@ -290,6 +304,105 @@ msa_status_t msa_cache_accept(void* const* pools, int num_pools, int row_bytes, 
     a.num_pools = count;
     return launch_cache_accept(p, a, stream);
   }));
+}
+
+size_t msa_step_tables_workspace_size(int batch) {
+  if (batch < 1 || batch > kMaxCacheRows) return 0;
+  return up256(4 * (size_t)batch * sizeof(int32_t));
+}
+
+msa_status_t msa_step_tables(const int32_t* page_table, int max_pages, int num_rows,
+                             const int32_t* seqused_k, int num_pages, const int32_t* rows,
+                             const int32_t* new_lens, int batch, int total_q,
+                             int32_t* cu_seqlens_q, int32_t* seqused_out, int32_t* table_out,
+                             int32_t* token_rows, int32_t* positions, long long* slots,
+                             int32_t* group_rows, int32_t* cu_groups, int32_t* group_blocks,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (max_pages < 1 || num_rows < 1 || num_pages < 1 || batch < 1 || total_q < 0) return MSA_INVALID_ARG;
+  for (const void* p : {(const void*)page_table, (const void*)seqused_k, (const void*)rows, (const void*)new_lens,
+                        (const void*)cu_seqlens_q, (const void*)seqused_out, (const void*)table_out,
+                        (const void*)group_rows, (const void*)cu_groups, (const void*)group_blocks})
+    if (!aligned(p, 4)) return MSA_INVALID_ARG;
+  if (!token_data(token_rows, 4, total_q) || !token_data(positions, 4, total_q) || !token_data(slots, 8, total_q))
+    return MSA_INVALID_ARG;
+  if (shares({cu_seqlens_q, seqused_out, table_out, token_rows, positions, slots, group_rows, cu_groups, group_blocks},
+             {page_table, seqused_k, rows, new_lens}))
+    return MSA_INVALID_ARG;
+  if (batch > kMaxCacheRows) return MSA_UNSUPPORTED;
+  if (workspace == nullptr || workspace_bytes < msa_step_tables_workspace_size(batch)) return MSA_WORKSPACE_TOO_SMALL;
+  if (!aligned(workspace, 256)) return MSA_INVALID_ARG;
+  StepTablesArgs a{};
+  a.page_table = page_table, a.max_pages = max_pages, a.num_rows = num_rows, a.num_pages = num_pages;
+  a.seqused_k = seqused_k, a.rows = rows, a.new_lens = new_lens, a.batch = batch, a.total_q = total_q;
+  a.cu_q = cu_seqlens_q, a.seqused_out = seqused_out, a.table_out = table_out;
+  a.token_rows = token_rows, a.positions = positions, a.slots = slots;
+  a.group_rows = group_rows, a.cu_groups = cu_groups, a.group_blocks = group_blocks;
+  a.plan = static_cast<int32_t*>(workspace);
+  return from_cuda(launch_step_tables(a, stream));
+}
+
+size_t msa_sample_workspace_size(int rows, int vocab) {
+  if (rows < 0 || vocab < 1 || rows > (1 << 24) || vocab > kMaxVocab) return 0;
+  const size_t n = (size_t)rows * sample_slices(rows, vocab).slices;
+  return up256(n * 8) + up256((size_t)rows * kSampleParts * 4) + up256((size_t)rows * kSampleParts * 8) +
+         up256(n * kSampleList * 8) + up256(n * 8);
+}
+
+msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride, int rows,
+                        int vocab, const float* uniforms, const float* temperature,
+                        const int32_t* top_k, const float* top_p, const float* min_p,
+                        int32_t* tokens, float* logprobs, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream) {
+  if (rows < 0 || vocab < 1 || stride < vocab) return MSA_INVALID_ARG;
+  if (dtype != MSA_BF16 && dtype != MSA_FP16 && dtype != MSA_FP32) return MSA_UNSUPPORTED;
+  if (!token_data(logits, dtype == MSA_FP32 ? 4 : 2, rows) || !token_data(uniforms, 4, rows) ||
+      !token_data(tokens, 4, rows))
+    return MSA_INVALID_ARG;
+  for (const void* p : {(const void*)temperature, (const void*)top_k, (const void*)top_p, (const void*)min_p,
+                        (const void*)logprobs})
+    if (p != nullptr && !aligned(p, 4)) return MSA_INVALID_ARG;
+  if (shares({tokens, logprobs}, {logits, uniforms, temperature, top_k, top_p, min_p})) return MSA_INVALID_ARG;
+  if (vocab > kMaxVocab || rows > (1 << 24)) return MSA_UNSUPPORTED;
+  if (rows == 0) return MSA_OK;
+  if (workspace == nullptr || workspace_bytes < msa_sample_workspace_size(rows, vocab)) return MSA_WORKSPACE_TOO_SMALL;
+  if (!aligned(workspace, 256)) return MSA_INVALID_ARG;
+  const SampleSlices c = sample_slices(rows, vocab);
+  SampleArgs a{};
+  a.logits = logits, a.stride = stride, a.type = dtype == MSA_BF16 ? 0 : dtype == MSA_FP16 ? 1 : 2;
+  a.rows = rows, a.vocab = vocab;
+  a.uniforms = uniforms, a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p;
+  a.tokens = tokens, a.logprobs = logprobs;
+  a.slice = c.slice, a.slices = c.slices;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  auto place = [&](size_t bytes) {
+    uint8_t* at = w;
+    w += up256(bytes);
+    return at;
+  };
+  const size_t n = (size_t)rows * c.slices;
+  a.best = reinterpret_cast<unsigned long long*>(place(n * 8));
+  a.parts_count = reinterpret_cast<uint32_t*>(place((size_t)rows * kSampleParts * 4));
+  a.parts_mass = reinterpret_cast<unsigned long long*>(place((size_t)rows * kSampleParts * 8));
+  a.list = reinterpret_cast<uint2*>(place(n * kSampleList * 8));
+  a.list_info = reinterpret_cast<int2*>(place(n * 8));
+  return from_cuda(launch_sample(a, stream));
+}
+
+msa_status_t msa_draft_path(const int32_t* sampled, const int32_t* drafts,
+                            const uint32_t* tree_mask, int mask_words,
+                            const int32_t* cu_seqlens_q, int batch, int total_q, int max_path,
+                            int32_t* path, int32_t* path_len, int32_t* next_tokens,
+                            cudaStream_t stream) {
+  if (mask_words < 1 || batch < 1 || total_q < 0 || max_path < 1) return MSA_INVALID_ARG;
+  if (!token_data(sampled, 4, total_q) || !token_data(drafts, 4, total_q) || !token_data(tree_mask, 4, total_q) ||
+      !aligned(cu_seqlens_q, 4) || !aligned(path, 4) || !aligned(path_len, 4) || !aligned(next_tokens, 4))
+    return MSA_INVALID_ARG;
+  if (shares({path, path_len, next_tokens}, {sampled, drafts, tree_mask, cu_seqlens_q})) return MSA_INVALID_ARG;
+  DraftPathArgs a{};
+  a.sampled = sampled, a.drafts = drafts, a.mask = tree_mask, a.mask_words = mask_words;
+  a.cu_q = cu_seqlens_q, a.batch = batch, a.total_q = total_q, a.max_path = max_path;
+  a.path = path, a.path_len = path_len, a.next = next_tokens;
+  return from_cuda(launch_draft_path(a, stream));
 }
 
 }  // extern "C"

@@ -39,7 +39,8 @@ typedef enum {
   MSA_CUDA_ERROR = 4            /* a CUDA runtime/driver call failed at launch */
 } msa_status_t;
 
-typedef enum { MSA_BF16 = 0, MSA_FP16 = 1, MSA_FP8_E4M3 = 2 } msa_dtype_t;
+/* MSA_FP32 is the type of logits (msa_sample); no tensor of the attention takes it. */
+typedef enum { MSA_BF16 = 0, MSA_FP16 = 1, MSA_FP8_E4M3 = 2, MSA_FP32 = 3 } msa_dtype_t;
 
 /* Human-readable name of a status code (static storage). */
 const char* msa_status_string(msa_status_t status);
@@ -415,6 +416,119 @@ msa_status_t msa_cache_accept(void* const* pools, int num_pools, int row_bytes, 
                               const int32_t* seqused_k, const int32_t* cu_seqlens_q,
                               const int32_t* path, const int32_t* path_len, int max_path,
                               int32_t* seqused_out, cudaStream_t stream);
+
+/*
+ * The tables of a step, from its requests' lengths.
+ *
+ * Request b of the step is row r = rows[b] of page_table (num_rows,
+ * max_pages), whose length Lk = seqused_k[r] counts the step's new tokens (as
+ * after msa_cache_extend); its Lq = new_lens[b] last ones, at least 0 and at
+ * most Lk, are its query tokens. A request whose row is out of range (-1, say)
+ * is padding: both lengths are 0. Where the sum of the tokens passes total_q,
+ * the request that does not fit and those after it get none (Lq 0).
+ * Written, all device memory:
+ *   cu_seqlens_q  int32 (B + 1), running sums of Lq
+ *   seqused_out   int32 (B), Lk
+ *   table_out     int32 (B, max_pages): the request's row up to block
+ *                 ceil(Lk / 128), -1 behind it and for entries outside
+ *                 [0, num_pages)
+ *   token_rows    int32 (total_q): each token's request
+ *   positions     int32 (total_q): its cache position Lk - Lq + i
+ *   slots         int64 (total_q): page * 128 + position % 128, -1 without a
+ *                 page; all three are -1 from cu_seqlens_q[B] on
+ *   group_rows    int32 (B), cu_groups int32 (B + 1), group_blocks int32 (B):
+ *                 the requests in groups that begin with the same page, for
+ *                 msa_prefix_attention. Group g is requests group_rows[
+ *                 cu_groups[g] .. cu_groups[g + 1]), ascending; groups stand in
+ *                 the order of their first requests, behind the last one they
+ *                 are empty. group_blocks[g] counts the leading blocks that all
+ *                 have in common with the first of them, at most
+ *                 (Lk - Lq) / 128 of any; 0 for one request alone. A request
+ *                 without tokens or without a first page is alone.
+ * workspace: msa_step_tables_workspace_size(B) bytes, 256-byte aligned,
+ * uninitialised; calls that share one must be ordered on the device.
+ * MSA_INVALID_ARG for a NULL or misaligned pointer (4 bytes, slots 8;
+ * per-token arrays may be NULL when total_q is 0), sizes below 1 (total_q may
+ * be 0) or an output that is an input; MSA_UNSUPPORTED for more than 16384
+ * requests.
+ */
+size_t msa_step_tables_workspace_size(int batch);
+msa_status_t msa_step_tables(const int32_t* page_table, int max_pages, int num_rows,
+                             const int32_t* seqused_k, int num_pages, const int32_t* rows,
+                             const int32_t* new_lens, int batch, int total_q,
+                             int32_t* cu_seqlens_q, int32_t* seqused_out, int32_t* table_out,
+                             int32_t* token_rows, int32_t* positions, long long* slots,
+                             int32_t* group_rows, int32_t* cu_groups, int32_t* group_blocks,
+                             void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Tokens from logits, one for each row.
+ *
+ * With x a row of vocab values, m its largest and T its temperature, a token's
+ * weight is w = exp((x - m) / T). Tokens stand in the order of falling x, equal
+ * ones in that of their numbers; S(n) is the sum of the first n of their
+ * weights. Of that order a beginning of n tokens is kept, where n is the least
+ * of
+ *   - top_k[row], when it is above 0 and below vocab;
+ *   - the least n with S(n) >= top_p[row] S(top_k), when top_p[row] < 1 (at
+ *     least 1);
+ *   - the number of tokens with w >= min_p[row] (as at most 1), when it is
+ *     above 0.
+ * The token is the first of them with S > u S(n), u = uniforms[row] in [0, 1)
+ * (below 0 counts as 0; 1 and above, or NaN: the last that has a weight). A
+ * temperature below 1e-5, or NaN, takes the largest; one above 1e30 counts as
+ * that. -inf and NaN are never taken; infinite logits share all weight evenly;
+ * in a row without any token the result is -1, with logprob -inf.
+ * Sums are exact: weights are rounded to 2^-44 of the largest one's, and to
+ * about 2^-35 of their own, and added as whole numbers; the same inputs give
+ * the same tokens.
+ *   logits       device, MSA_BF16, MSA_FP16 or MSA_FP32, (rows, vocab) with
+ *                `stride` values from row to row (at least vocab)
+ *   uniforms     device float32 (rows)
+ *   temperature, top_p, min_p  device float32 (rows), top_k device int32
+ *                (rows); each may be NULL (1 and no cut)
+ *   tokens       device int32 (rows)
+ *   logprobs     device float32 (rows) or NULL: ln w - ln S(vocab) of the
+ *                token, before the cuts (T = 1 where the largest is taken)
+ *   workspace    msa_sample_workspace_size(rows, vocab) bytes, 256-byte aligned,
+ *                uninitialised; calls that share one must be ordered on the device
+ * MSA_INVALID_ARG for a NULL or misaligned pointer (arrays of rows may be NULL
+ * when rows is 0), vocab below 1, a stride below vocab, or an output that is an
+ * input; MSA_UNSUPPORTED for another dtype, vocab above 2^19 or rows above 2^24.
+ */
+size_t msa_sample_workspace_size(int rows, int vocab);
+msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride, int rows,
+                        int vocab, const float* uniforms, const float* temperature,
+                        const int32_t* top_k, const float* top_p, const float* min_p,
+                        int32_t* tokens, float* logprobs, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+
+/*
+ * The path that sampled tokens take through each request's tree of drafts:
+ * what msa_cache_accept takes.
+ *
+ * Request b's Lq tokens (cu_seqlens_q) are the nodes of a tree, each behind its
+ * parent; node 0 is the root, a token that is accepted already. drafts holds
+ * the nodes' tokens and sampled what the model made after each (msa_sample of
+ * the nodes' logits). A node's parent is the highest of the nodes before it
+ * that its row of tree_mask (as msa_tree_attention takes it) names; one that
+ * names none has no parent. From the root on, the path goes to the lowest
+ * child whose draft is what was sampled at its parent.
+ *   tree_mask    device uint32 (total_q, mask_words)
+ *   path         device int32 (B, max_path): the path's nodes, -1 behind it;
+ *                it ends with its max_path-th node
+ *   path_len     device int32 (B); 0 for a request without tokens
+ *   next_tokens  device int32 (B): what was sampled at the path's end, the
+ *                next root; -1 for a request without tokens
+ * Tokens at or past total_q are not read. MSA_INVALID_ARG for a NULL or
+ * misaligned pointer (4 bytes; per-token arrays may be NULL when total_q is 0),
+ * sizes below 1 (total_q may be 0) or an output that is an input.
+ */
+msa_status_t msa_draft_path(const int32_t* sampled, const int32_t* drafts,
+                            const uint32_t* tree_mask, int mask_words,
+                            const int32_t* cu_seqlens_q, int batch, int total_q, int max_path,
+                            int32_t* path, int32_t* path_len, int32_t* next_tokens,
+                            cudaStream_t stream);
 
 /*
  * Dense proxy pass, MSA stage 1 ("flashinfer.msa_ops.msa_proxy_score").

@@ -1,0 +1,92 @@
+"""What the entry points of a step of samples refuse, decided on the host before any CUDA call (CPU only)."""
+import ctypes as C
+
+import pytest
+
+OK, INVALID, UNSUPPORTED, TOO_SMALL = 0, 1, 2, 3
+P = C.c_void_p(0x10000)      # never followed: the call ends before
+ODD = C.c_void_p(0x10002)
+
+
+def at(i):
+    return C.c_void_p(0x100000 + 0x1000 * i)
+
+
+@pytest.fixture(scope="module")
+def L():
+    import block_sparse_top_msa_gb300 as msa
+    msa.build()
+    return msa.lib()
+
+
+def call(fn, names, good, **changed):
+    return fn(*[changed.get(n, good[n]) for n in names])
+
+
+TABLES = "pt mp nr su np rows lens b t cu suo pto tr pos sl gr cg gb ws wb s".split()
+TABLES_GOOD = dict(pt=at(0), mp=4, nr=8, su=at(1), np=10, rows=at(2), lens=at(3), b=2, t=3, cu=at(4), suo=at(5), pto=at(6), tr=at(7), pos=at(8), sl=at(9), gr=at(10), cg=at(11),
+                   gb=at(12), ws=P, wb=1 << 20, s=None)
+
+
+@pytest.mark.parametrize("bad,status", [(dict(pt=None), INVALID), (dict(su=ODD), INVALID), (dict(rows=None), INVALID), (dict(lens=ODD), INVALID), (dict(cu=None), INVALID),
+                                        (dict(suo=None), INVALID), (dict(pto=ODD), INVALID), (dict(tr=None), INVALID), (dict(sl=C.c_void_p(0x10004)), INVALID), (dict(gr=None), INVALID),
+                                        (dict(cg=None), INVALID), (dict(gb=ODD), INVALID), (dict(mp=0), INVALID), (dict(nr=0), INVALID), (dict(np=0), INVALID), (dict(b=0), INVALID),
+                                        (dict(t=-1), INVALID), (dict(pto=at(0)), INVALID), (dict(suo=at(1)), INVALID), (dict(cu=at(3)), INVALID), (dict(gr=at(12)), INVALID),
+                                        (dict(b=16385), UNSUPPORTED), (dict(wb=16), TOO_SMALL), (dict(ws=None), TOO_SMALL), (dict(ws=C.c_void_p(0x10010)), INVALID)])
+def test_step_tables_refuses(L, bad, status):
+    assert call(L.msa_step_tables, TABLES, TABLES_GOOD, **bad) == status
+
+
+def test_step_tables_workspace(L):
+    assert L.msa_step_tables_workspace_size(0) == 0 and L.msa_step_tables_workspace_size(16385) == 0
+    assert L.msa_step_tables_workspace_size(1) == 256 and L.msa_step_tables_workspace_size(16384) == 16 * 16384
+
+
+SAMPLE = "x dt stride rows vocab u t k p m out lp ws wb s".split()
+SAMPLE_GOOD = dict(x=at(0), dt=3, stride=100, rows=0, vocab=100, u=at(1), t=None, k=None, p=None, m=None, out=at(2), lp=None, ws=P, wb=1 << 30, s=None)
+
+
+@pytest.mark.parametrize("bad,status", [(dict(), OK), (dict(x=None, u=None, out=None), OK), (dict(rows=1, x=None), INVALID), (dict(rows=1, u=None), INVALID),
+                                        (dict(rows=1, out=None), INVALID), (dict(x=ODD), INVALID), (dict(x=ODD, dt=0), OK), (dict(x=C.c_void_p(0x10001), dt=1), INVALID),
+                                        (dict(t=ODD), INVALID), (dict(k=ODD), INVALID), (dict(p=ODD), INVALID), (dict(m=ODD), INVALID), (dict(lp=ODD), INVALID),
+                                        (dict(rows=-1), INVALID), (dict(vocab=0), INVALID), (dict(stride=99), INVALID), (dict(dt=2), UNSUPPORTED), (dict(dt=4), UNSUPPORTED),
+                                        (dict(vocab=(1 << 19) + 1, stride=1 << 20), UNSUPPORTED), (dict(rows=(1 << 24) + 1), UNSUPPORTED), (dict(out=at(1)), INVALID),
+                                        (dict(lp=at(2)), INVALID), (dict(lp=at(3), t=at(3)), INVALID),
+                                        (dict(rows=1, ws=None), TOO_SMALL), (dict(rows=1, wb=100), TOO_SMALL), (dict(rows=1, ws=C.c_void_p(0x10010)), INVALID)])
+def test_sample_refuses(L, bad, status):
+    assert call(L.msa_sample, SAMPLE, SAMPLE_GOOD, **bad) == status
+
+
+def test_sample_workspace(L):
+    assert L.msa_sample_workspace_size(-1, 5) == 0 and L.msa_sample_workspace_size(1, 0) == 0 and L.msa_sample_workspace_size(1, (1 << 19) + 1) == 0
+    assert L.msa_sample_workspace_size(0, 5) == 0 and L.msa_sample_workspace_size(512, 200019) < 1 << 24
+
+
+PATH = "sa dr mask words cu b t w path len nxt s".split()
+PATH_GOOD = dict(sa=at(0), dr=at(1), mask=at(2), words=1, cu=at(3), b=1, t=4, w=4, path=at(4), len=at(5), nxt=at(6), s=None)
+
+
+@pytest.mark.parametrize("bad", [dict(sa=None), dict(dr=ODD), dict(mask=None), dict(words=0), dict(cu=None), dict(b=0), dict(t=-1), dict(w=0), dict(path=None), dict(len=ODD),
+                                 dict(nxt=None), dict(path=at(0)), dict(len=at(6)), dict(nxt=at(3))])
+def test_draft_path_refuses(L, bad):
+    assert call(L.msa_draft_path, PATH, PATH_GOOD, **bad) == INVALID
+
+
+def test_binding_refuses_before_the_library():
+    import torch
+
+    import block_sparse_top_msa_gb300 as msa
+    i, f = torch.zeros(3, dtype=torch.int32), torch.zeros(3)
+    with pytest.raises(ValueError):
+        msa.msa_step_tables(torch.zeros(2, 3, dtype=torch.int32), i, i, i, total_q=3, num_pages=4)
+    with pytest.raises(ValueError):
+        msa.msa_sample(torch.zeros(3, 10), f)
+    with pytest.raises(TypeError):
+        msa.msa_sample([1.0], f)
+    with pytest.raises(ValueError):
+        msa.msa_draft_path(i, i, torch.zeros(3, 1, dtype=torch.int32), i)
+
+
+def test_fp32_is_no_type_of_the_attention(L):
+    """The code of a logit's type, given to the operators that do not know it."""
+    assert L.msa_sparse_attention_fwd(P, 3, P, P, 3, P, 4, P, P, None, 0, 0, None, 1, 0, 128, 4, 2, 128, 32, 1, C.c_float(0.0), P, None, P, 1 << 30, None) == UNSUPPORTED
