@@ -118,6 +118,13 @@ def lib():
         L.msa_cache_accept.restype = i32
         L.msa_cache_accept.argtypes = [C.POINTER(vp), i32, i32, i32, vp, i32, i32, i32, vp, vp, vp,
                                        vp, i32, vp, vp]
+        prefix = [vp, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp, sz]
+        L.msa_prefix_attention_workspace_size.restype = sz
+        L.msa_prefix_attention_workspace_size.argtypes = [i32] * 6
+        L.msa_prefix_attention.restype = i32
+        L.msa_prefix_attention.argtypes = prefix + [vp]
+        L.msa_prefix_attention_prepare.restype = i32
+        L.msa_prefix_attention_prepare.argtypes = prefix + [C.POINTER(vp)]
         L.msa_step_tables_workspace_size.restype = sz
         L.msa_step_tables_workspace_size.argtypes = [i32]
         L.msa_step_tables.restype = i32
@@ -774,6 +781,43 @@ def msa_step_tables(page_table, seqused_k, rows, new_lens, *, total_q, num_pages
     include/msa.h. Returns a ``StepTables``; ``out`` is one to write to."""
     return StepTables._make((_native or _step()).step_tables(
         page_table, seqused_k, rows, new_lens, total_q, num_pages, out, workspace, stream))
+
+
+def msa_prefix_attention(q, k, v, cu_seqlens_q, *, page_table, seqused_k, group_rows=None,
+                         cu_groups=None, group_blocks=None, max_seqlen_q=None, causal=True,
+                         softmax_scale=None, return_softmax_lse=False, out=None, lse=None,
+                         workspace=None, stream=None):
+    """Attention of all keys of each request over a paged cache, in which the
+    first pages that groups of requests share are attended once for all of a
+    group; see ``msa_prefix_attention`` in include/msa.h. The groups are those of
+    a ``StepTables``; without them each request is by itself. Returns ``out`` or
+    ``(out, lse)``. ``max_seqlen_q``, which the other attentions take, is not needed
+    and not looked at."""
+    out, lse, _, _ = (_native or _step()).prefix_attention(
+        q, k, v, cu_seqlens_q, page_table, seqused_k, group_rows, cu_groups, group_blocks, causal,
+        softmax_scale, return_softmax_lse, out, lse, workspace, stream, False)
+    return out if lse is None else (out, lse)
+
+
+class PrefixAttentionRunner(SparseAttentionRunner):
+    """The attention over shared prefixes prepared once
+    (``msa_prefix_attention_prepare``) and launched by ``run()``; see
+    ``SparseAttentionRunner``."""
+
+    def __init__(self, q, k, v, cu_seqlens_q, *, page_table, seqused_k, group_rows=None,
+                 cu_groups=None, group_blocks=None, causal=True, softmax_scale=None,
+                 return_softmax_lse=False, out=None, lse=None, workspace=None):
+        self.out, self.lse, self.workspace, plan = (_native or _step()).prefix_attention(
+            q, k, v, cu_seqlens_q, page_table, seqused_k, group_rows, cu_groups, group_blocks,
+            causal, softmax_scale, return_softmax_lse, out, lse, workspace, None, True)
+        self._bound = (q, k, v, cu_seqlens_q, page_table, seqused_k, group_rows, cu_groups,
+                       group_blocks)
+        self._plan = C.c_void_p(plan)
+        self._lib = lib()
+
+    def run(self, stream=None):
+        with torch.cuda.device(self.out.device):  # the tensors' device, current or not
+            return super().run(stream)
 
 
 def msa_sample(logits, uniforms, *, temperature=None, top_k=None, top_p=None, min_p=None,

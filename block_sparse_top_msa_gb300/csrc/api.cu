@@ -5,6 +5,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <climits>
 #include <cmath>
 #include <mutex>
 #include <new>
@@ -397,6 +398,8 @@ struct ForwardPlan {
   bool skip_union = false;  // direct mode: the attention kernel builds one-token unions itself
   bool tree = false;        // msa_tree_attention: launch_tree alone
   TreeArgs t{};
+  bool prefix = false;      // msa_prefix_attention: launch_prefix alone
+  PrefixArgs x{};
   bool fp4_decode = false;  // packed-NVFP4 decode-shaped call: fp4_decode_kernel alone
   Fp4DecodeArgs f4{};
 };
@@ -798,6 +801,114 @@ msa_status_t build_tree(
   return MSA_OK;
 }
 
+// Workspace of the attention over shared prefixes.
+struct PrefixLayout {
+  size_t off_work, off_start, off_token, off_kept, off_ml, off_o, part_rows, total;
+};
+constexpr int kPrefixMaxPages = 1 << 23;  // tokens of a row's pages are counted in 32 bits
+
+PrefixLayout prefix_layout(int batch, int total_q, int hq, bool groups) {
+  PrefixLayout L{};
+  size_t off = up256((size_t)batch * 2 * sizeof(int4));
+  auto place = [&](size_t bytes) {
+    const size_t at = off;
+    off += up256(bytes);
+    return at;
+  };
+  L.off_work = place((size_t)batch * 4 * sizeof(int4));
+  L.off_start = place(2 * (2 * (size_t)batch + 1) * sizeof(long long));
+  L.off_token = place((size_t)total_q * sizeof(int2));
+  L.off_kept = place(sizeof(int));
+  L.part_rows = (size_t)total_q * hq * (groups ? 2 : 1);
+  const size_t rows = L.part_rows + (size_t)kPlanSMs * (kSmallRows + kBigRows);
+  L.off_ml = place(rows * sizeof(float2));
+  L.off_o = place(rows * 128 * sizeof(float));
+  L.total = off;
+  return L;
+}
+
+bool prefix_sizes_ok(int batch, int total_q, int hq, int hkv, int head_dim) {
+  return batch >= 1 && batch <= kMaxCacheRows && total_q >= 0 && hq >= 1 && hkv >= 1 && hq % hkv == 0 &&
+         hq / hkv <= 128 && head_dim == 128 && (long long)total_q * hq < (1ll << 30);
+}
+
+msa_status_t build_prefix(
+    const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
+    const int32_t* cu_seqlens_q, const int32_t* page_table, int max_pages, int num_pages,
+    const int32_t* seqused_k, const int32_t* group_rows, const int32_t* cu_groups,
+    const int32_t* group_blocks, int batch, int total_q, int num_qo_heads, int num_kv_heads,
+    int head_dim, int causal, float softmax_scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, ForwardPlan* plan) {
+  if (batch < 1 || total_q < 0 || num_qo_heads < 1 || num_kv_heads < 1 ||
+      num_qo_heads % num_kv_heads != 0 || max_pages < 1 || num_pages < 1)
+    return MSA_INVALID_ARG;
+  if (q == nullptr || k == nullptr || v == nullptr || cu_seqlens_q == nullptr || page_table == nullptr ||
+      seqused_k == nullptr || out == nullptr)
+    return MSA_INVALID_ARG;
+  const bool groups = group_rows != nullptr;
+  if (groups != (cu_groups != nullptr) || groups != (group_blocks != nullptr)) return MSA_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
+      !aligned(cu_seqlens_q, 4) || !aligned(page_table, 4) || !aligned(seqused_k, 4) ||
+      (groups && (!aligned(group_rows, 4) || !aligned(cu_groups, 4) || !aligned(group_blocks, 4))) ||
+      (lse && !aligned(lse, 4)) || (workspace && !aligned(workspace, 256)))
+    return MSA_INVALID_ARG;
+  if (!prefix_sizes_ok(batch, total_q, num_qo_heads, num_kv_heads, head_dim) || max_pages > kPrefixMaxPages)
+    return MSA_UNSUPPORTED;
+  if (q_dtype == MSA_FP16 ? kv_dtype != MSA_FP16
+                          : (q_dtype != MSA_BF16 || (kv_dtype != MSA_BF16 && kv_dtype != MSA_FP8_E4M3)))
+    return MSA_UNSUPPORTED;
+  const PrefixLayout L = prefix_layout(batch, total_q, num_qo_heads, groups);
+  if (workspace == nullptr || workspace_bytes < L.total) return MSA_WORKSPACE_TOO_SMALL;
+  plan->empty = total_q == 0;
+  if (plan->empty) return MSA_OK;
+  if (out == q) return MSA_INVALID_ARG;  // rows that are not finite read Q again
+  unsigned* fault = fault_word();
+  if (fault == nullptr) return MSA_CUDA_ERROR;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  plan->prefix = true;
+  PrefixArgs& a = plan->x;
+  a.fault = fault;
+  const bool e4m3 = kv_dtype == MSA_FP8_E4M3;
+  if (!map_pages(&a.tmap_k, k, e4m3 ? 1 : 2, num_kv_heads, num_pages) ||
+      !map_pages(&a.tmap_v, v, e4m3 ? 1 : 2, num_kv_heads, num_pages))
+    return MSA_CUDA_ERROR;
+  a.q = q;
+  a.k_pool = static_cast<const uint8_t*>(k);
+  a.v_pool = static_cast<const uint8_t*>(v);
+  a.e4m3 = e4m3 ? 1 : 0;
+  a.f16 = q_dtype == MSA_FP16 ? 1 : 0;
+  a.cu_q = cu_seqlens_q;
+  a.page_table = page_table;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.seqused_k = seqused_k;
+  a.group_rows = group_rows;
+  a.cu_groups = cu_groups;
+  a.group_blocks = group_blocks;
+  a.batch = batch;
+  a.total_q = total_q;
+  a.num_qo_heads = num_qo_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.causal = causal ? 1 : 0;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)head_dim);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.out = out;
+  a.lse = lse;
+  a.small_rows = INT_MAX;
+  a.small_grid = a.big_grid = kPlanSMs;
+  a.small_range = 1;
+  a.big_range = 8;
+  a.entry = reinterpret_cast<int4*>(ws);
+  a.work = reinterpret_cast<int4*>(ws + L.off_work);
+  a.start = reinterpret_cast<long long*>(ws + L.off_start);
+  a.token = reinterpret_cast<int2*>(ws + L.off_token);
+  a.kept = reinterpret_cast<int*>(ws + L.off_kept);
+  a.part_rows = L.part_rows;
+  a.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
+  a.part_o = reinterpret_cast<float*>(ws + L.off_o);
+  return MSA_OK;
+}
+
 // The packed-NVFP4 paged route: the E4M3 kernel instance (converter warps),
 // fed by bulk copies of each page's K and V slices and block scales, with
 // the K global scale folded into the softmax scale and the V global scale
@@ -909,6 +1020,12 @@ msa_status_t launch_forward(const ForwardPlan& p, cudaStream_t stream) {
   if (p.fp4_decode) {
     mark(1, stream);
     const cudaError_t e = launch_fp4_decode(p.f4, stream);
+    mark(2, stream);
+    return from_cuda(e);
+  }
+  if (p.prefix) {
+    mark(1, stream);
+    const cudaError_t e = launch_prefix(p.x, stream);
     mark(2, stream);
     return from_cuda(e);
   }
@@ -1076,6 +1193,52 @@ msa_status_t msa_tree_attention_prepare(
 }
 
 #undef MSA_TREE_ARGS
+
+size_t msa_prefix_attention_workspace_size(int batch, int total_q, int num_qo_heads,
+                                           int num_kv_heads, int head_dim, int groups) {
+  if (!prefix_sizes_ok(batch, total_q, num_qo_heads, num_kv_heads, head_dim)) return 0;
+  return prefix_layout(batch, total_q, num_qo_heads, groups != 0).total;
+}
+
+#define MSA_PREFIX_ARGS                                                                            \
+  q, q_dtype, k, v, kv_dtype, cu_seqlens_q, page_table, max_pages, num_pages, seqused_k,           \
+      group_rows, cu_groups, group_blocks, batch, total_q, num_qo_heads, num_kv_heads, head_dim,   \
+      causal, softmax_scale, out, lse, workspace, workspace_bytes
+
+msa_status_t msa_prefix_attention(
+    const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
+    const int32_t* cu_seqlens_q, const int32_t* page_table, int max_pages, int num_pages,
+    const int32_t* seqused_k, const int32_t* group_rows, const int32_t* cu_groups,
+    const int32_t* group_blocks, int batch, int total_q, int num_qo_heads, int num_kv_heads,
+    int head_dim, int causal, float softmax_scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream) {
+  msa::ForwardPlan p;
+  const msa_status_t st = msa::build_prefix(MSA_PREFIX_ARGS, &p);
+  if (st != MSA_OK) return st;
+  return msa::launch_forward(p, stream);
+}
+
+msa_status_t msa_prefix_attention_prepare(
+    const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
+    const int32_t* cu_seqlens_q, const int32_t* page_table, int max_pages, int num_pages,
+    const int32_t* seqused_k, const int32_t* group_rows, const int32_t* cu_groups,
+    const int32_t* group_blocks, int batch, int total_q, int num_qo_heads, int num_kv_heads,
+    int head_dim, int causal, float softmax_scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, msa_attention_plan_t** plan_out) {
+  if (plan_out == nullptr) return MSA_INVALID_ARG;
+  *plan_out = nullptr;
+  msa_attention_plan_t* plan = new (std::nothrow) msa_attention_plan_t;
+  if (plan == nullptr) return MSA_CUDA_ERROR;
+  const msa_status_t st = msa::build_prefix(MSA_PREFIX_ARGS, &plan->p);
+  if (st != MSA_OK) {
+    delete plan;
+    return st;
+  }
+  *plan_out = plan;
+  return MSA_OK;
+}
+
+#undef MSA_PREFIX_ARGS
 
 msa_status_t msa_proxy_score(const void* q, msa_dtype_t q_dtype, const void* k,
                              msa_dtype_t k_dtype, const int32_t* cu_seqlens_q,

@@ -360,6 +360,63 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// ------------------------------------------------- attention, shared prefixes
+// q, k, v, cu_seqlens_q, page_table, seqused_k, group_rows, cu_groups,
+// group_blocks (or None), causal, softmax_scale (or None), return_softmax_lse,
+// out, lse, workspace, stream, prepare: (out, lse or None, workspace, plan or
+// None).
+PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want_args("msa_prefix_attention", n, 17);
+  const Tensor& q = tensor("q", a[0]);
+  check_place("q", q, nullptr);
+  if (!is_16bit(q.scalar_type())) wrong_dtype("q", q, "bfloat16 or float16");
+  dense("q", a[0], nullptr, q.scalar_type(), {-1, -1, 128});
+  const at::Device dev = q.device();
+  const Tensor& k = tensor("k", a[1]);
+  if (!is_kv(k.scalar_type())) wrong_dtype("k", k, "bfloat16, float16 or float8_e4m3fn");
+  dense("k", a[1], &dev, k.scalar_type(), {-1, -1, 128, 128});
+  const Tensor& v = dense("v", a[2], &dev, k.scalar_type(), k.sizes());
+  const Tensor& cu = dense("cu_seqlens_q", a[3], &dev, at::kInt, {-1});
+  const int64_t rows = cu.size(0) > 0 ? cu.size(0) - 1 : 0;
+  const Tensor& pt = dense("page_table", a[4], &dev, at::kInt, {rows, -1});
+  const Tensor& used = dense("seqused_k", a[5], &dev, at::kInt, {rows});
+  const int given = (a[6] != Py_None) + (a[7] != Py_None) + (a[8] != Py_None);
+  if (given != 0 && given != 3) bad_value("group_rows, cu_groups and group_blocks go together");
+  const int32_t *group_rows = nullptr, *cu_groups = nullptr, *blocks = nullptr;
+  if (given) {
+    group_rows = ptr<const int32_t>(dense("group_rows", a[6], &dev, at::kInt, {rows}));
+    cu_groups = ptr<const int32_t>(dense("cu_groups", a[7], &dev, at::kInt, {rows + 1}));
+    blocks = ptr<const int32_t>(dense("group_blocks", a[8], &dev, at::kInt, {rows}));
+  }
+  const int causal = as_flag(a[9]);
+  const float scale = a[10] == Py_None ? 0.f : as_float(a[10]);
+  const Place place(dev, a[15]);
+  const int total = size32("q", q.size(0)), hq = size32("q", q.size(1)), hkv = size32("k", k.size(1));
+  const int max_pages = size32("page_table", pt.size(1)), pages = size32("k", k.size(0)), batch = size32("cu", rows);
+  const msa_dtype_t qt = code(q.scalar_type()), kt = code(k.scalar_type());
+  const Tensor out = output("out", a[12], dev, q.scalar_type(), q.sizes());
+  Tensor lse;
+  if (a[13] != Py_None || as_flag(a[11])) lse = output("lse", a[13], dev, at::kFloat, Shape{total, hq});
+  const Tensor ws = workspace(a[14], dev, msa_prefix_attention_workspace_size(batch, total, hq, hkv, 128, given));
+  const bool prepare = as_flag(a[16]);
+  msa_attention_plan_t* plan = nullptr;
+#define MSA_PREFIX_CALL                                                                                          \
+  q.data_ptr(), qt, k.data_ptr(), v.data_ptr(), kt, ptr<const int32_t>(cu), ptr<const int32_t>(pt), max_pages,   \
+      pages, ptr<const int32_t>(used), group_rows, cu_groups, blocks, batch, total, hq, hkv, 128, causal, scale, \
+      out.data_ptr(), lse.defined() ? ptr<float>(lse) : nullptr, ws.data_ptr(), (size_t)ws.numel()
+  if (prepare) check("msa_prefix_attention_prepare", msa_prefix_attention_prepare(MSA_PREFIX_CALL, &plan));
+  else if (total > 0) check("msa_prefix_attention", msa_prefix_attention(MSA_PREFIX_CALL, place.stream()));
+#undef MSA_PREFIX_CALL
+  PyObject* r = tuple_of({out, lse, ws, Tensor()});
+  if (prepare) {
+    Py_DECREF(PyTuple_GET_ITEM(r, 3));
+    PyTuple_SET_ITEM(r, 3, PyLong_FromVoidPtr(plan));
+  }
+  return r;
+  END_HANDLE_TH_ERRORS
+}
+
 // ------------------------------------------------------------------ the cache
 // The pools of a cache: a list or tuple of tensors (num_pages, ...) of one
 // shape and dtype, or one tensor with a leading dimension over them.
@@ -650,6 +707,7 @@ PyMethodDef methods[] = {MSA_METHOD(qk_norm_rope),
                          MSA_METHOD(qk_norm_rope_append),
                          MSA_METHOD(qk_norm_rope_bwd),
                          MSA_METHOD(tree_attention),
+                         MSA_METHOD(prefix_attention),
                          MSA_METHOD(cache_extend),
                          MSA_METHOD(cache_fork),
                          MSA_METHOD(cache_free),

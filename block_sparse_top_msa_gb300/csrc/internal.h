@@ -185,6 +185,45 @@ struct TreeArgs {
 };
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
 
+// Attention over shared prefixes (prefix.cu). Two lines of work: units of few
+// rows (line 0) and of many.
+constexpr int kSmallRows = 16, kBigRows = 256;
+// What a block costs a unit of an entry with so many rows.
+__host__ __device__ constexpr int prefix_weight(int line, int rows) { return line == 0 ? 1 : rows > 128 ? 4 : 3; }
+struct PrefixArgs {
+  unsigned* fault = nullptr;
+  CUtensorMap tmap_k;  // (.., 128, Hkv, pages)
+  CUtensorMap tmap_v;
+  const void* q = nullptr;
+  const uint8_t* k_pool = nullptr;
+  const uint8_t* v_pool = nullptr;
+  int e4m3 = 0, f16 = 0;  // the cache's type, else bf16
+  const int32_t* cu_q = nullptr;
+  const int32_t* page_table = nullptr;
+  int max_pages = 0, num_pages = 0;
+  const int32_t* seqused_k = nullptr;
+  const int32_t* group_rows = nullptr;  // NULL: each request by itself
+  const int32_t* cu_groups = nullptr;
+  const int32_t* group_blocks = nullptr;
+  int batch = 0, total_q = 0, num_qo_heads = 0, num_kv_heads = 0, causal = 0;
+  float scale_log2 = 0.f;
+  void* out = nullptr;
+  float* lse = nullptr;
+  int small_rows = 0;  // entries of more rows go to line 1
+  int small_grid = 0, big_grid = 0, small_range = 0, big_range = 0;  // CTAs, and the least cost of a range
+  // Workspace. Positions: the requests in the order of the groups; entries: the
+  // positions' own runs, then the groups'.
+  int4* entry = nullptr;       // (batch, 2): first token in that order, tokens, request, group; first row of q, Lk - Lq, Lk
+  int4* work = nullptr;        // (2 batch, 2): first token, rows, page row, first block; blocks, keys that all rows see, Lk, group
+  long long* start = nullptr;  // (2, 2 batch + 1): running sums of the entries' costs on each line
+  int2* token = nullptr;       // (total_q): each token's row of q, and its position
+  int* kept = nullptr;         // tokens in all
+  size_t part_rows = 0;        // rows of parts before the CTAs' own
+  float2* part_ml = nullptr;   // (part_rows + small_grid * kSmallRows + big_grid * kBigRows)
+  float* part_o = nullptr;     // the same, 128 each
+};
+cudaError_t launch_prefix(const PrefixArgs& a, cudaStream_t s);
+
 struct ProxyArgs {
   unsigned* fault;      // device fault word (bounded-wait expiry, capacity)
   CUtensorMap tmap_q;   // (d, Hq, Tq) 16-bit, box (64, G, Wm)

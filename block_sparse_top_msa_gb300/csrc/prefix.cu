@@ -1,0 +1,811 @@
+// Attention over a paged cache in which groups of requests share their first
+// pages: those are attended once for all tokens of a group.
+//
+// Each request's tokens attend to all of its keys, so a row (token, query head)
+// is the softmax over two runs of blocks: its group's and its own. Both are
+// entries of a work list, with the rows that attend them (a group's, all of its
+// tokens' rows), and a row's parts (m, l, O) of each run are joined at the end:
+// with M = max m_i and L = sum 2^(m_i - M) l_i, out = sum 2^(m_i - M) O_i / L.
+//
+// An entry's rows are cut into tiles and, with each KV head, units; the units'
+// blocks, laid end to end, are cut into equal ranges, one per CTA, wherever
+// they end: a long run is split over many CTAs, short ones share one. The first
+// piece of a unit leaves its parts at the rows' own places, the others (a CTA
+// has one at most, its first) at the CTA's.
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <climits>
+
+#include "common.cuh"
+#include "internal.h"
+#include "softmax.cuh"
+
+namespace msa {
+namespace {
+
+template <class T>
+MSA_DEV T warp_upto(T v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const T o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+constexpr int kPlanThreads = 1024;
+template <class T>
+MSA_DEV T block_upto(T v, T* s_warp, T& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const T inc = warp_upto(v, lane);
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = inc;
+  __syncthreads();
+  const T w = warp_upto(s_warp[lane], lane);
+  all = __shfl_sync(0xffffffffu, w, 31);
+  const T before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return inc + (warp > 0 ? before : T(0));
+}
+
+// The work list, by one block: requests in the order of their groups, where
+// their tokens begin in that order, the blocks that each group attends for
+// all, and the running sums of what the entries cost. Entry i < batch is the
+// i-th request's own run, entry batch + g that of group g.
+__global__ void __launch_bounds__(kPlanThreads)
+    prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
+  extern __shared__ int dyn[];
+  __shared__ long long s_sum[32];
+  __shared__ int s_int[32];
+  __shared__ int s_kept;
+  int* least = dyn;              // (batch): blocks that a group attends for all
+  int* tokens = dyn + a.batch;   // (batch): a group's tokens
+  int* members = dyn + 2 * a.batch;  // (batch): its requests that have some
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int G = a.num_qo_heads / a.num_kv_heads;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const bool groups = a.group_rows != nullptr;
+  for (int g = tid; g < a.batch; g += kPlanThreads) {
+    least[g] = groups ? max(0, min(__ldg(a.group_blocks + g), a.max_pages)) : 0;
+    tokens[g] = members[g] = 0;
+  }
+  if (tid == 0) s_kept = 0;
+  __syncthreads();
+  int before = 0;
+  for (int i0 = 0; i0 < a.batch; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    int b = -1, t0 = 0, lq = 0, lk = 0, g = i;
+    if (i < a.batch) {
+      b = groups ? __ldg(a.group_rows + i) : i;
+      if (b >= 0 && b < a.batch) {
+        t0 = __ldg(a.cu_q + b);
+        const int t1 = __ldg(a.cu_q + b + 1);
+        if (t0 >= 0 && t1 <= a.total_q && t1 > t0) lq = t1 - t0;
+        lk = max(0, __ldg(a.seqused_k + b));
+      }
+      if (groups) {
+        int lo = 0;  // the last group that begins at or before i
+        for (int hi = a.batch; hi - lo > 1;) {
+          const int mid = (lo + hi) >> 1;
+          if (__ldg(a.cu_groups + mid) <= i) lo = mid; else hi = mid;
+        }
+        g = lo;
+      }
+    }
+    int all;
+    const int tau = before + block_upto<int>(lq, s_int, all) - lq;
+    before += all;
+    if (i < a.batch) {
+      // With requests listed twice the sums may pass the tokens there are: the
+      // rest is left out.
+      if (tau < 0 || lq > a.total_q - tau) lq = 0;
+      a.entry[2 * i] = make_int4(tau, lq, b, g);
+      a.entry[2 * i + 1] = make_int4(t0, lk - lq, lk, 0);
+      if (lq > 0) {
+        atomicMin(&least[g], max(0, lk - lq) / kBlk);
+        atomicAdd(&tokens[g], lq);
+        atomicAdd(&members[g], 1);
+        atomicMax(&s_kept, tau + lq);
+      }
+    }
+  }
+  __syncthreads();
+  // Each token's place in the groups' order, a warp for each request.
+  for (int i = warp; i < a.batch; i += kPlanThreads / 32) {
+    const int4 x = a.entry[2 * i];
+    const int t0 = a.entry[2 * i + 1].x;
+    for (int j = lane; j < x.y; j += 32) a.token[x.x + j] = make_int2(t0 + j, i);
+  }
+  __syncthreads();
+  long long cost_before[2] = {0, 0};
+  for (int e0 = 0; e0 < 2 * a.batch; e0 += kPlanThreads) {
+    const int e = e0 + tid;
+    long long cost[2] = {0, 0};
+    int4 x = make_int4(0, 0, 0, 0), y = make_int4(0, 0, 0, 0);  // tau, rows, page row, first block; blocks, first key that may be hidden, Lk, 0
+    if (e < a.batch) {
+      const int4 r = a.entry[2 * e], s = a.entry[2 * e + 1];
+      const int from = members[r.w] > 1 ? least[r.w] : 0;
+      const int blocks = (int)min((long long)a.max_pages, ((long long)s.z + kBlk - 1) / kBlk);
+      x = make_int4(r.x, r.y * G, r.z, from);
+      y = make_int4(r.y > 0 ? max(0, blocks - from) : 0, a.causal ? s.y : s.z, s.z, r.w);
+    } else if (e < 2 * a.batch) {
+      const int g = e - a.batch;
+      if (groups && members[g] > 1 && least[g] > 0) {
+        const int first = max(0, min(__ldg(a.cu_groups + g), a.batch - 1)), lead = __ldg(a.group_rows + first);
+        x = make_int4(a.entry[2 * first].x, tokens[g] * G, max(0, min(lead, a.batch - 1)), 0);
+        y = make_int4(least[g], least[g] * kBlk, least[g] * kBlk, g);
+      }
+    }
+    if (e < 2 * a.batch) {
+      const int line = x.y > a.small_rows;
+      const int tile = line ? kBigRows : kSmallRows;
+      cost[line] = (long long)((x.y + tile - 1) / tile) * a.num_kv_heads * y.x * prefix_weight(line, x.y);
+    }
+#pragma unroll
+    for (int l = 0; l < 2; ++l) {
+      long long all;
+      const long long upto = cost_before[l] + block_upto<long long>(cost[l], s_sum, all);
+      if (e < 2 * a.batch) a.start[l * (2 * a.batch + 1) + e] = upto - cost[l];
+      cost_before[l] += all;
+    }
+    if (e < 2 * a.batch) {
+      a.work[2 * e] = x;
+      a.work[2 * e + 1] = y;
+    }
+  }
+  if (tid < 2) a.start[tid * (2 * a.batch + 1) + 2 * a.batch] = cost_before[tid];
+  if (tid == 0) *a.kept = s_kept;
+}
+
+// The partition of a line's [0, total) into the CTAs' ranges.
+struct Ranges {
+  long long total;
+  int n;
+  MSA_DEV long long start(int i) const { return total * i / n; }
+  // The range that position p < total is in: the last i with start(i) <= p.
+  MSA_DEV int holder(long long p) const { return (int)((p * n + n - 1) / total); }
+};
+MSA_DEV Ranges ranges_of(const PrefixArgs& a, int line) {
+  const long long total = __ldcg(a.start + line * (2 * a.batch + 1) + 2 * a.batch);
+  const long long most = total / (line ? a.big_range : a.small_range);
+  const int grid = line ? a.big_grid : a.small_grid;
+  return {total, (int)(most < 1 ? 1 : most < grid ? most : grid)};
+}
+
+// A piece of a unit: blocks [j0, j0 + n) of one entry's tile with one KV head.
+struct Piece {
+  int n;          // blocks; 0: no more
+  int b, h, j0;   // page row, KV head, first block
+  int row0, rows; // rows of the entry
+  int tau;        // the entry's first token
+  int hidden, lk; // row r sees keys below min(lk, hidden + r / G + 1)
+  int place;      // of row 0's parts: its own, or (below 0) the CTA's
+  int keys;       // keys from j0 on that some row sees
+};
+
+// Walks a CTA's range, piece by piece.
+struct Walk {
+  const PrefixArgs& a;
+  int line;
+  long long at, end;
+  int e;
+  MSA_DEV Walk(const PrefixArgs& args, int l, const Ranges& r, int cta) : a(args), line(l), at(0), end(0), e(0) {
+    if (r.total <= 0 || cta >= r.n) return;
+    at = r.start(cta), end = r.start(cta + 1);
+    const long long* start = a.start + line * (2 * a.batch + 1);
+    int lo = 0;  // the last entry that begins at or before `at`
+    for (int hi = 2 * a.batch; hi - lo > 1;) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldcg(start + mid) <= at) lo = mid; else hi = mid;
+    }
+    e = lo;
+  }
+  MSA_DEV bool next(Piece& p) {
+    p.n = 0;
+    while (at < end && p.n == 0) step(p);
+    return p.n > 0;
+  }
+  // The piece at `at`, which may hold no block's first position.
+  MSA_DEV void step(Piece& p) {
+    const long long* start = a.start + line * (2 * a.batch + 1);
+    while (__ldcg(start + e + 1) <= at) ++e;
+    const int4 x = __ldcg(a.work + 2 * e), y = __ldcg(a.work + 2 * e + 1);
+    const int G = a.num_qo_heads / a.num_kv_heads, tile_rows = line ? kBigRows : kSmallRows;
+    const int w = prefix_weight(line, x.y);
+    const long long len = (long long)y.x * w, rel = at - __ldcg(start + e);
+    const long long unit = rel / len;
+    const int in = (int)(rel - unit * len);
+    const long long unit_end = at - in + len, stop = unit_end < end ? unit_end : end;
+    // Block j belongs to the range that its first position is in.
+    const int j0 = (in + w - 1) / w, j1 = (int)((stop - (at - in) + w - 1) / w);
+    const int tile = (int)(unit / a.num_kv_heads);
+    at = stop;
+    p.n = j1 - j0;
+    p.b = x.z, p.h = (int)(unit - (long long)tile * a.num_kv_heads);
+    p.j0 = x.w + j0;
+    p.row0 = tile * tile_rows, p.rows = min(tile_rows, x.y - p.row0);
+    p.tau = x.x;
+    p.hidden = y.y, p.lk = y.z;
+    p.place = j0 == 0 ? (e >= a.batch ? a.total_q : 0) + x.x : -1;
+    const long long last = min((long long)y.z, (long long)y.y + (p.row0 + p.rows - 1) / G + 1) - (long long)p.j0 * kBlk;
+    p.keys = (int)max(0ll, min(last, (long long)p.n * kBlk));
+  }
+};
+
+// ------------------------------------------------------- few rows: 16 a tile
+// Eight warps take 16 keys each of a block, all 16 rows: S by warp-level MMAs
+// (the rows are too few for a tile of 128), its own softmax (m, l) and its own
+// O, so a warp waits for no other until the piece ends, where the eight are
+// joined. Bound by memory: a block of 64 KB takes an SM's share of the
+// bandwidth 3000 clocks. K and V come by TMA through a ring of blocks, one
+// warp ahead; the join borrows the next free slots of the ring.
+constexpr int kWarps = 8;
+template <int KV>  // 0 bf16, 1 f16, 2 E4M3 with bf16 q
+struct Small {
+  static constexpr int kSize = KV == 2 ? 1 : 2;
+  static constexpr int kTile = 128 * 128 * kSize;  // K or V of a block
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kStages = KV == 2 ? 6 : 3;
+  static constexpr int kJoin = kWarps * 16 * 128 * 4 / kStage;  // slots that eight O fill
+  static constexpr int kThreads = (kWarps + 1) * 32;
+};
+constexpr int kQStride = 272;  // bytes of a row of Q in shared memory
+template <int KV>
+struct __align__(1024) SmallSmem {
+  uint8_t stage[Small<KV>::kStages][Small<KV>::kStage];
+  uint8_t q[2][16 * kQStride];
+  Piece piece[2];
+  float2 ml[2][kWarps][16];
+  int page_ok[Small<KV>::kStages];
+  uint64_t piece_full[2], piece_empty[2], full[Small<KV>::kStages], empty[Small<KV>::kStages], join;
+  int abort;
+};
+static_assert(sizeof(SmallSmem<0>) <= 226 * 1024 && sizeof(SmallSmem<2>) <= 226 * 1024, "too much shared memory");
+
+MSA_DEV void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+MSA_DEV void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <bool F16>
+MSA_DEV void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+        "%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, "
+        "%2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+MSA_DEV uint32_t e4m3x2_to_f16(uint32_t pair) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)pair));
+  return h;
+}
+// Of two keys' 16 bits each: those below `n` kept.
+MSA_DEV uint32_t keep_keys(int first, int n) { return (first < n ? 0xffffu : 0u) | (first + 1 < n ? 0xffff0000u : 0u); }
+
+template <int KV>
+__global__ void __launch_bounds__(Small<KV>::kThreads, 1)
+    prefix_small_kernel(const __grid_constant__ PrefixArgs a) {
+  using C = Small<KV>;
+  constexpr bool kF16 = KV != 0;  // the MMAs' operands
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+  SmallSmem<KV>& sm = *reinterpret_cast<SmallSmem<KV>*>(smem_raw + pad);
+  unsigned* fault = a.fault;
+  volatile int* abort = &sm.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.num_qo_heads / a.num_kv_heads;
+  if (tid == 0) {
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&sm.piece_full[s], 33);
+      mbar_init(&sm.piece_empty[s], kWarps);
+    }
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&sm.full[s], 1);
+      mbar_init(&sm.empty[s], kWarps);
+    }
+    mbar_init(&sm.join, kWarps);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const Ranges ranges = ranges_of(a, 0);
+
+  if (warp == kWarps) {
+    // ------------------------------------------------------------- K, V and Q
+    if (lane == 0) {
+      tma_prefetch_desc(&a.tmap_k);
+      tma_prefetch_desc(&a.tmap_v);
+    }
+    Walk walk(a, 0, ranges, blockIdx.x);
+    bool ok = true;
+    int stage = 0, np = 0;
+    uint32_t turn = 0;  // of the ring: how often it has gone round
+    auto acquire = [&]() -> bool {  // the next slot, free
+      bool free = turn == 0 || mbar_wait_sleep(&sm.empty[stage], (turn - 1) & 1, fault, kFaultWaitSoftmax, abort);
+      return __all_sync(0xffffffffu, free);
+    };
+    auto advance = [&]() {
+      if (++stage == C::kStages) stage = 0, ++turn;
+    };
+    Piece p{};
+    while (ok) {
+      const bool more = walk.next(p);
+      const int slot = np & 1;
+      ok = np < 2 || mbar_wait_sleep(&sm.piece_empty[slot], ((np >> 1) - 1) & 1, fault, kFaultWaitSoftmax, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ++np;
+      if (more) {
+        // Q's rows of the tile, zeros behind them.
+        const uint8_t* q = static_cast<const uint8_t*>(a.q);
+        for (int i = lane; i < 256; i += 32) {
+          const int r = i >> 4, c = i & 15, row = p.row0 + r;
+          const bool live = r < p.rows;
+          size_t from = 0;
+          if (live) {
+            const int token = __ldcg(&a.token[p.tau + row / G].x);
+            from = ((size_t)token * a.num_qo_heads + (size_t)p.h * G + row % G) * 256 + c * 16;
+          }
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(sm.q[slot] + r * kQStride + c * 16)),
+                       "l"(q + from), "r"(live ? 16 : 0)
+                       : "memory");
+        }
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.piece_full[slot])) : "memory");
+      if (lane == 0) {
+        sm.piece[slot] = p;
+        mbar_arrive(&sm.piece_full[slot]);
+      }
+      __syncwarp();
+      if (!more) break;
+      const int blocks = (p.keys + kBlk - 1) / kBlk;
+      const int32_t* pages = a.page_table + (size_t)p.b * a.max_pages + p.j0;
+      int page32 = -1;
+      for (int j = 0; ok && j < blocks; ++j) {
+        if ((j & 31) == 0) page32 = j + lane < blocks ? __ldg(pages + j + lane) : -1;
+        const int page = __shfl_sync(0xffffffffu, page32, j & 31);
+        ok = acquire();
+        if (!ok) break;
+        if (lane == 0) {
+          const bool there = page >= 0 && page < a.num_pages;
+          sm.page_ok[stage] = there;
+          if (there) {
+            uint8_t* at = sm.stage[stage];
+            mbar_expect_tx(&sm.full[stage], C::kStage);
+            if constexpr (KV == 2) {
+              tma_load_4d(at, &a.tmap_k, &sm.full[stage], 0, 0, p.h, page);
+              tma_load_4d(at + C::kTile, &a.tmap_v, &sm.full[stage], 0, 0, p.h, page);
+            } else {
+              for (int c = 0; c < 2; ++c) {
+                tma_load_4d(at + c * 16384, &a.tmap_k, &sm.full[stage], c * 64, 0, p.h, page);
+                tma_load_4d(at + C::kTile + c * 16384, &a.tmap_v, &sm.full[stage], c * 64, 0, p.h, page);
+              }
+            }
+          } else {
+            mbar_arrive(&sm.full[stage]);
+          }
+        }
+        __syncwarp();
+        advance();
+      }
+      // The slots that the join uses.
+      for (int j = 0; ok && j < C::kJoin; ++j) {
+        ok = acquire();
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&sm.full[stage]);
+        advance();
+      }
+    }
+    // Copies in flight land before the CTA's shared memory is given back.
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (!ok) {
+      for (int s = 0; s < C::kStages; ++s) {
+        // The slot's last phase: the one of this turn for slots before `stage`.
+        const uint32_t t = s < stage ? turn : turn - 1;
+        if (s < stage || turn > 0) mbar_wait_sleep(&sm.full[s], t & 1, fault, kFaultWaitTma);
+      }
+    }
+    return;
+  }
+
+  // ---------------------------------------------------------------- the warps
+  const int g = lane >> 2, t = lane & 3;
+  int stage = 0, np = 0;
+  uint32_t turn = 0, joins = 0;
+  bool ok = true;
+  auto advance = [&]() {
+    if (++stage == C::kStages) stage = 0, ++turn;
+  };
+  while (true) {
+    const int slot = np & 1;
+    ok = mbar_wait_sleep(&sm.piece_full[slot], (np >> 1) & 1, fault, kFaultWaitOther, abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    ++np;
+    const Piece p = sm.piece[slot];
+    if (p.n == 0) break;
+    // Q as the products want it; with E4M3 keys as f16, each row scaled by a
+    // power of two that puts its largest value just below f16's largest, and
+    // with the dims in the order in which a thread reads K: its 32 of them.
+    uint32_t q[8][4];
+    float scale[2] = {a.scale_log2, a.scale_log2};
+    if constexpr (KV == 2) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        uint32_t w[16];
+        uint32_t big = 0u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sm.q[slot] + (g + 8 * r) * kQStride + t * 64 + c * 16);
+          w[4 * c] = x.x, w[4 * c + 1] = x.y, w[4 * c + 2] = x.z, w[4 * c + 3] = x.w;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) big = max(big, max(w[i] & 0x7f80u, (w[i] >> 16) & 0x7f80u));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const int e = (int)(big >> 7), k = e == 255 ? 0 : min(120, 142 - e);
+        const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+        scale[r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          q[i >> 1][r + 2 * (i & 1)] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
+      }
+    } else {
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks)
+        ldmatrix4(q[ks], smem_u32(sm.q[slot] + ((lane & 7) + ((lane >> 3) & 1) * 8) * kQStride + (ks * 2 + (lane >> 4)) * 16));
+    }
+    // Keys that rows g and g + 8 see, counted from the piece's first.
+    int sees[2];
+    const long long base = (long long)p.j0 * kBlk;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const long long lim = min((long long)p.lk, (long long)p.hidden + (p.row0 + g + 8 * r) / G + 1) - base;
+      sees[r] = (int)max(0ll, min(lim, (long long)p.keys));
+    }
+    const int all_see = (int)max(0ll, min(min((long long)p.lk, (long long)p.hidden + p.row0 / G + 1) - base, (long long)p.keys));
+    const int here = (int)max(0ll, min((long long)p.lk - base, (long long)p.n * kBlk));  // keys of the sequence
+    float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+    const int blocks = (p.keys + kBlk - 1) / kBlk;
+    for (int j = 0; j < blocks; ++j) {
+      ok = mbar_wait_sleep(&sm.full[stage], turn & 1, fault, kFaultWaitTma, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int k0 = j * kBlk + warp * 16;  // the warp's first key
+      if (k0 < p.keys && sm.page_ok[stage]) {
+        const uint32_t ks0 = smem_u32(sm.stage[stage]), vs0 = ks0 + C::kTile;
+        float s[2][4] = {};
+        if constexpr (KV == 2) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt) {
+            const int row = warp * 16 + nt * 8 + g;
+            const uint8_t* at = sm.stage[stage] + row * 128;
+            const uint4 x = *reinterpret_cast<const uint4*>(at + (((2 * t) ^ (row & 7)) << 4));
+            const uint4 y = *reinterpret_cast<const uint4*>(at + (((2 * t + 1) ^ (row & 7)) << 4));
+            const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+              mma16816<kF16>(s[nt], q[ks], e4m3x2_to_f16(w[ks] & 0xffffu), e4m3x2_to_f16(w[ks] >> 16));
+          }
+        } else {
+          const int row = warp * 16 + (lane >> 4) * 8 + (lane & 7);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks) {
+            const int c = ks * 2 + ((lane >> 3) & 1);
+            uint32_t b[4];
+            ldmatrix4(b, ks0 + (c >> 3) * 16384 + sw128_offset(row, c & 7));
+            mma16816<kF16>(s[0], q[ks], b[0], b[1]);
+            mma16816<kF16>(s[1], q[ks], b[2], b[3]);
+          }
+        }
+        if (k0 + 16 > all_see) {
+#pragma unroll
+          for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (k0 + nt * 8 + 2 * t + (c & 1) >= sees[c >> 1]) s[nt][c] = -INFINITY;
+        }
+        // The rows' maxima over the four threads that hold a row.
+        bool grows = false;
+        float alpha[2] = {1.f, 1.f}, ref[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = fmaxf(fmaxf(s[0][2 * r], s[0][2 * r + 1]), fmaxf(s[1][2 * r], s[1][2 * r + 1]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          update_max(mx != -INFINITY, mx, scale[r], m[r], l[r], alpha[r], grows);
+          ref[r] = m[r] == -INFINITY ? 0.f : m[r];
+        }
+        if (__any_sync(0xffffffffu, grows)) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) o[i][c] *= alpha[c >> 1];
+        }
+        uint32_t pa[4];
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float p0 = ex2(fmaf(s[nt][2 * r], scale[r], -ref[r])), p1 = ex2(fmaf(s[nt][2 * r + 1], scale[r], -ref[r]));
+            l[r] += p0 + p1;
+            pa[2 * nt + r] = pack_x2<kF16>(p0, p1);
+          }
+        // What the page holds behind the sequence's end may be anything.
+        const bool tail = k0 + 16 > here;
+        const uint32_t keep0 = keep_keys(k0 + 2 * t, here), keep1 = keep_keys(k0 + 8 + 2 * t, here);
+        const int vrow = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
+        if constexpr (KV == 2) {
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t v[4];
+            ldmatrix4_trans(v, vs0 + sw128_offset(vrow, cc * 2 + (lane >> 4)));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t b[2][2];  // [dim parity][keys 0-7, 8-15]
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                b[0][k] = e4m3x2_to_f16(__byte_perm(v[2 * h + k], 0u, 0x4420));
+                b[1][k] = e4m3x2_to_f16(__byte_perm(v[2 * h + k], 0u, 0x4431));
+                if (tail) b[0][k] &= k ? keep1 : keep0, b[1][k] &= k ? keep1 : keep0;
+              }
+              mma16816<kF16>(o[4 * cc + 2 * h], pa, b[0][0], b[0][1]);
+              mma16816<kF16>(o[4 * cc + 2 * h + 1], pa, b[1][0], b[1][1]);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int dn = 0; dn < 8; ++dn) {
+            const int c = dn * 2 + (lane >> 4);
+            uint32_t v[4];
+            ldmatrix4_trans(v, vs0 + (c >> 3) * 16384 + sw128_offset(vrow, c & 7));
+            if (tail) v[0] &= keep0, v[1] &= keep1, v[2] &= keep0, v[3] &= keep1;
+            mma16816<kF16>(o[2 * dn], pa, v[0], v[1]);
+            mma16816<kF16>(o[2 * dn + 1], pa, v[2], v[3]);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.empty[stage]);
+      advance();
+    }
+    if (!ok) break;
+    // ------------------------------------------------------------------ joined
+    const int js = stage;
+    for (int j = 0; ok && j < C::kJoin; ++j) {
+      ok = mbar_wait_sleep(&sm.full[stage], turn & 1, fault, kFaultWaitOther, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      advance();
+    }
+    if (!ok) break;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+      if (m[r] == -INFINITY && !(l[r] == 0.f)) m[r] = 0.f;  // nothing but NaN
+      if (t == 0) sm.ml[slot][warp][g + 8 * r] = make_float2(m[r], l[r]);
+    }
+    // Warp w's O: row r, column c at r * 128 + (c ^ 8 (r & 3)) of its 8 KB.
+    auto o_of = [&](int w) -> float* {
+      const int byte = w * 8192, s = js + byte / C::kStage;
+      return reinterpret_cast<float*>(sm.stage[s >= C::kStages ? s - C::kStages : s] + byte % C::kStage);
+    };
+    float* mine = o_of(warp);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = g + 8 * r, x = (row & 3) << 3;
+      if constexpr (KV == 2) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          *reinterpret_cast<float4*>(mine + row * 128 + ((16 * c + 4 * t) ^ x)) =
+              make_float4(o[2 * c][2 * r], o[2 * c + 1][2 * r], o[2 * c][2 * r + 1], o[2 * c + 1][2 * r + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          *reinterpret_cast<float2*>(mine + row * 128 + ((8 * i + 2 * t) ^ x)) = make_float2(o[i][2 * r], o[i][2 * r + 1]);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.join);
+    ok = mbar_wait_sleep(&sm.join, joins & 1, fault, kFaultWaitOther, abort);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) break;
+    ++joins;
+    const int row = tid >> 4, col = (tid & 15) * 8;
+    float M = -INFINITY, L = 0.f, sum[8] = {};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[slot][w][row].x);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 ml = sm.ml[slot][w][row];
+      if (ml.x == -INFINITY) continue;
+      const float f = ex2(ml.x - M);
+      L += f * ml.y;
+      const float* from = o_of(w) + row * 128 + (col ^ ((row & 3) << 3));
+      const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 4);
+      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) sum[c] = fmaf(f, v[c], sum[c]);
+    }
+    if (row < p.rows) {
+      const int r = p.row0 + row;
+      const size_t at = p.place >= 0 ? (size_t)(p.place + r / G) * a.num_qo_heads + (size_t)p.h * G + r % G
+                                     : a.part_rows + (size_t)blockIdx.x * kSmallRows + row;
+      float4* to = reinterpret_cast<float4*>(a.part_o + at * kHeadDim + col);
+      to[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      to[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+      if (col == 0) a.part_ml[at] = make_float2(M, L);
+    }
+    fence_async_smem();  // the slots are TMA's again
+    __syncwarp();
+    if (lane == 0) {
+      for (int j = 0, s = js; j < C::kJoin; ++j, s = s + 1 == C::kStages ? 0 : s + 1) mbar_arrive(&sm.empty[s]);
+      mbar_arrive(&sm.piece_empty[slot]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the join
+// One row's own run from its own visible keys, in fp32, by a warp: a lane takes
+// a key of 32, and then four columns of their V. Rows of a tile share the
+// products, so a row also multiplies, by P = 0, later tokens' values, which may
+// be infinite or NaN: such rows are computed anew here.
+__device__ __noinline__ void own_run(const PrefixArgs& a, size_t orow, int b, int h, int block0, int sees, int lane,
+                                     float& m, float& l, float (&acc)[4]) {
+  auto value = [&](const uint8_t* rows, int i, bool e4m3) {
+    if (e4m3) {
+      const uint32_t h2 = e4m3x2_to_f16(__ldg(rows + i));
+      return __low2float(*reinterpret_cast<const __half2*>(&h2));
+    }
+    const uint16_t w = __ldg(reinterpret_cast<const uint16_t*>(rows) + i);
+    return a.f16 ? __half2float(__ushort_as_half(w)) : __uint_as_float((uint32_t)w << 16);
+  };
+  const uint8_t* q = static_cast<const uint8_t*>(a.q) + orow * kHeadDim * 2;
+  m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) acc[c] = 0.f;
+  for (int k0 = block0 * kBlk; k0 < sees; k0 += 32) {
+    const int page = k0 / kBlk < a.max_pages ? __ldg(a.page_table + (size_t)b * a.max_pages + k0 / kBlk) : -1;
+    if (page < 0 || page >= a.num_pages) continue;
+    const size_t at = ((size_t)page * a.num_kv_heads + h) * kBlk * kHeadDim * (a.e4m3 ? 1 : 2);
+    const int in = k0 % kBlk, n = min(32, sees - k0);
+    float s = -INFINITY;
+    if (lane < n) {
+      s = 0.f;
+#pragma unroll 8
+      for (int c = 0; c < kHeadDim; ++c)
+        s = fmaf(value(q, c, false), value(a.k_pool + at, (in + lane) * kHeadDim + c, a.e4m3), s);
+      s *= a.scale_log2;
+    }
+    float top = s;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    top = fmaxf(top, m);
+    const bool nan = __any_sync(0xffffffffu, s != s);
+    if (top == -INFINITY && !nan) continue;
+    const float alpha = m == -INFINITY ? 0.f : ex2(m - top);
+    const float p = s == -INFINITY ? 0.f : ex2(s - top);
+    m = top;
+    l *= alpha;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] *= alpha;
+    for (int x = 0; x < n; ++x) {
+      const float px = __shfl_sync(0xffffffffu, p, x);
+      l += px;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        acc[c] = fmaf(px, value(a.v_pool + at, (in + x) * kHeadDim + 4 * lane + c, a.e4m3), acc[c]);
+    }
+  }
+  if (m == -INFINITY && !(l == 0.f)) m = 0.f;
+}
+
+// A warp for each row; a lane has four columns. The parts of the group's run,
+// then those of the own one, each in the order of its pieces.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(kJoinWarps * 32)
+    prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
+  const int lane = threadIdx.x & 31, G = a.num_qo_heads / a.num_kv_heads;
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const long long rows = (long long)__ldcg(a.kept) * a.num_qo_heads;
+  const Ranges lines[2] = {ranges_of(a, 0), ranges_of(a, 1)};
+  for (long long i = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5); i < rows; i += (long long)gridDim.x * kJoinWarps) {
+    const int tau = (int)(i / a.num_qo_heads), hq = (int)(i - (long long)tau * a.num_qo_heads), h = hq / G;
+    const int2 token = __ldcg(a.token + tau);
+    const size_t orow = (size_t)token.x * a.num_qo_heads + hq;
+    const int group = __ldcg(&a.work[2 * token.y + 1].w);
+    float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    auto add = [&](float m, float l, float4 o) {
+      if (m == -INFINITY) return;  // a part without a visible key may hold anything
+      const float top = fmaxf(M, m), f = M == -INFINITY ? 0.f : ex2(M - top), p = ex2(m - top);
+      M = top;
+      L = fmaf(L, f, p * l);
+      acc[0] = fmaf(p, o.x, acc[0] * f), acc[1] = fmaf(p, o.y, acc[1] * f);
+      acc[2] = fmaf(p, o.z, acc[2] * f), acc[3] = fmaf(p, o.w, acc[3] * f);
+    };
+    auto add_at = [&](size_t at) {
+      const float2 ml = __ldcg(a.part_ml + at);
+      add(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.part_o + at * kHeadDim) + lane));
+    };
+    auto run = [&](int e, bool prefix) {
+      const int4 x = __ldcg(a.work + 2 * e);
+      const int blocks = __ldcg(&a.work[2 * e + 1].x);
+      if (blocks == 0) return;
+      const int line = x.y > a.small_rows, r = (tau - x.x) * G + hq % G;
+      const int tile_rows = line ? kBigRows : kSmallRows, tile = r / tile_rows;
+      const int w = prefix_weight(line, x.y);
+      const long long len = (long long)blocks * w;
+      const long long at = __ldcg(a.start + line * (2 * a.batch + 1) + e) + ((long long)tile * a.num_kv_heads + h) * len;
+      const int c0 = lines[line].holder(at), c1 = lines[line].holder(at + len - w);
+      add_at((size_t)((prefix ? a.total_q : 0) + tau) * a.num_qo_heads + hq);
+      const size_t slots = a.part_rows + (line ? (size_t)a.small_grid * kSmallRows : 0);
+      for (int c = c0 + 1; c <= c1; ++c) add_at(slots + (size_t)c * tile_rows + (r - tile * tile_rows));
+    };
+    if (a.group_rows != nullptr) run(a.batch + group, true);
+    const float gm = M, gl = L, g0 = acc[0], g1 = acc[1], g2 = acc[2], g3 = acc[3];
+    run(token.y, false);
+    const float odd = acc[0] * 0.f + acc[1] * 0.f + acc[2] * 0.f + acc[3] * 0.f;
+    const int4 x = __ldcg(a.work + 2 * token.y);
+    if (a.causal && x.y > G && __any_sync(0xffffffffu, !(odd == 0.f && L < INFINITY))) {
+      const int4 y = __ldcg(a.work + 2 * token.y + 1);
+      float m, l, o[4];
+      const int sees = (int)min((long long)y.z, (long long)y.y + (tau - x.x) + 1);
+      own_run(a, orow, x.z, h, x.w, sees, lane, m, l, o);
+      M = gm, L = gl, acc[0] = g0, acc[1] = g1, acc[2] = g2, acc[3] = g3;
+      add(m, l, make_float4(o[0], o[1], o[2], o[3]));
+    }
+    const bool has = L != 0.f;
+    const float inv = has ? 1.f / L : 0.f;
+    auto pack = [&](float x, float y) { return a.f16 ? pack_f16x2(x, y) : pack_bf16x2(x, y); };
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * kHeadDim)[lane] =
+        make_uint2(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv));
+    if (lane == 0 && a.lse != nullptr) a.lse[orow] = has ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+template <int KV>
+cudaError_t launch_small(const PrefixArgs& a, cudaStream_t s) {
+  const int smem = (int)sizeof(SmallSmem<KV>) + 1024;
+  cudaError_t e = set_smem_limit((const void*)prefix_small_kernel<KV>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(prefix_small_kernel<KV>, dim3(a.small_grid), Small<KV>::kThreads, smem, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix(const PrefixArgs& a, cudaStream_t s) {
+  const int smem = 3 * a.batch * (int)sizeof(int);
+  cudaError_t e = set_smem_limit((const void*)prefix_plan_kernel, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(prefix_plan_kernel, dim3(1), kPlanThreads, smem, s, a);
+  if (e != cudaSuccess) return e;
+  e = a.e4m3 ? launch_small<2>(a, s) : a.f16 ? launch_small<1>(a, s) : launch_small<0>(a, s);
+  if (e != cudaSuccess) return e;
+  const long long rows = (long long)a.total_q * a.num_qo_heads;
+  const long long blocks = (rows + kJoinWarps - 1) / kJoinWarps;
+  return launch_dependent(prefix_join_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), kJoinWarps * 32, 0, s, a);
+}
+
+}  // namespace msa

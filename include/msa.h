@@ -271,6 +271,60 @@ msa_status_t msa_tree_attention_prepare(
     size_t workspace_bytes, msa_attention_plan_t** plan);
 
 /*
+ * Attention of all of a request's keys over a paged cache, where groups of
+ * requests share their first pages: those are read and multiplied once for all
+ * tokens of a group. Prompts that were forked into samples (msa_cache_fork)
+ * are such groups; msa_step_tables finds them.
+ *
+ * A request's Lq query tokens are its last Lq keys as well; causal, token i
+ * sees the keys up to its own, Lk - Lq + i, else all Lk. A block without a
+ * page has no keys. A row that sees none is 0, with lse -inf.
+ *   q            device, MSA_BF16 or MSA_FP16, (total_q, Hq, 128)
+ *   k, v         device, (num_pages, Hkv, 128, 128) of q's dtype, or
+ *                MSA_FP8_E4M3 with bf16 q
+ *   cu_seqlens_q device int32 (B + 1); page_table device int32 (B, max_pages);
+ *                seqused_k device int32 (B), Lk
+ *   group_rows, cu_groups, group_blocks  device int32 (B), (B + 1), (B), as
+ *                msa_step_tables writes them, or NULL all three (each request
+ *                by itself). Each request is listed once. The rows of
+ *                page_table of a group's requests agree in its first
+ *                group_blocks blocks (the first request's pages are read); of
+ *                those, the ones that lie before every new token of the group
+ *                are attended for all, the others by each request.
+ *   softmax_scale  0 or below: 1 / sqrt(128)
+ *   out          device, as q; another tensor than q
+ *   lse          device float32 (total_q, Hq) or NULL: natural log
+ *   workspace    msa_prefix_attention_workspace_size(...) bytes (groups: whether
+ *                they are given), 256-byte aligned, uninitialised; calls that
+ *                share one must be ordered on the device
+ * Rows at or past cu_seqlens_q[B], and those of requests that no group lists,
+ * are left as they were. What a token does not see may hold anything,
+ * infinities and NaN included; one that sees a NaN gets NaN. The same inputs
+ * give the same bits. MSA_INVALID_ARG for a NULL or misaligned pointer, some of
+ * the group arrays without the others, sizes below 1 (total_q may be 0) or q as
+ * out; MSA_UNSUPPORTED for head_dim != 128, another dtype, Hq / Hkv above 128,
+ * more than 16384 requests, max_pages above 2^23 or total_q * Hq >= 2^30.
+ * msa_prefix_attention_prepare binds the call into a plan that
+ * msa_sparse_attention_run launches.
+ */
+size_t msa_prefix_attention_workspace_size(int batch, int total_q, int num_qo_heads,
+                                           int num_kv_heads, int head_dim, int groups);
+msa_status_t msa_prefix_attention(
+    const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
+    const int32_t* cu_seqlens_q, const int32_t* page_table, int max_pages, int num_pages,
+    const int32_t* seqused_k, const int32_t* group_rows, const int32_t* cu_groups,
+    const int32_t* group_blocks, int batch, int total_q, int num_qo_heads, int num_kv_heads,
+    int head_dim, int causal, float softmax_scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, cudaStream_t stream);
+msa_status_t msa_prefix_attention_prepare(
+    const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
+    const int32_t* cu_seqlens_q, const int32_t* page_table, int max_pages, int num_pages,
+    const int32_t* seqused_k, const int32_t* group_rows, const int32_t* cu_groups,
+    const int32_t* group_blocks, int batch, int total_q, int num_qo_heads, int num_kv_heads,
+    int head_dim, int causal, float softmax_scale, void* out, float* lse, void* workspace,
+    size_t workspace_bytes, msa_attention_plan_t** plan);
+
+/*
  * Norms of queries and keys for each head, with the position rotation in the
  * same pass: what makes the attention's q and k out of a projection's output.
  *
