@@ -118,7 +118,7 @@ def lib():
         L.msa_cache_accept.restype = i32
         L.msa_cache_accept.argtypes = [C.POINTER(vp), i32, i32, i32, vp, i32, i32, i32, vp, vp, vp,
                                        vp, i32, vp, vp]
-        prefix = [vp, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp, sz]
+        prefix = [vp, i32, vp, vp, i32, vp, vp, i32, i32, vp, vp, vp, vp] + [i32] * 7 + [f32, vp, vp, vp, sz]
         L.msa_prefix_attention_workspace_size.restype = sz
         L.msa_prefix_attention_workspace_size.argtypes = [i32] * 6
         L.msa_prefix_attention.restype = i32
@@ -790,12 +790,12 @@ def msa_prefix_attention(q, k, v, cu_seqlens_q, *, page_table, seqused_k, group_
     """Attention of all keys of each request over a paged cache, in which the
     first pages that groups of requests share are attended once for all of a
     group; see ``msa_prefix_attention`` in include/msa.h. The groups are those of
-    a ``StepTables``; without them each request is by itself. Returns ``out`` or
-    ``(out, lse)``. ``max_seqlen_q``, which the other attentions take, is not needed
-    and not looked at."""
+    a ``StepTables``; without them each request is by itself. ``max_seqlen_q`` bounds
+    every request's tokens; None (nothing known) does not read the device. Returns
+    ``out`` or ``(out, lse)``."""
     out, lse, _, _ = (_native or _step()).prefix_attention(
-        q, k, v, cu_seqlens_q, page_table, seqused_k, group_rows, cu_groups, group_blocks, causal,
-        softmax_scale, return_softmax_lse, out, lse, workspace, stream, False)
+        q, k, v, cu_seqlens_q, page_table, seqused_k, group_rows, cu_groups, group_blocks,
+        max_seqlen_q, causal, softmax_scale, return_softmax_lse, out, lse, workspace, stream, False)
     return out if lse is None else (out, lse)
 
 
@@ -805,11 +805,11 @@ class PrefixAttentionRunner(SparseAttentionRunner):
     ``SparseAttentionRunner``."""
 
     def __init__(self, q, k, v, cu_seqlens_q, *, page_table, seqused_k, group_rows=None,
-                 cu_groups=None, group_blocks=None, causal=True, softmax_scale=None,
-                 return_softmax_lse=False, out=None, lse=None, workspace=None):
+                 cu_groups=None, group_blocks=None, max_seqlen_q=None, causal=True,
+                 softmax_scale=None, return_softmax_lse=False, out=None, lse=None, workspace=None):
         self.out, self.lse, self.workspace, plan = (_native or _step()).prefix_attention(
             q, k, v, cu_seqlens_q, page_table, seqused_k, group_rows, cu_groups, group_blocks,
-            causal, softmax_scale, return_softmax_lse, out, lse, workspace, None, True)
+            max_seqlen_q, causal, softmax_scale, return_softmax_lse, out, lse, workspace, None, True)
         self._bound = (q, k, v, cu_seqlens_q, page_table, seqused_k, group_rows, cu_groups,
                        group_blocks)
         self._plan = C.c_void_p(plan)

@@ -837,7 +837,7 @@ msa_status_t build_prefix(
     const int32_t* cu_seqlens_q, const int32_t* page_table, int max_pages, int num_pages,
     const int32_t* seqused_k, const int32_t* group_rows, const int32_t* cu_groups,
     const int32_t* group_blocks, int batch, int total_q, int num_qo_heads, int num_kv_heads,
-    int head_dim, int causal, float softmax_scale, void* out, float* lse, void* workspace,
+    int head_dim, int max_seqlen_q, int causal, float softmax_scale, void* out, float* lse, void* workspace,
     size_t workspace_bytes, ForwardPlan* plan) {
   if (batch < 1 || total_q < 0 || num_qo_heads < 1 || num_kv_heads < 1 ||
       num_qo_heads % num_kv_heads != 0 || max_pages < 1 || num_pages < 1)
@@ -846,6 +846,7 @@ msa_status_t build_prefix(
       seqused_k == nullptr || out == nullptr)
     return MSA_INVALID_ARG;
   const bool groups = group_rows != nullptr;
+  if (max_seqlen_q < 0) return MSA_INVALID_ARG;
   if (groups != (cu_groups != nullptr) || groups != (group_blocks != nullptr)) return MSA_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) ||
       !aligned(cu_seqlens_q, 4) || !aligned(page_table, 4) || !aligned(seqused_k, 4) ||
@@ -894,7 +895,9 @@ msa_status_t build_prefix(
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = out;
   a.lse = lse;
-  a.small_rows = INT_MAX;
+  // Without groups and with few rows a request there is no unit of many rows.
+  const long long most = (long long)max_seqlen_q * (num_qo_heads / num_kv_heads);
+  a.small_rows = !groups && max_seqlen_q > 0 && most <= kSmallRows ? INT_MAX : kSmallRows;
   a.small_grid = a.big_grid = kPlanSMs;
   a.small_range = 1;
   a.big_range = 8;
@@ -1203,14 +1206,14 @@ size_t msa_prefix_attention_workspace_size(int batch, int total_q, int num_qo_he
 #define MSA_PREFIX_ARGS                                                                            \
   q, q_dtype, k, v, kv_dtype, cu_seqlens_q, page_table, max_pages, num_pages, seqused_k,           \
       group_rows, cu_groups, group_blocks, batch, total_q, num_qo_heads, num_kv_heads, head_dim,   \
-      causal, softmax_scale, out, lse, workspace, workspace_bytes
+      max_seqlen_q, causal, softmax_scale, out, lse, workspace, workspace_bytes
 
 msa_status_t msa_prefix_attention(
     const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
     const int32_t* cu_seqlens_q, const int32_t* page_table, int max_pages, int num_pages,
     const int32_t* seqused_k, const int32_t* group_rows, const int32_t* cu_groups,
     const int32_t* group_blocks, int batch, int total_q, int num_qo_heads, int num_kv_heads,
-    int head_dim, int causal, float softmax_scale, void* out, float* lse, void* workspace,
+    int head_dim, int max_seqlen_q, int causal, float softmax_scale, void* out, float* lse, void* workspace,
     size_t workspace_bytes, cudaStream_t stream) {
   msa::ForwardPlan p;
   const msa_status_t st = msa::build_prefix(MSA_PREFIX_ARGS, &p);
@@ -1223,7 +1226,7 @@ msa_status_t msa_prefix_attention_prepare(
     const int32_t* cu_seqlens_q, const int32_t* page_table, int max_pages, int num_pages,
     const int32_t* seqused_k, const int32_t* group_rows, const int32_t* cu_groups,
     const int32_t* group_blocks, int batch, int total_q, int num_qo_heads, int num_kv_heads,
-    int head_dim, int causal, float softmax_scale, void* out, float* lse, void* workspace,
+    int head_dim, int max_seqlen_q, int causal, float softmax_scale, void* out, float* lse, void* workspace,
     size_t workspace_bytes, msa_attention_plan_t** plan_out) {
   if (plan_out == nullptr) return MSA_INVALID_ARG;
   *plan_out = nullptr;

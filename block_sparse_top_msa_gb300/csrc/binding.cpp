@@ -362,12 +362,12 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // ------------------------------------------------- attention, shared prefixes
 // q, k, v, cu_seqlens_q, page_table, seqused_k, group_rows, cu_groups,
-// group_blocks (or None), causal, softmax_scale (or None), return_softmax_lse,
-// out, lse, workspace, stream, prepare: (out, lse or None, workspace, plan or
-// None).
+// group_blocks (or None), max_seqlen_q (or None), causal, softmax_scale (or
+// None), return_softmax_lse, out, lse, workspace, stream, prepare: (out, lse or
+// None, workspace, plan or None).
 PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
-  want_args("msa_prefix_attention", n, 17);
+  want_args("msa_prefix_attention", n, 18);
   const Tensor& q = tensor("q", a[0]);
   check_place("q", q, nullptr);
   if (!is_16bit(q.scalar_type())) wrong_dtype("q", q, "bfloat16 or float16");
@@ -389,22 +389,23 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     cu_groups = ptr<const int32_t>(dense("cu_groups", a[7], &dev, at::kInt, {rows + 1}));
     blocks = ptr<const int32_t>(dense("group_blocks", a[8], &dev, at::kInt, {rows}));
   }
-  const int causal = as_flag(a[9]);
-  const float scale = a[10] == Py_None ? 0.f : as_float(a[10]);
-  const Place place(dev, a[15]);
+  const int max_q = a[9] == Py_None ? 0 : as_int(a[9]);
+  const int causal = as_flag(a[10]);
+  const float scale = a[11] == Py_None ? 0.f : as_float(a[11]);
+  const Place place(dev, a[16]);
   const int total = size32("q", q.size(0)), hq = size32("q", q.size(1)), hkv = size32("k", k.size(1));
   const int max_pages = size32("page_table", pt.size(1)), pages = size32("k", k.size(0)), batch = size32("cu", rows);
   const msa_dtype_t qt = code(q.scalar_type()), kt = code(k.scalar_type());
-  const Tensor out = output("out", a[12], dev, q.scalar_type(), q.sizes());
+  const Tensor out = output("out", a[13], dev, q.scalar_type(), q.sizes());
   Tensor lse;
-  if (a[13] != Py_None || as_flag(a[11])) lse = output("lse", a[13], dev, at::kFloat, Shape{total, hq});
-  const Tensor ws = workspace(a[14], dev, msa_prefix_attention_workspace_size(batch, total, hq, hkv, 128, given));
-  const bool prepare = as_flag(a[16]);
+  if (a[14] != Py_None || as_flag(a[12])) lse = output("lse", a[14], dev, at::kFloat, Shape{total, hq});
+  const Tensor ws = workspace(a[15], dev, msa_prefix_attention_workspace_size(batch, total, hq, hkv, 128, given));
+  const bool prepare = as_flag(a[17]);
   msa_attention_plan_t* plan = nullptr;
 #define MSA_PREFIX_CALL                                                                                          \
   q.data_ptr(), qt, k.data_ptr(), v.data_ptr(), kt, ptr<const int32_t>(cu), ptr<const int32_t>(pt), max_pages,   \
-      pages, ptr<const int32_t>(used), group_rows, cu_groups, blocks, batch, total, hq, hkv, 128, causal, scale, \
-      out.data_ptr(), lse.defined() ? ptr<float>(lse) : nullptr, ws.data_ptr(), (size_t)ws.numel()
+      pages, ptr<const int32_t>(used), group_rows, cu_groups, blocks, batch, total, hq, hkv, 128, max_q, causal, \
+      scale, out.data_ptr(), lse.defined() ? ptr<float>(lse) : nullptr, ws.data_ptr(), (size_t)ws.numel()
   if (prepare) check("msa_prefix_attention_prepare", msa_prefix_attention_prepare(MSA_PREFIX_CALL, &plan));
   else if (total > 0) check("msa_prefix_attention", msa_prefix_attention(MSA_PREFIX_CALL, place.stream()));
 #undef MSA_PREFIX_CALL

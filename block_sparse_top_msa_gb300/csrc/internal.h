@@ -209,7 +209,7 @@ struct PrefixArgs {
   float scale_log2 = 0.f;
   void* out = nullptr;
   float* lse = nullptr;
-  int small_rows = 0;  // entries of more rows go to line 1
+  int small_rows = 0;  // entries of more rows go to line 1; INT_MAX: there is none
   int small_grid = 0, big_grid = 0, small_range = 0, big_range = 0;  // CTAs, and the least cost of a range
   // Workspace. Positions: the requests in the order of the groups; entries: the
   // positions' own runs, then the groups'.
@@ -223,6 +223,7 @@ struct PrefixArgs {
   float* part_o = nullptr;     // the same, 128 each
 };
 cudaError_t launch_prefix(const PrefixArgs& a, cudaStream_t s);
+cudaError_t launch_prefix_big(const PrefixArgs& a, cudaStream_t s);  // line 1 (prefix_big.cu)
 
 struct ProxyArgs {
   unsigned* fault;      // device fault word (bounded-wait expiry, capacity)

@@ -291,6 +291,7 @@ msa_status_t msa_tree_attention_prepare(
  *                group_blocks blocks (the first request's pages are read); of
  *                those, the ones that lie before every new token of the group
  *                are attended for all, the others by each request.
+ *   max_seqlen_q host bound on every Lq, or 0 when unknown
  *   softmax_scale  0 or below: 1 / sqrt(128)
  *   out          device, as q; another tensor than q
  *   lse          device float32 (total_q, Hq) or NULL: natural log
@@ -314,14 +315,14 @@ msa_status_t msa_prefix_attention(
     const int32_t* cu_seqlens_q, const int32_t* page_table, int max_pages, int num_pages,
     const int32_t* seqused_k, const int32_t* group_rows, const int32_t* cu_groups,
     const int32_t* group_blocks, int batch, int total_q, int num_qo_heads, int num_kv_heads,
-    int head_dim, int causal, float softmax_scale, void* out, float* lse, void* workspace,
+    int head_dim, int max_seqlen_q, int causal, float softmax_scale, void* out, float* lse, void* workspace,
     size_t workspace_bytes, cudaStream_t stream);
 msa_status_t msa_prefix_attention_prepare(
     const void* q, msa_dtype_t q_dtype, const void* k, const void* v, msa_dtype_t kv_dtype,
     const int32_t* cu_seqlens_q, const int32_t* page_table, int max_pages, int num_pages,
     const int32_t* seqused_k, const int32_t* group_rows, const int32_t* cu_groups,
     const int32_t* group_blocks, int batch, int total_q, int num_qo_heads, int num_kv_heads,
-    int head_dim, int causal, float softmax_scale, void* out, float* lse, void* workspace,
+    int head_dim, int max_seqlen_q, int causal, float softmax_scale, void* out, float* lse, void* workspace,
     size_t workspace_bytes, msa_attention_plan_t** plan);
 
 /*

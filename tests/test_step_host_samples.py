@@ -92,15 +92,15 @@ def test_fp32_is_no_type_of_the_attention(L):
     assert L.msa_sparse_attention_fwd(P, 3, P, P, 3, P, 4, P, P, None, 0, 0, None, 1, 0, 128, 4, 2, 128, 32, 1, C.c_float(0.0), P, None, P, 1 << 30, None) == UNSUPPORTED
 
 
-PREFIX = "q dt k v kdt cu pt mp np su rows ends blocks b t hq hkv d causal scale out lse ws wb s".split()
-PREFIX_GOOD = dict(q=at(0), dt=0, k=at(1), v=at(2), kdt=0, cu=at(3), pt=at(4), mp=4, np=4, su=at(5), rows=at(6), ends=at(7), blocks=at(8), b=1, t=0, hq=8, hkv=2, d=128, causal=1, scale=C.c_float(0.0),
+PREFIX = "q dt k v kdt cu pt mp np su rows ends blocks b t hq hkv d mq causal scale out lse ws wb s".split()
+PREFIX_GOOD = dict(q=at(0), dt=0, k=at(1), v=at(2), kdt=0, cu=at(3), pt=at(4), mp=4, np=4, su=at(5), rows=at(6), ends=at(7), blocks=at(8), b=1, t=0, hq=8, hkv=2, d=128, mq=0, causal=1, scale=C.c_float(0.0),
                    out=at(9), lse=None, ws=P, wb=1 << 30, s=None)
 
 
 @pytest.mark.parametrize("bad,status", [(dict(), OK), (dict(rows=None, ends=None, blocks=None), OK), (dict(kdt=2), OK), (dict(dt=1, kdt=1), OK), (dict(q=None), INVALID),
                                         (dict(k=ODD), INVALID), (dict(v=None), INVALID), (dict(cu=ODD), INVALID), (dict(pt=None), INVALID), (dict(su=None), INVALID),
                                         (dict(rows=None), INVALID), (dict(ends=None), INVALID), (dict(blocks=None), INVALID), (dict(rows=ODD), INVALID), (dict(b=0), INVALID),
-                                        (dict(t=-1), INVALID), (dict(mp=0), INVALID), (dict(np=0), INVALID), (dict(hq=9), INVALID), (dict(hkv=0), INVALID), (dict(out=None), INVALID),
+                                        (dict(t=-1), INVALID), (dict(mq=-1), INVALID), (dict(mp=0), INVALID), (dict(np=0), INVALID), (dict(hq=9), INVALID), (dict(hkv=0), INVALID), (dict(out=None), INVALID),
                                         (dict(t=1, out=at(0)), INVALID), (dict(lse=ODD), INVALID), (dict(ws=C.c_void_p(0x10010)), INVALID), (dict(d=64), UNSUPPORTED),
                                         (dict(hq=258), UNSUPPORTED), (dict(b=16385), UNSUPPORTED), (dict(mp=(1 << 23) + 1), UNSUPPORTED), (dict(kdt=1), UNSUPPORTED),
                                         (dict(dt=1, kdt=2), UNSUPPORTED), (dict(dt=3), UNSUPPORTED), (dict(kdt=3), UNSUPPORTED), (dict(t=1 << 28), UNSUPPORTED),
