@@ -803,7 +803,7 @@ msa_status_t build_tree(
 
 // Workspace of the attention over shared prefixes.
 struct PrefixLayout {
-  size_t off_work, off_start, off_token, off_kept, off_ml, off_o, part_rows, total;
+  size_t off_group, off_work, off_start, off_chunk, off_token, off_meta, off_cut, off_odd, off_ml, off_o, part_rows, total;
 };
 constexpr int kPrefixMaxPages = 1 << 23;  // tokens of a row's pages are counted in 32 bits
 
@@ -815,10 +815,14 @@ PrefixLayout prefix_layout(int batch, int total_q, int hq, bool groups) {
     off += up256(bytes);
     return at;
   };
-  L.off_work = place((size_t)batch * 4 * sizeof(int4));
+  L.off_group = place((size_t)batch * sizeof(int));
+  L.off_work = place((size_t)batch * 8 * sizeof(int4));
   L.off_start = place(2 * (2 * (size_t)batch + 1) * sizeof(long long));
+  L.off_chunk = place((2 * (size_t)batch + 1) * sizeof(int));
   L.off_token = place((size_t)total_q * sizeof(int2));
-  L.off_kept = place(sizeof(int));
+  L.off_meta = place(4 * sizeof(int));
+  L.off_cut = place((size_t)kPlanSMs * sizeof(int4));
+  L.off_odd = place((size_t)total_q * hq * sizeof(int));
   L.part_rows = (size_t)total_q * hq * (groups ? 2 : 1);
   const size_t rows = L.part_rows + (size_t)kPlanSMs * (kSmallRows + kBigRows);
   L.off_ml = place(rows * sizeof(float2));
@@ -899,13 +903,15 @@ msa_status_t build_prefix(
   const long long most = (long long)max_seqlen_q * (num_qo_heads / num_kv_heads);
   a.small_rows = !groups && max_seqlen_q > 0 && most <= kSmallRows ? INT_MAX : kSmallRows;
   a.small_grid = a.big_grid = kPlanSMs;
-  a.small_range = 1;
-  a.big_range = 8;
   a.entry = reinterpret_cast<int4*>(ws);
   a.work = reinterpret_cast<int4*>(ws + L.off_work);
   a.start = reinterpret_cast<long long*>(ws + L.off_start);
   a.token = reinterpret_cast<int2*>(ws + L.off_token);
-  a.kept = reinterpret_cast<int*>(ws + L.off_kept);
+  a.group = reinterpret_cast<int*>(ws + L.off_group);
+  a.chunk = reinterpret_cast<int*>(ws + L.off_chunk);
+  a.meta = reinterpret_cast<int*>(ws + L.off_meta);
+  a.cut = reinterpret_cast<int4*>(ws + L.off_cut);
+  a.odd = reinterpret_cast<int*>(ws + L.off_odd);
   a.part_rows = L.part_rows;
   a.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
   a.part_o = reinterpret_cast<float*>(ws + L.off_o);

@@ -185,11 +185,13 @@ struct TreeArgs {
 };
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
 
-// Attention over shared prefixes (prefix.cu). Two lines of work: units of few
-// rows (line 0) and of many.
+// Attention over shared prefixes (prefix.cu, prefix_big.cu, prefix_work.cuh).
+// Two lines of work: units of few rows (line 0) and of many. Costs of a unit
+// besides its blocks, and the least cost of a CTA's range, at least a unit's
+// with one block.
 constexpr int kSmallRows = 16, kBigRows = 256;
-// What a block costs a unit of an entry with so many rows.
-__host__ __device__ constexpr int prefix_weight(int line, int rows) { return line == 0 ? 1 : rows > 128 ? 4 : 3; }
+constexpr int kSmallUnitCost = 1, kBigUnitCost = 12, kSmallRange = 3, kBigRange = 16;
+constexpr int kGroupRun = 1 << 30;  // of an entry's first block: the entry is a group's
 struct PrefixArgs {
   unsigned* fault = nullptr;
   CUtensorMap tmap_k;  // (.., 128, Hkv, pages)
@@ -210,14 +212,18 @@ struct PrefixArgs {
   void* out = nullptr;
   float* lse = nullptr;
   int small_rows = 0;  // entries of more rows go to line 1; INT_MAX: there is none
-  int small_grid = 0, big_grid = 0, small_range = 0, big_range = 0;  // CTAs, and the least cost of a range
-  // Workspace. Positions: the requests in the order of the groups; entries: the
-  // positions' own runs, then the groups'.
-  int4* entry = nullptr;       // (batch, 2): first token in that order, tokens, request, group; first row of q, Lk - Lq, Lk
-  int4* work = nullptr;        // (2 batch, 2): first token, rows, page row, first block; blocks, keys that all rows see, Lk, group
-  long long* start = nullptr;  // (2, 2 batch + 1): running sums of the entries' costs on each line
+  int small_grid = 0, big_grid = 0;
+  // Workspace. Positions: the requests in the order of the groups. Entries: the
+  // positions' own runs and the groups', each on one of the lines.
+  int4* entry = nullptr;       // (batch, 2): first token in that order, tokens, request, group; first row of q, Lk - Lq, Lk, entry
+  int* group = nullptr;        // (batch): a group's entry; entries are numbers on their line, + kGroupRun on line 1, -1 for none
+  int4* work = nullptr;        // (2, 2 batch, 2): first token, rows, page row, first block (| kGroupRun); blocks, keys that all rows see, Lk, group before or -1
+  long long* start = nullptr;  // (2, 2 batch + 1): running sums of the entries' costs
+  int* chunk = nullptr;        // (2 batch + 1): of line 1's entries, 16 rows of one KV head each, of those that are requests'
   int2* token = nullptr;       // (total_q): each token's row of q, and its position
-  int* kept = nullptr;         // tokens in all
+  int* meta = nullptr;         // tokens in all, entries on line 0, on line 1, odd rows
+  int4* cut = nullptr;         // (small_grid): the unit that begins in the CTA's range and goes on after it: entry, tile and head; entry -1: none
+  int* odd = nullptr;          // (total_q * Hq): rows that are not finite, by token in the groups' order and head
   size_t part_rows = 0;        // rows of parts before the CTAs' own
   float2* part_ml = nullptr;   // (part_rows + small_grid * kSmallRows + big_grid * kBigRows)
   float* part_o = nullptr;     // the same, 128 each

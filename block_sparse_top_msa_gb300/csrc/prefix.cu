@@ -12,6 +12,11 @@
 // they end: a long run is split over many CTAs, short ones share one. The first
 // piece of a unit leaves its parts at the rows' own places, the others (a CTA
 // has one at most, its first) at the CTA's.
+//
+// Groups' runs, and those of requests with many rows, are units of 256 rows
+// for prefix_big.cu (line 1); the other requests' are units of 16 rows here
+// (line 0), which come after: a unit that one CTA has whole takes its group's
+// parts in and writes its rows. What is left is joined by the last kernel.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -48,19 +53,41 @@ MSA_DEV T block_upto(T v, T* s_warp, T& all) {
   return inc + (warp > 0 ? before : T(0));
 }
 
-// The work list, by one block: requests in the order of their groups, where
+// Three running sums over a block; every thread has to come.
+struct Sums {
+  long long v[3];
+};
+MSA_DEV Sums block_sums(Sums x, Sums* s_warp, Sums& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) x.v[i] = warp_upto(x.v[i], lane);
+  __syncthreads();
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  Sums w = s_warp[lane];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    w.v[i] = warp_upto(w.v[i], lane);
+    all.v[i] = __shfl_sync(0xffffffffu, w.v[i], 31);
+    const long long before = __shfl_sync(0xffffffffu, w.v[i], warp > 0 ? warp - 1 : 0);
+    if (warp > 0) x.v[i] += before;
+  }
+  return x;
+}
+
+// The work, by one block: the requests in the order of their groups, where
 // their tokens begin in that order, the blocks that each group attends for
-// all, and the running sums of what the entries cost. Entry i < batch is the
-// i-th request's own run, entry batch + g that of group g.
+// all, the two lines' entries and the running sums of what they cost.
 __global__ void __launch_bounds__(kPlanThreads)
     prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ int dyn[];
-  __shared__ long long s_sum[32];
+  __shared__ Sums s_sums[32];
   __shared__ int s_int[32];
   __shared__ int s_kept;
-  int* least = dyn;              // (batch): blocks that a group attends for all
-  int* tokens = dyn + a.batch;   // (batch): a group's tokens
-  int* members = dyn + 2 * a.batch;  // (batch): its requests that have some
+  int* least = dyn;             // (batch): blocks that a group attends for all
+  int* tokens = dyn + a.batch;  // (batch): a group's tokens
+  uint32_t* several = reinterpret_cast<uint32_t*>(dyn + 2 * a.batch);                 // a bit per group: more than one request has some
+  uint16_t* begins = reinterpret_cast<uint16_t*>(several + (a.batch + 31) / 32);  // (batch): cu_groups
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.num_qo_heads / a.num_kv_heads;
   grid_dependency_wait();
@@ -68,8 +95,11 @@ __global__ void __launch_bounds__(kPlanThreads)
   const bool groups = a.group_rows != nullptr;
   for (int g = tid; g < a.batch; g += kPlanThreads) {
     least[g] = groups ? max(0, min(__ldg(a.group_blocks + g), a.max_pages)) : 0;
-    tokens[g] = members[g] = 0;
+    tokens[g] = 0;
+    begins[g] = (uint16_t)(groups ? max(0, min(__ldg(a.cu_groups + g), 65535)) : g);
+    if ((g & 31) == 0) several[g >> 5] = 0u;
   }
+  for (int i = tid; i < a.small_grid; i += kPlanThreads) a.cut[i] = make_int4(-1, 0, 0, 0);
   if (tid == 0) s_kept = 0;
   __syncthreads();
   int before = 0;
@@ -88,7 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         int lo = 0;  // the last group that begins at or before i
         for (int hi = a.batch; hi - lo > 1;) {
           const int mid = (lo + hi) >> 1;
-          if (__ldg(a.cu_groups + mid) <= i) lo = mid; else hi = mid;
+          if (begins[mid] <= i) lo = mid; else hi = mid;
         }
         g = lo;
       }
@@ -101,61 +131,69 @@ __global__ void __launch_bounds__(kPlanThreads)
       // rest is left out.
       if (tau < 0 || lq > a.total_q - tau) lq = 0;
       a.entry[2 * i] = make_int4(tau, lq, b, g);
-      a.entry[2 * i + 1] = make_int4(t0, lk - lq, lk, 0);
+      a.entry[2 * i + 1] = make_int4(t0, lk - lq, lk, -1);
       if (lq > 0) {
         atomicMin(&least[g], max(0, lk - lq) / kBlk);
-        atomicAdd(&tokens[g], lq);
-        atomicAdd(&members[g], 1);
+        if (atomicAdd(&tokens[g], lq) > 0) atomicOr(&several[g >> 5], 1u << (g & 31));
         atomicMax(&s_kept, tau + lq);
       }
     }
   }
   __syncthreads();
+  Sums base{};  // costs of the lines; entries on line 0, on line 1 from bit 16, chunks from bit 32
+  for (int e0 = 0; e0 < 2 * a.batch; e0 += kPlanThreads) {
+    const int e = e0 + tid, g = e - a.batch;
+    int4 x = make_int4(0, 0, 0, 0), y = make_int4(0, 0, 0, 0);
+    int line = -1;
+    if (e < a.batch) {
+      const int4 r = a.entry[2 * e], s = a.entry[2 * e + 1];
+      const bool shares = (several[r.w >> 5] >> (r.w & 31)) & 1u;
+      const int from = shares ? least[r.w] : 0;
+      const int blocks = (int)min((long long)a.max_pages, ((long long)s.z + kBlk - 1) / kBlk);
+      x = make_int4(r.x, r.y * G, r.z, from);
+      y = make_int4(max(0, blocks - from), a.causal ? s.y : s.z, s.z, from > 0 ? r.w : -1);
+      if (r.y > 0) line = x.y > a.small_rows;
+    } else if (e < 2 * a.batch && groups && ((several[g >> 5] >> (g & 31)) & 1u) && least[g] > 0) {
+      const int first = min((int)begins[g], a.batch - 1), lead = __ldg(a.group_rows + first);
+      x = make_int4(a.entry[2 * first].x, tokens[g] * G, max(0, min(lead, a.batch - 1)), kGroupRun);
+      y = make_int4(least[g], least[g] * kBlk, least[g] * kBlk, -1);
+      line = 1;
+    }
+    Sums mine{};
+    if (line >= 0) {
+      const int tile = tile_rows_of(line);
+      mine.v[line] = (long long)((x.y + tile - 1) / tile) * a.num_kv_heads * (unit_cost(line) + (long long)y.x * block_cost(line, x.y));
+      mine.v[2] = 1ll << (16 * line);
+      if (line == 1 && e < a.batch) mine.v[2] += (long long)((x.y + 15) / 16) * a.num_kv_heads << 32;
+    }
+    Sums all;
+    const Sums upto = block_sums(mine, s_sums, all);
+    const long long counts = base.v[2] + upto.v[2] - mine.v[2];
+    const int at = line == 1 ? (int)(counts >> 16) & 0xffff : (int)counts & 0xffff;
+    if (line >= 0) {
+      a.start[line * (2 * a.batch + 1) + at] = base.v[line] + upto.v[line] - mine.v[line];
+      a.work[line * 4 * a.batch + 2 * at] = x;
+      a.work[line * 4 * a.batch + 2 * at + 1] = y;
+      if (line == 1) a.chunk[at] = (int)(counts >> 32);
+    }
+    if (e < a.batch) a.entry[2 * e + 1].w = line < 0 ? -1 : line == 1 ? at | kGroupRun : at;
+    else if (e < 2 * a.batch) a.group[g] = line < 0 ? -1 : at;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) base.v[i] += all.v[i];
+  }
+  if (tid < 2) {
+    const int n = (int)(base.v[2] >> (16 * tid)) & 0xffff;
+    a.start[tid * (2 * a.batch + 1) + n] = base.v[tid];
+    a.meta[1 + tid] = n;
+    if (tid == 1) a.chunk[n] = (int)(base.v[2] >> 32);
+    if (tid == 0) a.meta[0] = s_kept, a.meta[3] = 0;
+  }
   // Each token's place in the groups' order, a warp for each request.
   for (int i = warp; i < a.batch; i += kPlanThreads / 32) {
     const int4 x = a.entry[2 * i];
     const int t0 = a.entry[2 * i + 1].x;
     for (int j = lane; j < x.y; j += 32) a.token[x.x + j] = make_int2(t0 + j, i);
   }
-  __syncthreads();
-  long long cost_before[2] = {0, 0};
-  for (int e0 = 0; e0 < 2 * a.batch; e0 += kPlanThreads) {
-    const int e = e0 + tid;
-    long long cost[2] = {0, 0};
-    int4 x = make_int4(0, 0, 0, 0), y = make_int4(0, 0, 0, 0);  // tau, rows, page row, first block; blocks, first key that may be hidden, Lk, 0
-    if (e < a.batch) {
-      const int4 r = a.entry[2 * e], s = a.entry[2 * e + 1];
-      const int from = members[r.w] > 1 ? least[r.w] : 0;
-      const int blocks = (int)min((long long)a.max_pages, ((long long)s.z + kBlk - 1) / kBlk);
-      x = make_int4(r.x, r.y * G, r.z, from);
-      y = make_int4(r.y > 0 ? max(0, blocks - from) : 0, a.causal ? s.y : s.z, s.z, r.w);
-    } else if (e < 2 * a.batch) {
-      const int g = e - a.batch;
-      if (groups && members[g] > 1 && least[g] > 0) {
-        const int first = max(0, min(__ldg(a.cu_groups + g), a.batch - 1)), lead = __ldg(a.group_rows + first);
-        x = make_int4(a.entry[2 * first].x, tokens[g] * G, max(0, min(lead, a.batch - 1)), 0);
-        y = make_int4(least[g], least[g] * kBlk, least[g] * kBlk, g);
-      }
-    }
-    if (e < 2 * a.batch) {
-      const int line = x.y > a.small_rows;
-      const int tile = line ? kBigRows : kSmallRows;
-      cost[line] = (long long)((x.y + tile - 1) / tile) * a.num_kv_heads * y.x * prefix_weight(line, x.y);
-    }
-#pragma unroll
-    for (int l = 0; l < 2; ++l) {
-      long long all;
-      const long long upto = cost_before[l] + block_upto<long long>(cost[l], s_sum, all);
-      if (e < 2 * a.batch) a.start[l * (2 * a.batch + 1) + e] = upto - cost[l];
-      cost_before[l] += all;
-    }
-    if (e < 2 * a.batch) {
-      a.work[2 * e] = x;
-      a.work[2 * e + 1] = y;
-    }
-  }
-  if (tid < 2) a.start[tid * (2 * a.batch + 1) + 2 * a.batch] = cost_before[tid];
-  if (tid == 0) *a.kept = s_kept;
 }
 
 // ------------------------------------------------------- few rows: 16 a tile
@@ -163,8 +201,9 @@ __global__ void __launch_bounds__(kPlanThreads)
 // (the rows are too few for a tile of 128), its own softmax (m, l) and its own
 // O, so a warp waits for no other until the piece ends, where the eight are
 // joined. Bound by memory: a block of 64 KB takes an SM's share of the
-// bandwidth 3000 clocks. K and V come by TMA through a ring of blocks, one
-// warp ahead; the join borrows the next free slots of the ring.
+// bandwidth 3000 clocks. One warp hands out the pieces with their Q, another
+// brings K and V by TMA through a ring of blocks; the join borrows the next
+// free slots of that ring.
 constexpr int kWarps = 8;
 template <int KV>  // 0 bf16, 1 f16, 2 E4M3 with bf16 q
 struct Small {
@@ -173,17 +212,19 @@ struct Small {
   static constexpr int kStage = 2 * kTile;
   static constexpr int kStages = KV == 2 ? 6 : 3;
   static constexpr int kJoin = kWarps * 16 * 128 * 4 / kStage;  // slots that eight O fill
-  static constexpr int kThreads = (kWarps + 1) * 32;
+  static constexpr int kThreads = (kWarps + 2) * 32;
 };
+constexpr int kPieces = 4;  // of the ring that hands them out
 constexpr int kQStride = 272;  // bytes of a row of Q in shared memory
 template <int KV>
 struct __align__(1024) SmallSmem {
   uint8_t stage[Small<KV>::kStages][Small<KV>::kStage];
-  uint8_t q[2][16 * kQStride];
-  Piece piece[2];
+  uint8_t q[kPieces][16 * kQStride];
+  Piece piece[kPieces];
+  Before before[kPieces];
   float2 ml[2][kWarps][16];
   int page_ok[Small<KV>::kStages];
-  uint64_t piece_full[2], piece_empty[2], full[Small<KV>::kStages], empty[Small<KV>::kStages], join;
+  uint64_t piece_full[kPieces], piece_empty[kPieces], full[Small<KV>::kStages], empty[Small<KV>::kStages], join;
   int abort;
 };
 static_assert(sizeof(SmallSmem<0>) <= 226 * 1024 && sizeof(SmallSmem<2>) <= 226 * 1024, "too much shared memory");
@@ -236,9 +277,9 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.num_qo_heads / a.num_kv_heads;
   if (tid == 0) {
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kPieces; ++s) {
       mbar_init(&sm.piece_full[s], 33);
-      mbar_init(&sm.piece_empty[s], kWarps);
+      mbar_init(&sm.piece_empty[s], kWarps + 1);
     }
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sm.full[s], 1);
@@ -251,17 +292,67 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
   __syncthreads();
   grid_dependency_wait();
   grid_dependents_launch();
-  const Ranges ranges = ranges_of(a, 0);
 
   if (warp == kWarps) {
-    // ------------------------------------------------------------- K, V and Q
+    // ------------------------------------------------------------ pieces and Q
+    const Ranges ranges = ranges_of(a, 0), big = ranges_of(a, 1);
+    Walk walk(a, 0, ranges, blockIdx.x);
+    Piece p{};
+    int e = -1, row0 = -1;
+    uint32_t from[8];  // a lane's eight of the tile's sixteen-byte groups: token of the row, times heads
+    int4 cut = make_int4(-1, 0, 0, 0);
+    for (int np = 0;; ++np) {
+      const bool more = walk.next(p);
+      const int slot = np % kPieces;
+      bool ok = np < kPieces ||
+                mbar_wait_sleep(&sm.piece_empty[slot], ((np / kPieces) - 1) & 1, fault, kFaultWaitSoftmax, abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      Before f{};
+      if (more) {
+        // Q's rows of the tile, zeros behind them. A lane has 16 bytes of each
+        // second row.
+        const int c = lane & 15;
+        if (p.e != e || p.row0 != row0) {
+          e = p.e, row0 = p.row0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int r = 2 * i + (lane >> 4), row = row0 + r;
+            from[i] = r < p.rows ? (uint32_t)__ldcg(&a.token[p.tau + row / G].x) * a.num_qo_heads + row % G : 0u;
+          }
+        }
+        const uint8_t* q = static_cast<const uint8_t*>(a.q) + c * 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = 2 * i + (lane >> 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(sm.q[slot] + r * kQStride + c * 16)),
+                       "l"(q + ((size_t)from[i] + (r < p.rows ? p.h * G : 0)) * 256), "r"(r < p.rows ? 16 : 0)
+                       : "memory");
+        }
+        if (p.whole) f = before_of(a, big, p.group, p.tau, p.row0, p.rows, p.h);
+        else if (p.place >= 0) cut = make_int4(p.e, p.tile_head, 0, 0);
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.piece_full[slot])) : "memory");
+      if (lane == 0) {
+        sm.piece[slot] = p;
+        sm.before[slot] = f;
+        mbar_arrive(&sm.piece_full[slot]);
+      }
+      __syncwarp();
+      if (!more) break;
+    }
+    if (lane == 0) a.cut[blockIdx.x] = cut;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    return;
+  }
+  if (warp == kWarps + 1) {
+    // ---------------------------------------------------------------- K and V
     if (lane == 0) {
       tma_prefetch_desc(&a.tmap_k);
       tma_prefetch_desc(&a.tmap_v);
     }
-    Walk walk(a, 0, ranges, blockIdx.x);
     bool ok = true;
-    int stage = 0, np = 0;
+    int stage = 0;
     uint32_t turn = 0;  // of the ring: how often it has gone round
     auto acquire = [&]() -> bool {  // the next slot, free
       bool free = turn == 0 || mbar_wait_sleep(&sm.empty[stage], (turn - 1) & 1, fault, kFaultWaitSoftmax, abort);
@@ -270,37 +361,15 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
     auto advance = [&]() {
       if (++stage == C::kStages) stage = 0, ++turn;
     };
-    Piece p{};
-    while (ok) {
-      const bool more = walk.next(p);
-      const int slot = np & 1;
-      ok = np < 2 || mbar_wait_sleep(&sm.piece_empty[slot], ((np >> 1) - 1) & 1, fault, kFaultWaitSoftmax, abort);
+    for (int np = 0; ok; ++np) {
+      const int slot = np % kPieces;
+      ok = mbar_wait_sleep(&sm.piece_full[slot], (np / kPieces) & 1, fault, kFaultWaitOther, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      ++np;
-      if (more) {
-        // Q's rows of the tile, zeros behind them.
-        const uint8_t* q = static_cast<const uint8_t*>(a.q);
-        for (int i = lane; i < 256; i += 32) {
-          const int r = i >> 4, c = i & 15, row = p.row0 + r;
-          const bool live = r < p.rows;
-          size_t from = 0;
-          if (live) {
-            const int token = __ldcg(&a.token[p.tau + row / G].x);
-            from = ((size_t)token * a.num_qo_heads + (size_t)p.h * G + row % G) * 256 + c * 16;
-          }
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(sm.q[slot] + r * kQStride + c * 16)),
-                       "l"(q + from), "r"(live ? 16 : 0)
-                       : "memory");
-        }
-      }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.piece_full[slot])) : "memory");
-      if (lane == 0) {
-        sm.piece[slot] = p;
-        mbar_arrive(&sm.piece_full[slot]);
-      }
+      const Piece p = sm.piece[slot];
       __syncwarp();
-      if (!more) break;
+      if (lane == 0) mbar_arrive(&sm.piece_empty[slot]);
+      if (p.n < 0) break;
       const int blocks = (p.keys + kBlk - 1) / kBlk;
       const int32_t* pages = a.page_table + (size_t)p.b * a.max_pages + p.j0;
       int page32 = -1;
@@ -340,7 +409,6 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
       }
     }
     // Copies in flight land before the CTA's shared memory is given back.
-    asm volatile("cp.async.wait_all;" ::: "memory");
     if (!ok) {
       for (int s = 0; s < C::kStages; ++s) {
         // The slot's last phase: the one of this turn for slots before `stage`.
@@ -360,13 +428,16 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
     if (++stage == C::kStages) stage = 0, ++turn;
   };
   while (true) {
-    const int slot = np & 1;
-    ok = mbar_wait_sleep(&sm.piece_full[slot], (np >> 1) & 1, fault, kFaultWaitOther, abort);
+    const int slot = np % kPieces, ms = np & 1;
+    ok = mbar_wait_sleep(&sm.piece_full[slot], (np / kPieces) & 1, fault, kFaultWaitOther, abort);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     ++np;
     const Piece p = sm.piece[slot];
-    if (p.n == 0) break;
+    if (p.n < 0) break;
+    // Of the row that this thread writes at the end.
+    const int out_row = tid >> 4, er = p.row0 + out_row;
+    const int token = out_row < p.rows ? __ldcg(&a.token[p.tau + er / G].x) : 0;
     // Q as the products want it; with E4M3 keys as f16, each row scaled by a
     // power of two that puts its largest value just below f16's largest, and
     // with the dims in the order in which a thread reads K: its 32 of them.
@@ -530,7 +601,7 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
       if (m[r] == -INFINITY && !(l[r] == 0.f)) m[r] = 0.f;  // nothing but NaN
-      if (t == 0) sm.ml[slot][warp][g + 8 * r] = make_float2(m[r], l[r]);
+      if (t == 0) sm.ml[ms][warp][g + 8 * r] = make_float2(m[r], l[r]);
     }
     // Warp w's O: row r, column c at r * 128 + (c ^ 8 (r & 3)) of its 8 KB.
     auto o_of = [&](int w) -> float* {
@@ -558,37 +629,50 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
     ++joins;
-    const int row = tid >> 4, col = (tid & 15) * 8;
-    float M = -INFINITY, L = 0.f, sum[8] = {};
+    const int col = (tid & 15) * 8;
+    float M = -INFINITY;
+    Joined own;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[slot][w][row].x);
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm.ml[ms][w][out_row].x);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float2 ml = sm.ml[slot][w][row];
+      const float2 ml = sm.ml[ms][w][out_row];
       if (ml.x == -INFINITY) continue;
       const float f = ex2(ml.x - M);
-      L += f * ml.y;
-      const float* from = o_of(w) + row * 128 + (col ^ ((row & 3) << 3));
+      own.l += f * ml.y;
+      const float* from = o_of(w) + out_row * 128 + (col ^ ((out_row & 3) << 3));
       const float4 x = *reinterpret_cast<const float4*>(from), y = *reinterpret_cast<const float4*>(from + 4);
       const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-      for (int c = 0; c < 8; ++c) sum[c] = fmaf(f, v[c], sum[c]);
+      for (int c = 0; c < 8; ++c) own.o[c] = fmaf(f, v[c], own.o[c]);
     }
-    if (row < p.rows) {
-      const int r = p.row0 + row;
-      const size_t at = p.place >= 0 ? (size_t)(p.place + r / G) * a.num_qo_heads + (size_t)p.h * G + r % G
-                                     : a.part_rows + (size_t)blockIdx.x * kSmallRows + row;
-      float4* to = reinterpret_cast<float4*>(a.part_o + at * kHeadDim + col);
-      to[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
-      to[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
-      if (col == 0) a.part_ml[at] = make_float2(M, L);
-    }
+    own.m = M;
+    const Before before = sm.before[slot];
     fence_async_smem();  // the slots are TMA's again
     __syncwarp();
     if (lane == 0) {
       for (int j = 0, s = js; j < C::kJoin; ++j, s = s + 1 == C::kStages ? 0 : s + 1) mbar_arrive(&sm.empty[s]);
       mbar_arrive(&sm.piece_empty[slot]);
     }
+    // The row: written where the unit is whole, else its parts.
+    const bool live = out_row < p.rows;
+    const size_t hq = (size_t)p.h * G + er % G, own_row = (size_t)(p.tau + er / G) * a.num_qo_heads + hq;
+    bool odd = false;
+    if (live && p.whole) {
+      Joined all;
+      all.add_before(a, before, out_row, own_row, col);
+      all.add(make_float2(own.m, own.l), own.o);
+      odd = a.causal && p.many && !all.finite();
+      all.write(a, (size_t)token * a.num_qo_heads + hq, col);
+    } else if (live) {
+      const size_t at = p.place >= 0 ? own_row : cta_parts(a, 0) + (size_t)blockIdx.x * kSmallRows + out_row;
+      float4* to = reinterpret_cast<float4*>(a.part_o + at * kHeadDim + col);
+      to[0] = make_float4(own.o[0], own.o[1], own.o[2], own.o[3]);
+      to[1] = make_float4(own.o[4], own.o[5], own.o[6], own.o[7]);
+      if (col == 0) a.part_ml[at] = make_float2(own.m, own.l);
+    }
+    const unsigned rows_odd = __ballot_sync(0xffffffffu, odd);
+    if ((lane & 15) == 0 && ((rows_odd >> lane) & 0xffffu)) a.odd[atomicAdd(a.meta + 3, 1)] = (int)own_row;
   }
 }
 
@@ -647,67 +731,96 @@ __device__ __noinline__ void own_run(const PrefixArgs& a, size_t orow, int b, in
   if (m == -INFINITY && !(l == 0.f)) m = 0.f;
 }
 
-// A warp for each row; a lane has four columns. The parts of the group's run,
-// then those of the own one, each in the order of its pieces.
-constexpr int kJoinWarps = 8;
-__global__ void __launch_bounds__(kJoinWarps * 32)
+// A row that is not finite: its group's parts, and its own run anew.
+__device__ __noinline__ void odd_row(const PrefixArgs& a, const Ranges& big, int own_row, int lane) {
+  const int G = a.num_qo_heads / a.num_kv_heads, tau = own_row / a.num_qo_heads, hq = own_row - tau * a.num_qo_heads, h = hq / G;
+  const int2 token = __ldcg(a.token + tau);
+  const int code = __ldcg(&a.entry[2 * token.y + 1].w);
+  const int4* w = work_of(a, code >= kGroupRun) + 2 * (code & ~kGroupRun);
+  const int4 x = __ldcg(w), y = __ldcg(w + 1);
+  const int row = (tau - x.x) * G + hq - h * G, col = (lane & 15) * 8;
+  const size_t orow = (size_t)token.x * a.num_qo_heads + hq;
+  const Before f = before_of(a, big, y.w, x.x, row, 1, h);
+  Joined all;
+  all.add_before(a, f, 0, own_row, col);
+  float m, l, o[4];
+  const int sees = (int)min((long long)y.z, (long long)y.y + (tau - x.x) + 1);
+  own_run(a, orow, x.z, h, x.w & ~kGroupRun, sees, lane, m, l, o);
+  float v[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) v[c] = __shfl_sync(0xffffffffu, o[c & 3], 2 * (lane & 15) + (c >> 2));
+  all.add(make_float2(m, l), v);
+  if (lane < 16) all.write(a, orow, col);
+}
+
+// Joins what is left: 16 rows at a time of the requests on line 1, of the units
+// of line 0 that ranges cut; 16 threads a row, of eight columns each. First the
+// parts of the group's run, then those of the own one, in the order of the
+// pieces.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads)
     prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
-  const int lane = threadIdx.x & 31, G = a.num_qo_heads / a.num_kv_heads;
+  __shared__ Piece s_piece;  // the rows' own unit; rows 16, from row0 on
+  __shared__ Before s_before;
+  __shared__ Parts s_parts;
+  __shared__ int s_line;
+  __shared__ uint32_t s_odd;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.num_qo_heads / a.num_kv_heads;
   grid_dependency_wait();
   grid_dependents_launch();
-  const long long rows = (long long)__ldcg(a.kept) * a.num_qo_heads;
   const Ranges lines[2] = {ranges_of(a, 0), ranges_of(a, 1)};
-  for (long long i = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5); i < rows; i += (long long)gridDim.x * kJoinWarps) {
-    const int tau = (int)(i / a.num_qo_heads), hq = (int)(i - (long long)tau * a.num_qo_heads), h = hq / G;
-    const int2 token = __ldcg(a.token + tau);
-    const size_t orow = (size_t)token.x * a.num_qo_heads + hq;
-    const int group = __ldcg(&a.work[2 * token.y + 1].w);
-    float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    auto add = [&](float m, float l, float4 o) {
-      if (m == -INFINITY) return;  // a part without a visible key may hold anything
-      const float top = fmaxf(M, m), f = M == -INFINITY ? 0.f : ex2(M - top), p = ex2(m - top);
-      M = top;
-      L = fmaf(L, f, p * l);
-      acc[0] = fmaf(p, o.x, acc[0] * f), acc[1] = fmaf(p, o.y, acc[1] * f);
-      acc[2] = fmaf(p, o.z, acc[2] * f), acc[3] = fmaf(p, o.w, acc[3] * f);
-    };
-    auto add_at = [&](size_t at) {
-      const float2 ml = __ldcg(a.part_ml + at);
-      add(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.part_o + at * kHeadDim) + lane));
-    };
-    auto run = [&](int e, bool prefix) {
-      const int4 x = __ldcg(a.work + 2 * e);
-      const int blocks = __ldcg(&a.work[2 * e + 1].x);
-      if (blocks == 0) return;
-      const int line = x.y > a.small_rows, r = (tau - x.x) * G + hq % G;
-      const int tile_rows = line ? kBigRows : kSmallRows, tile = r / tile_rows;
-      const int w = prefix_weight(line, x.y);
-      const long long len = (long long)blocks * w;
-      const long long at = __ldcg(a.start + line * (2 * a.batch + 1) + e) + ((long long)tile * a.num_kv_heads + h) * len;
-      const int c0 = lines[line].holder(at), c1 = lines[line].holder(at + len - w);
-      add_at((size_t)((prefix ? a.total_q : 0) + tau) * a.num_qo_heads + hq);
-      const size_t slots = a.part_rows + (line ? (size_t)a.small_grid * kSmallRows : 0);
-      for (int c = c0 + 1; c <= c1; ++c) add_at(slots + (size_t)c * tile_rows + (r - tile * tile_rows));
-    };
-    if (a.group_rows != nullptr) run(a.batch + group, true);
-    const float gm = M, gl = L, g0 = acc[0], g1 = acc[1], g2 = acc[2], g3 = acc[3];
-    run(token.y, false);
-    const float odd = acc[0] * 0.f + acc[1] * 0.f + acc[2] * 0.f + acc[3] * 0.f;
-    const int4 x = __ldcg(a.work + 2 * token.y);
-    if (a.causal && x.y > G && __any_sync(0xffffffffu, !(odd == 0.f && L < INFINITY))) {
-      const int4 y = __ldcg(a.work + 2 * token.y + 1);
-      float m, l, o[4];
-      const int sees = (int)min((long long)y.z, (long long)y.y + (tau - x.x) + 1);
-      own_run(a, orow, x.z, h, x.w, sees, lane, m, l, o);
-      M = gm, L = gl, acc[0] = g0, acc[1] = g1, acc[2] = g2, acc[3] = g3;
-      add(m, l, make_float4(o[0], o[1], o[2], o[3]));
+  const int odd = __ldcg(a.meta + 3);
+  for (int i = blockIdx.x * (kJoinThreads / 32) + warp; i < odd; i += gridDim.x * (kJoinThreads / 32))
+    odd_row(a, lines[1], __ldcg(a.odd + i), lane);
+  const int entries = __ldcg(a.meta + 2), chunks = __ldcg(a.chunk + entries);
+  for (int i = blockIdx.x; i < a.small_grid + chunks; i += gridDim.x) {
+    if (warp == 0) {
+      int line = 0, e = -1, tile_head = 0, row0 = 0;
+      if (i < a.small_grid) {
+        const int4 cut = __ldcg(a.cut + i);
+        e = cut.x, tile_head = cut.y;
+        row0 = tile_head / a.num_kv_heads * kSmallRows;
+      } else {
+        line = 1;
+        e = last_upto(a.chunk, entries, i - a.small_grid);
+        const int c = i - a.small_grid - __ldcg(a.chunk + e), r = c / a.num_kv_heads;
+        row0 = r * 16;
+        tile_head = row0 / kBigRows * a.num_kv_heads + c - r * a.num_kv_heads;
+      }
+      Piece p{};
+      p.n = -1;
+      if (e >= 0) {
+        const int4* w = work_of(a, line) + 2 * e;
+        const int4 x = __ldcg(w), y = __ldcg(w + 1);
+        p.n = y.x;
+        p.h = tile_head % a.num_kv_heads;
+        p.row0 = row0, p.rows = min(16, x.y - row0), p.tau = x.x, p.many = x.y > G;
+        const Parts parts = parts_of(a, line, lines[line], e, x.y, y.x, tile_head);
+        const Before f = before_of(a, lines[1], y.w, x.x, row0, p.rows, p.h);
+        if (lane == 0) s_parts = parts, s_before = f;
+      }
+      if (lane == 0) s_piece = p, s_line = line, s_odd = 0u;
     }
-    const bool has = L != 0.f;
-    const float inv = has ? 1.f / L : 0.f;
-    auto pack = [&](float x, float y) { return a.f16 ? pack_f16x2(x, y) : pack_bf16x2(x, y); };
-    reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + orow * kHeadDim)[lane] =
-        make_uint2(pack(acc[0] * inv, acc[1] * inv), pack(acc[2] * inv, acc[3] * inv));
-    if (lane == 0 && a.lse != nullptr) a.lse[orow] = has ? (M + log2f(L)) * 0.69314718055994531f : -INFINITY;
+    __syncthreads();
+    const Piece p = s_piece;
+    const int row = tid >> 4, er = p.row0 + row, col = (tid & 15) * 8;
+    const bool live = p.n >= 0 && row < p.rows;
+    const size_t hq = (size_t)p.h * G + er % G, own_row = (size_t)(p.tau + er / G) * a.num_qo_heads + hq;
+    if (live) {
+      const int token = __ldcg(&a.token[p.tau + er / G].x), line = s_line, tile_rows = tile_rows_of(line);
+      Joined all;
+      all.add_before(a, s_before, row, own_row, col);
+      all.add_parts(a, own_row, cta_parts(a, line), tile_rows, er % tile_rows, s_parts, col);
+      if (a.causal && p.many && !all.finite()) atomicOr(&s_odd, 1u << row);
+      all.write(a, (size_t)token * a.num_qo_heads + hq, col);
+    }
+    __syncthreads();
+    for (uint32_t left = s_odd; left != 0u; left &= left - 1u) {
+      const int r = __ffs(left) - 1, o = p.row0 + r;
+      if (r % (kJoinThreads / 32) == warp)
+        odd_row(a, lines[1], (int)((p.tau + o / G) * a.num_qo_heads + p.h * G + o % G), lane);
+    }
+    __syncthreads();
   }
 }
 
@@ -722,7 +835,7 @@ cudaError_t launch_small(const PrefixArgs& a, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_prefix(const PrefixArgs& a, cudaStream_t s) {
-  const int smem = 3 * a.batch * (int)sizeof(int);
+  const int smem = (2 * a.batch + (a.batch + 31) / 32) * 4 + (a.batch * 2 + 3) / 4 * 4;
   cudaError_t e = set_smem_limit((const void*)prefix_plan_kernel, smem);
   if (e != cudaSuccess) return e;
   e = launch_dependent(prefix_plan_kernel, dim3(1), kPlanThreads, smem, s, a);
@@ -733,9 +846,11 @@ cudaError_t launch_prefix(const PrefixArgs& a, cudaStream_t s) {
   }
   e = a.e4m3 ? launch_small<2>(a, s) : a.f16 ? launch_small<1>(a, s) : launch_small<0>(a, s);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)a.total_q * a.num_qo_heads;
-  const long long blocks = (rows + kJoinWarps - 1) / kJoinWarps;
-  return launch_dependent(prefix_join_kernel, dim3((unsigned)(blocks < 1216 ? blocks : 1216)), kJoinWarps * 32, 0, s, a);
+  // Cut units, and as many chunks as there can be, up to eight blocks an SM.
+  const long long chunks = ((long long)a.total_q * a.num_qo_heads + 15) / 16 + (long long)a.batch * a.num_kv_heads;
+  const long long items = a.small_grid + (a.small_rows < INT_MAX ? chunks : 0);
+  return launch_dependent(prefix_join_kernel, dim3((unsigned)(items < 8 * a.small_grid ? items : 8 * a.small_grid)),
+                          kJoinThreads, 0, s, a);
 }
 
 }  // namespace msa

@@ -170,11 +170,11 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
   auto read_seg = [&](int n, Piece& s) -> bool {
     const int slot = n % kSegRing;
     if (!mbar_wait_sleep(&sm.seg_full[slot], (n / kSegRing) & 1, fault, kFaultWaitOther, abort)) {
-      s.n = 0;
+      s.n = -1;
       return false;
     }
     s = sm.piece[slot];
-    return s.n > 0;
+    return s.n >= 0;
   };
   auto release_seg = [&](int n) { mbar_arrive(&sm.seg_empty[n % kSegRing]); };
   auto blocks_of = [](const Piece& s) { return (s.keys + kBlk - 1) / kBlk; };
@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     auto place_of = [&](const Piece& s, int r) -> size_t {
       const int er = s.row0 + r;
       return s.place >= 0 ? (size_t)(s.place + er / G) * a.num_qo_heads + (size_t)s.h * G + er % G
-                          : a.part_rows + (size_t)a.small_grid * kSmallRows + (size_t)blockIdx.x * kBigRows + r;
+                          : cta_parts(a, 1) + (size_t)blockIdx.x * kBigRows + r;
     };
 
     // The next piece with blocks; what rows of pieces without any get is here

@@ -1,13 +1,30 @@
-// The work list of the attention over shared prefixes, as its kernels walk it:
-// lines of units' blocks cut into ranges.
+// The work of the attention over shared prefixes, as its kernels walk it: two
+// lines of units' blocks, each cut into ranges, one per CTA.
 #pragma once
 
 #include "common.cuh"
 #include "internal.h"
+#include "softmax.cuh"
 
 namespace msa {
 
-// The partition of a line's [0, total) into the CTAs' ranges.
+// Costs: a block, and what a unit takes besides its blocks (its Q, its
+// epilogue, the change of units). Line 0 counts in halves of a block of 16
+// rows, line 1 in quarters of a block of two tiles of 128.
+MSA_DEV int block_cost(int line, int rows) { return line == 0 ? 2 : rows > 128 ? 4 : 3; }
+MSA_DEV int unit_cost(int line) { return line == 0 ? kSmallUnitCost : kBigUnitCost; }
+MSA_DEV int tile_rows_of(int line) { return line == 0 ? kSmallRows : kBigRows; }
+// Where block j of a unit lies on the line, from the unit's beginning: what the
+// unit takes besides counts with its first block.
+MSA_DEV int block_at(int line, int cost, int j) { return j == 0 ? 0 : unit_cost(line) + j * cost; }
+// The first block that lies at or after `in`.
+MSA_DEV int block_from(int line, int cost, int in) {
+  return in <= 0 ? 0 : max(1, (in - unit_cost(line) + cost - 1) / cost);
+}
+
+// The partition of a line's [0, total) into the CTAs' ranges. A range is never
+// shorter than a unit's first block, so each CTA between those of a unit's first
+// and last block holds one of its blocks.
 struct Ranges {
   long long total;
   int n;
@@ -15,70 +32,215 @@ struct Ranges {
   // The range that position p < total is in: the last i with start(i) <= p.
   MSA_DEV int holder(long long p) const { return (int)((p * n + n - 1) / total); }
 };
+MSA_DEV const long long* starts_of(const PrefixArgs& a, int line) { return a.start + line * (2 * a.batch + 1); }
+MSA_DEV const int4* work_of(const PrefixArgs& a, int line) { return a.work + line * 4 * a.batch; }
 MSA_DEV Ranges ranges_of(const PrefixArgs& a, int line) {
-  const long long total = __ldcg(a.start + line * (2 * a.batch + 1) + 2 * a.batch);
-  const long long most = total / (line ? a.big_range : a.small_range);
+  const long long total = __ldcg(starts_of(a, line) + __ldcg(a.meta + 1 + line));
+  const long long most = total / (line ? kBigRange : kSmallRange);
   const int grid = line ? a.big_grid : a.small_grid;
   return {total, (int)(most < 1 ? 1 : most < grid ? most : grid)};
 }
+// The last of n ascending numbers, the first of them at most `at`, that is at
+// most `at`; by a whole warp.
+template <class T>
+MSA_DEV int last_upto(const T* v, int n, T at) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;  // in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+    const unsigned under = __ballot_sync(0xffffffffu, i < hi && __ldcg(v + (i < hi ? i : lo)) <= at);
+    const int k = 31 - __clz(under);  // lane 0 is under
+    hi = min(hi, lo + (k + 1) * step);
+    lo += k * step;
+  }
+  return lo;
+}
 
-// A piece of a unit: blocks [j0, j0 + n) of one entry's tile with one KV head.
+// A piece of a unit: some blocks of one entry's tile with one KV head.
 struct Piece {
-  int n;          // blocks; 0: no more
-  int b, h, j0;   // page row, KV head, first block
-  int row0, rows; // rows of the entry
-  int tau;        // the entry's first token
-  int hidden, lk; // row r sees keys below min(lk, hidden + r / G + 1)
-  int place;      // of row 0's parts: its own, or (below 0) the CTA's
-  int keys;       // keys from j0 on that some row sees
+  int n;           // blocks; -1: no more
+  int whole;       // all of the unit's
+  int b, h, j0;    // page row, KV head, first block
+  int row0, rows;  // rows of the entry
+  int tau;         // the entry's first token
+  int hidden, lk;  // row r sees keys below min(lk, hidden + r / G + 1)
+  int place;       // of row 0's parts: its own, or (below 0) the CTA's
+  int keys;        // keys from j0 on that some row sees
+  int e, tile_head;  // the unit: entry, tile * heads + head
+  int group;       // whose run comes before this entry's own; -1: none
+  int many;        // the entry has rows of more than one token
 };
 
-// Walks a CTA's range, piece by piece.
+// Walks a CTA's range, piece by piece; by a whole warp, whose lanes agree. The
+// next entry is read while this one's units are handed out.
 struct Walk {
   const PrefixArgs& a;
-  int line;
-  long long at, end;
-  int e;
-  MSA_DEV Walk(const PrefixArgs& args, int l, const Ranges& r, int cta) : a(args), line(l), at(0), end(0), e(0) {
+  int line, list;
+  long long at, end, unit_at;
+  int e, tile, h, len, cost, tiles;
+  int4 x, y, nx, ny;
+  MSA_DEV void ahead() {
+    const int4* w = work_of(a, line) + 2 * min(e + 1, list - 1);
+    nx = __ldcg(w), ny = __ldcg(w + 1);
+  }
+  MSA_DEV void open() {
+    cost = block_cost(line, x.y);
+    len = unit_cost(line) + y.x * cost;
+    tiles = (x.y + tile_rows_of(line) - 1) / tile_rows_of(line);
+  }
+  MSA_DEV Walk(const PrefixArgs& args, int l, const Ranges& r, int cta)
+      : a(args), line(l), list(__ldcg(args.meta + 1 + l)), at(0), end(0) {
     if (r.total <= 0 || cta >= r.n) return;
     at = r.start(cta), end = r.start(cta + 1);
-    const long long* start = a.start + line * (2 * a.batch + 1);
-    int lo = 0;  // the last entry that begins at or before `at`
-    for (int hi = 2 * a.batch; hi - lo > 1;) {
-      const int mid = (lo + hi) >> 1;
-      if (__ldcg(start + mid) <= at) lo = mid; else hi = mid;
-    }
-    e = lo;
+    const long long* start = starts_of(a, line);
+    e = last_upto(start, list, at);
+    const int4* w = work_of(a, line) + 2 * e;
+    x = __ldcg(w), y = __ldcg(w + 1);
+    open();
+    ahead();
+    const long long first = __ldcg(start + e);
+    const int unit = (int)((at - first) / len);
+    unit_at = first + (long long)unit * len;
+    tile = unit / a.num_kv_heads;
+    h = unit - tile * a.num_kv_heads;
   }
   MSA_DEV bool next(Piece& p) {
-    p.n = 0;
-    while (at < end && p.n == 0) step(p);
-    return p.n > 0;
+    p.n = -1;
+    while (at < end && p.n < 0) step(p);
+    return p.n >= 0;
   }
-  // The piece at `at`, which may hold no block's first position.
   MSA_DEV void step(Piece& p) {
-    const long long* start = a.start + line * (2 * a.batch + 1);
-    while (__ldcg(start + e + 1) <= at) ++e;
-    const int4 x = __ldcg(a.work + 2 * e), y = __ldcg(a.work + 2 * e + 1);
-    const int G = a.num_qo_heads / a.num_kv_heads, tile_rows = line ? kBigRows : kSmallRows;
-    const int w = prefix_weight(line, x.y);
-    const long long len = (long long)y.x * w, rel = at - __ldcg(start + e);
-    const long long unit = rel / len;
-    const int in = (int)(rel - unit * len);
-    const long long unit_end = at - in + len, stop = unit_end < end ? unit_end : end;
-    // Block j belongs to the range that its first position is in.
-    const int j0 = (in + w - 1) / w, j1 = (int)((stop - (at - in) + w - 1) / w);
-    const int tile = (int)(unit / a.num_kv_heads);
-    at = stop;
-    p.n = j1 - j0;
-    p.b = x.z, p.h = (int)(unit - (long long)tile * a.num_kv_heads);
-    p.j0 = x.w + j0;
-    p.row0 = tile * tile_rows, p.rows = min(tile_rows, x.y - p.row0);
-    p.tau = x.x;
-    p.hidden = y.y, p.lk = y.z;
-    p.place = j0 == 0 ? (e >= a.batch ? a.total_q : 0) + x.x : -1;
-    const long long last = min((long long)y.z, (long long)y.y + (p.row0 + p.rows - 1) / G + 1) - (long long)p.j0 * kBlk;
-    p.keys = (int)max(0ll, min(last, (long long)p.n * kBlk));
+    const int in = (int)(at - unit_at);
+    const bool ends = unit_at + len <= end;  // within the range
+    const int j0 = block_from(line, cost, in), j1 = ends ? y.x : min(y.x, block_from(line, cost, (int)(end - unit_at)));
+    if (j1 > j0 || in == 0) {
+      const int G = a.num_qo_heads / a.num_kv_heads;
+      p.n = j1 - j0;
+      p.whole = j0 == 0 && j1 == y.x;
+      p.b = x.z, p.h = h, p.j0 = (x.w & ~kGroupRun) + j0;
+      p.row0 = tile * tile_rows_of(line), p.rows = min(tile_rows_of(line), x.y - p.row0);
+      p.tau = x.x;
+      p.hidden = y.y, p.lk = y.z;
+      p.place = j0 == 0 ? ((x.w & kGroupRun) ? a.total_q : 0) + x.x : -1;
+      const long long last = min((long long)y.z, (long long)y.y + (p.row0 + p.rows - 1) / G + 1) - (long long)p.j0 * kBlk;
+      p.keys = (int)max(0ll, min(last, (long long)p.n * kBlk));
+      p.e = e, p.tile_head = tile * a.num_kv_heads + h;
+      p.group = y.w;
+      p.many = x.y > G;
+    }
+    at = ends ? unit_at + len : end;
+    if (ends) {
+      unit_at = at;
+      if (++h == a.num_kv_heads) {
+        h = 0;
+        if (++tile == tiles) {
+          tile = 0, ++e;
+          x = nx, y = ny;
+          open();
+          ahead();
+        }
+      }
+    }
+  }
+};
+
+// Where the parts of a unit are: at the rows' own places, and at those of the
+// `n` CTAs from c0 + 1 on.
+struct Parts {
+  int c0, n;
+};
+// Of a unit (entry e of a line with these blocks and rows).
+MSA_DEV Parts parts_of(const PrefixArgs& a, int line, const Ranges& r, int e, int rows, int blocks, int tile_head) {
+  const int cost = block_cost(line, rows), len = unit_cost(line) + blocks * cost;
+  const long long at = __ldcg(starts_of(a, line) + e) + (long long)tile_head * len;
+  const int c0 = r.holder(at), c1 = blocks > 1 ? r.holder(at + block_at(line, cost, blocks - 1)) : c0;
+  return {c0, c1 - c0};
+}
+MSA_DEV size_t cta_parts(const PrefixArgs& a, int line) {
+  return a.part_rows + (line ? (size_t)a.small_grid * kSmallRows : 0);
+}
+
+// The parts of a group's run that rows of one of its requests join: of up to 16
+// rows side by side, which lie in one of its tiles or two.
+struct Before {
+  int on;        // the request has a group's run before its own
+  int row0;      // of the group's entry: its row of row 0
+  int tile;      // and the tile of that row
+  Parts parts[2];  // of this tile and the next
+};
+// By a whole warp.
+MSA_DEV Before before_of(const PrefixArgs& a, const Ranges& big, int group, int tau, int row0, int rows, int h) {
+  Before f{};
+  const int code = group < 0 ? -1 : __ldcg(a.group + group);
+  if (code < 0) return f;
+  const int4* w = work_of(a, 1) + 2 * code;
+  const int4 x = __ldcg(w);
+  const int blocks = __ldcg(&w[1].x), G = a.num_qo_heads / a.num_kv_heads;
+  f.on = 1;
+  f.row0 = (tau - x.x) * G + row0;
+  f.tile = f.row0 / kBigRows;
+  const int lane = threadIdx.x & 31, last = (f.row0 + rows - 1) / kBigRows;
+  const Parts mine = parts_of(a, 1, big, code, x.y, blocks, min(f.tile + (lane & 1), last) * a.num_kv_heads + h);
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    f.parts[i] = {__shfl_sync(0xffffffffu, mine.c0, i), __shfl_sync(0xffffffffu, mine.n, i)};
+  return f;
+}
+
+// Running sum of eight columns of a row's parts, by one thread.
+struct Joined {
+  float m = -INFINITY, l = 0.f, o[8] = {};
+  MSA_DEV void add(float2 ml, const float (&v)[8]) {
+    if (ml.x == -INFINITY) return;  // a part without a visible key may hold anything
+    const float top = fmaxf(m, ml.x), f = m == -INFINITY ? 0.f : ex2(m - top), p = ex2(ml.x - top);
+    m = top;
+    l = fmaf(l, f, p * ml.y);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) o[c] = fmaf(p, v[c], o[c] * f);
+  }
+  // Those at `first`, then those of the CTAs; loads of four at a time.
+  MSA_DEV void add_parts(const PrefixArgs& a, size_t first, size_t ctas, int tile_rows, int row, Parts parts, int col) {
+    constexpr int kAhead = 4;
+    for (int i0 = 0; i0 <= parts.n; i0 += kAhead) {
+      float2 ml[kAhead];
+      float4 v[kAhead][2];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int i = min(i0 + u, parts.n);
+        const size_t at = i == 0 ? first : ctas + (size_t)(parts.c0 + i) * tile_rows + row;
+        ml[u] = __ldcg(a.part_ml + at);
+        const float4* from = reinterpret_cast<const float4*>(a.part_o + at * kHeadDim + col);
+        v[u][0] = __ldcg(from), v[u][1] = __ldcg(from + 1);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (i0 + u > parts.n) break;
+        const float x[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w, v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
+        add(ml[u], x);
+      }
+    }
+  }
+  MSA_DEV void add_before(const PrefixArgs& a, const Before& f, int r, size_t own_row, int col) {
+    if (!f.on) return;
+    const int row = f.row0 + r, tile = row / kBigRows;
+    add_parts(a, (size_t)a.total_q * a.num_qo_heads + own_row, cta_parts(a, 1), kBigRows, row - tile * kBigRows,
+              f.parts[tile - f.tile], col);
+  }
+  MSA_DEV bool finite() const {
+    float x = 0.f;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) x = fmaf(o[c], 0.f, x);
+    return x == 0.f && l < INFINITY;
+  }
+  // Output row `orow` (token and head of q).
+  MSA_DEV void write(const PrefixArgs& a, size_t orow, int col) const {
+    const bool has = l != 0.f;
+    const float inv = has ? 1.f / l : 0.f;
+    auto pack = [&](float x, float y) { return a.f16 ? pack_f16x2(x, y) : pack_bf16x2(x, y); };
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * kHeadDim + col) =
+        make_uint4(pack(o[0] * inv, o[1] * inv), pack(o[2] * inv, o[3] * inv), pack(o[4] * inv, o[5] * inv),
+                   pack(o[6] * inv, o[7] * inv));
+    if (col == 0 && a.lse != nullptr) a.lse[orow] = has ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
 };
 
