@@ -816,15 +816,15 @@ PrefixLayout prefix_layout(int batch, int total_q, int hq, bool groups) {
     return at;
   };
   L.off_group = place((size_t)batch * sizeof(int));
-  L.off_work = place((size_t)batch * 8 * sizeof(int4));
-  L.off_start = place(2 * (2 * (size_t)batch + 1) * sizeof(long long));
+  L.off_work = place((size_t)batch * 4 * sizeof(int4));
+  L.off_start = place((2 * (size_t)batch + 1) * sizeof(long long));
   L.off_chunk = place((2 * (size_t)batch + 1) * sizeof(int));
   L.off_token = place((size_t)total_q * sizeof(int2));
-  L.off_meta = place(4 * sizeof(int));
+  L.off_meta = place(2 * sizeof(int));
   L.off_cut = place((size_t)kPlanSMs * sizeof(int4));
   L.off_odd = place((size_t)total_q * hq * sizeof(int));
   L.part_rows = (size_t)total_q * hq * (groups ? 2 : 1);
-  const size_t rows = L.part_rows + (size_t)kPlanSMs * (kSmallRows + kBigRows);
+  const size_t rows = L.part_rows + (size_t)kPlanSMs * kBigRows;
   L.off_ml = place(rows * sizeof(float2));
   L.off_o = place(rows * 128 * sizeof(float));
   L.total = off;
@@ -899,10 +899,8 @@ msa_status_t build_prefix(
   a.scale_log2 = scale * 1.4426950408889634f;
   a.out = out;
   a.lse = lse;
-  // Without groups and with few rows a request there is no unit of many rows.
-  const long long most = (long long)max_seqlen_q * (num_qo_heads / num_kv_heads);
-  a.small_rows = !groups && max_seqlen_q > 0 && most <= kSmallRows ? INT_MAX : kSmallRows;
-  a.small_grid = a.big_grid = kPlanSMs;
+  a.small = !groups && max_seqlen_q > 0 && (long long)max_seqlen_q * (num_qo_heads / num_kv_heads) <= kSmallRows ? 1 : 0;
+  a.grid = kPlanSMs;
   a.entry = reinterpret_cast<int4*>(ws);
   a.work = reinterpret_cast<int4*>(ws + L.off_work);
   a.start = reinterpret_cast<long long*>(ws + L.off_start);

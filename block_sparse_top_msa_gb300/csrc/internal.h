@@ -185,12 +185,12 @@ struct TreeArgs {
 };
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t s);
 
-// Attention over shared prefixes (prefix.cu, prefix_big.cu, prefix_work.cuh).
-// Two lines of work: units of few rows (line 0) and of many. Costs of a unit
-// besides its blocks, and the least cost of a CTA's range, at least a unit's
-// with one block.
+// Attention over shared prefixes (prefix.cu, prefix_big.cu, prefix_work.cuh). A
+// call's units are all of few rows (prefix.cu's kernel) or all of many
+// (prefix_big.cu). Costs of a unit besides its blocks, and the least cost of a
+// CTA's range, at least a unit's with one block.
 constexpr int kSmallRows = 16, kBigRows = 256;
-constexpr int kSmallUnitCost = 1, kBigUnitCost = 12, kSmallRange = 3, kBigRange = 16;
+constexpr int kSmallUnitCost = 5, kBigUnitCost = 12, kSmallRange = 7, kBigRange = 16;
 constexpr int kGroupRun = 1 << 30;  // of an entry's first block: the entry is a group's
 struct PrefixArgs {
   unsigned* fault = nullptr;
@@ -211,25 +211,25 @@ struct PrefixArgs {
   float scale_log2 = 0.f;
   void* out = nullptr;
   float* lse = nullptr;
-  int small_rows = 0;  // entries of more rows go to line 1; INT_MAX: there is none
-  int small_grid = 0, big_grid = 0;
+  int small = 0;  // units of kSmallRows rows (no groups then), else of kBigRows
+  int grid = 0;   // CTAs
   // Workspace. Positions: the requests in the order of the groups. Entries: the
-  // positions' own runs and the groups', each on one of the lines.
-  int4* entry = nullptr;       // (batch, 2): first token in that order, tokens, request, group; first row of q, Lk - Lq, Lk, entry
-  int* group = nullptr;        // (batch): a group's entry; entries are numbers on their line, + kGroupRun on line 1, -1 for none
-  int4* work = nullptr;        // (2, 2 batch, 2): first token, rows, page row, first block (| kGroupRun); blocks, keys that all rows see, Lk, group before or -1
-  long long* start = nullptr;  // (2, 2 batch + 1): running sums of the entries' costs
-  int* chunk = nullptr;        // (2 batch + 1): of line 1's entries, 16 rows of one KV head each, of those that are requests'
+  // positions' own runs, then the groups', those that there are.
+  int4* entry = nullptr;       // (batch, 2): first token in that order, tokens, request, group; first row of q, Lk - Lq, Lk, entry or -1
+  int* group = nullptr;        // (batch): a group's entry or -1
+  int4* work = nullptr;        // (2 batch, 2): first token, rows, page row, first block (| kGroupRun); blocks, keys that all rows see, Lk, group before or -1
+  long long* start = nullptr;  // (2 batch + 1): running sums of the entries' costs
+  int* chunk = nullptr;        // (2 batch + 1): running count of what the join does for entries with a group before: 16 rows of one KV head each
   int2* token = nullptr;       // (total_q): each token's row of q, and its position
-  int* meta = nullptr;         // tokens in all, entries on line 0, on line 1, odd rows
-  int4* cut = nullptr;         // (small_grid): the unit that begins in the CTA's range and goes on after it: entry, tile and head; entry -1: none
+  int* meta = nullptr;         // entries, odd rows
+  int4* cut = nullptr;         // (grid): the unit without a group before that begins in the CTA's range and goes on after it: entry, tile and head; entry -1: none
   int* odd = nullptr;          // (total_q * Hq): rows that are not finite, by token in the groups' order and head
   size_t part_rows = 0;        // rows of parts before the CTAs' own
-  float2* part_ml = nullptr;   // (part_rows + small_grid * kSmallRows + big_grid * kBigRows)
+  float2* part_ml = nullptr;   // (part_rows + grid * kBigRows)
   float* part_o = nullptr;     // the same, 128 each
 };
 cudaError_t launch_prefix(const PrefixArgs& a, cudaStream_t s);
-cudaError_t launch_prefix_big(const PrefixArgs& a, cudaStream_t s);  // line 1 (prefix_big.cu)
+cudaError_t launch_prefix_big(const PrefixArgs& a, cudaStream_t s);  // the units, where they are of many rows
 
 struct ProxyArgs {
   unsigned* fault;      // device fault word (bounded-wait expiry, capacity)

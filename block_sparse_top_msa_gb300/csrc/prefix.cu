@@ -13,10 +13,10 @@
 // piece of a unit leaves its parts at the rows' own places, the others (a CTA
 // has one at most, its first) at the CTA's.
 //
-// Groups' runs, and those of requests with many rows, are units of 256 rows
-// for prefix_big.cu (line 1); the other requests' are units of 16 rows here
-// (line 0), which come after: a unit that one CTA has whole takes its group's
-// parts in and writes its rows. What is left is joined by the last kernel.
+// Where requests have at most 16 rows for each KV head and share nothing, the
+// units are of 16 rows and this file's kernel takes them; else they are of 256,
+// prefix_big.cu's. A unit that is a request's alone and that one CTA has whole
+// is written there and then; what is left is joined by the last kernel.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -53,67 +53,70 @@ MSA_DEV T block_upto(T v, T* s_warp, T& all) {
   return inc + (warp > 0 ? before : T(0));
 }
 
-// Three running sums over a block; every thread has to come.
+// Two running sums over a block; every thread has to come.
 struct Sums {
-  long long v[3];
+  long long cost, counts;
 };
 MSA_DEV Sums block_sums(Sums x, Sums* s_warp, Sums& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) x.v[i] = warp_upto(x.v[i], lane);
+  x = {warp_upto(x.cost, lane), warp_upto(x.counts, lane)};
   __syncthreads();
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
   Sums w = s_warp[lane];
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    w.v[i] = warp_upto(w.v[i], lane);
-    all.v[i] = __shfl_sync(0xffffffffu, w.v[i], 31);
-    const long long before = __shfl_sync(0xffffffffu, w.v[i], warp > 0 ? warp - 1 : 0);
-    if (warp > 0) x.v[i] += before;
-  }
+  w = {warp_upto(w.cost, lane), warp_upto(w.counts, lane)};
+  all = {__shfl_sync(0xffffffffu, w.cost, 31), __shfl_sync(0xffffffffu, w.counts, 31)};
+  const int from = warp > 0 ? warp - 1 : 0;
+  const Sums before{__shfl_sync(0xffffffffu, w.cost, from), __shfl_sync(0xffffffffu, w.counts, from)};
+  if (warp > 0) x.cost += before.cost, x.counts += before.counts;
   return x;
 }
 
 // The work, by one block: the requests in the order of their groups, where
 // their tokens begin in that order, the blocks that each group attends for
-// all, the two lines' entries and the running sums of what they cost.
+// all, the entries and the running sums of what they cost.
 __global__ void __launch_bounds__(kPlanThreads)
     prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ int dyn[];
   __shared__ Sums s_sums[32];
   __shared__ int s_int[32];
-  __shared__ int s_kept;
   int* least = dyn;             // (batch): blocks that a group attends for all
   int* tokens = dyn + a.batch;  // (batch): a group's tokens
-  uint32_t* several = reinterpret_cast<uint32_t*>(dyn + 2 * a.batch);                 // a bit per group: more than one request has some
+  uint32_t* several = reinterpret_cast<uint32_t*>(dyn + 2 * a.batch);             // a bit per group: more than one request has some
   uint16_t* begins = reinterpret_cast<uint16_t*>(several + (a.batch + 31) / 32);  // (batch): cu_groups
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.num_qo_heads / a.num_kv_heads;
   grid_dependency_wait();
   grid_dependents_launch();
   const bool groups = a.group_rows != nullptr;
+  // Up to a thread each the requests stay in registers from the first pass to
+  // the second.
+  int b = -1, t0 = 0, t1 = 0, lk = 0;
+  auto request = [&](int i) {
+    b = groups ? __ldg(a.group_rows + i) : i;
+    t0 = t1 = lk = 0;
+    if (b >= 0 && b < a.batch) {
+      t0 = __ldg(a.cu_q + b), t1 = __ldg(a.cu_q + b + 1);
+      lk = max(0, __ldg(a.seqused_k + b));
+    }
+  };
+  if (tid < a.batch) request(tid);
   for (int g = tid; g < a.batch; g += kPlanThreads) {
     least[g] = groups ? max(0, min(__ldg(a.group_blocks + g), a.max_pages)) : 0;
     tokens[g] = 0;
     begins[g] = (uint16_t)(groups ? max(0, min(__ldg(a.cu_groups + g), 65535)) : g);
     if ((g & 31) == 0) several[g >> 5] = 0u;
   }
-  for (int i = tid; i < a.small_grid; i += kPlanThreads) a.cut[i] = make_int4(-1, 0, 0, 0);
-  if (tid == 0) s_kept = 0;
+  for (int i = tid; i < a.grid; i += kPlanThreads) a.cut[i] = make_int4(-1, 0, 0, 0);
   __syncthreads();
-  int before = 0;
+  int before = 0, tau = 0, lq = 0, g = 0;
   for (int i0 = 0; i0 < a.batch; i0 += kPlanThreads) {
     const int i = i0 + tid;
-    int b = -1, t0 = 0, lq = 0, lk = 0, g = i;
+    lq = 0;
     if (i < a.batch) {
-      b = groups ? __ldg(a.group_rows + i) : i;
-      if (b >= 0 && b < a.batch) {
-        t0 = __ldg(a.cu_q + b);
-        const int t1 = __ldg(a.cu_q + b + 1);
-        if (t0 >= 0 && t1 <= a.total_q && t1 > t0) lq = t1 - t0;
-        lk = max(0, __ldg(a.seqused_k + b));
-      }
+      if (i0 > 0) request(i);
+      if (t0 >= 0 && t1 <= a.total_q && t1 > t0) lq = t1 - t0;
+      g = i;
       if (groups) {
         int lo = 0;  // the last group that begins at or before i
         for (int hi = a.batch; hi - lo > 1;) {
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       }
     }
     int all;
-    const int tau = before + block_upto<int>(lq, s_int, all) - lq;
+    tau = before + block_upto<int>(lq, s_int, all) - lq;
     before += all;
     if (i < a.batch) {
       // With requests listed twice the sums may pass the tokens there are: the
@@ -135,64 +138,63 @@ __global__ void __launch_bounds__(kPlanThreads)
       if (lq > 0) {
         atomicMin(&least[g], max(0, lk - lq) / kBlk);
         if (atomicAdd(&tokens[g], lq) > 0) atomicOr(&several[g >> 5], 1u << (g & 31));
-        atomicMax(&s_kept, tau + lq);
       }
     }
   }
   __syncthreads();
-  Sums base{};  // costs of the lines; entries on line 0, on line 1 from bit 16, chunks from bit 32
+  Sums base{};  // cost; entries, and chunks from bit 32
+  const int tile = tile_rows_of(a);
   for (int e0 = 0; e0 < 2 * a.batch; e0 += kPlanThreads) {
-    const int e = e0 + tid, g = e - a.batch;
+    const int e = e0 + tid, eg = e - a.batch;
     int4 x = make_int4(0, 0, 0, 0), y = make_int4(0, 0, 0, 0);
-    int line = -1;
+    bool there = false, joined = false;
     if (e < a.batch) {
-      const int4 r = a.entry[2 * e], s = a.entry[2 * e + 1];
+      int4 r, s;
+      if (e0 == 0 && a.batch <= kPlanThreads) r = make_int4(tau, lq, b, g), s = make_int4(t0, lk - lq, lk, -1);
+      else r = a.entry[2 * e], s = a.entry[2 * e + 1];
       const bool shares = (several[r.w >> 5] >> (r.w & 31)) & 1u;
       const int from = shares ? least[r.w] : 0;
       const int blocks = (int)min((long long)a.max_pages, ((long long)s.z + kBlk - 1) / kBlk);
       x = make_int4(r.x, r.y * G, r.z, from);
       y = make_int4(max(0, blocks - from), a.causal ? s.y : s.z, s.z, from > 0 ? r.w : -1);
-      if (r.y > 0) line = x.y > a.small_rows;
-    } else if (e < 2 * a.batch && groups && ((several[g >> 5] >> (g & 31)) & 1u) && least[g] > 0) {
-      const int first = min((int)begins[g], a.batch - 1), lead = __ldg(a.group_rows + first);
-      x = make_int4(a.entry[2 * first].x, tokens[g] * G, max(0, min(lead, a.batch - 1)), kGroupRun);
-      y = make_int4(least[g], least[g] * kBlk, least[g] * kBlk, -1);
-      line = 1;
+      there = r.y > 0;
+      joined = there && from > 0;
+    } else if (e < 2 * a.batch && groups && ((several[eg >> 5] >> (eg & 31)) & 1u) && least[eg] > 0) {
+      const int first = min((int)begins[eg], a.batch - 1), lead = __ldg(a.group_rows + first);
+      x = make_int4(a.entry[2 * first].x, tokens[eg] * G, max(0, min(lead, a.batch - 1)), kGroupRun);
+      y = make_int4(least[eg], least[eg] * kBlk, least[eg] * kBlk, -1);
+      there = true;
     }
     Sums mine{};
-    if (line >= 0) {
-      const int tile = tile_rows_of(line);
-      mine.v[line] = (long long)((x.y + tile - 1) / tile) * a.num_kv_heads * (unit_cost(line) + (long long)y.x * block_cost(line, x.y));
-      mine.v[2] = 1ll << (16 * line);
-      if (line == 1 && e < a.batch) mine.v[2] += (long long)((x.y + 15) / 16) * a.num_kv_heads << 32;
+    if (there) {
+      mine.cost = (long long)((x.y + tile - 1) / tile) * a.num_kv_heads * (unit_cost(a) + (long long)y.x * block_cost(a, x.y));
+      mine.counts = 1 + (joined ? (long long)((x.y + 15) / 16) * a.num_kv_heads << 32 : 0);
     }
     Sums all;
     const Sums upto = block_sums(mine, s_sums, all);
-    const long long counts = base.v[2] + upto.v[2] - mine.v[2];
-    const int at = line == 1 ? (int)(counts >> 16) & 0xffff : (int)counts & 0xffff;
-    if (line >= 0) {
-      a.start[line * (2 * a.batch + 1) + at] = base.v[line] + upto.v[line] - mine.v[line];
-      a.work[line * 4 * a.batch + 2 * at] = x;
-      a.work[line * 4 * a.batch + 2 * at + 1] = y;
-      if (line == 1) a.chunk[at] = (int)(counts >> 32);
+    const long long counts = base.counts + upto.counts - mine.counts;
+    const int at = (int)counts;
+    if (there) {
+      a.start[at] = base.cost + upto.cost - mine.cost;
+      a.chunk[at] = (int)(counts >> 32);
+      a.work[2 * at] = x;
+      a.work[2 * at + 1] = y;
     }
-    if (e < a.batch) a.entry[2 * e + 1].w = line < 0 ? -1 : line == 1 ? at | kGroupRun : at;
-    else if (e < 2 * a.batch) a.group[g] = line < 0 ? -1 : at;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) base.v[i] += all.v[i];
+    if (e < a.batch) a.entry[2 * e + 1].w = there ? at : -1;
+    else if (e < 2 * a.batch) a.group[eg] = there ? at : -1;
+    base = {base.cost + all.cost, base.counts + all.counts};
   }
-  if (tid < 2) {
-    const int n = (int)(base.v[2] >> (16 * tid)) & 0xffff;
-    a.start[tid * (2 * a.batch + 1) + n] = base.v[tid];
-    a.meta[1 + tid] = n;
-    if (tid == 1) a.chunk[n] = (int)(base.v[2] >> 32);
-    if (tid == 0) a.meta[0] = s_kept, a.meta[3] = 0;
+  if (tid == 0) {
+    const int n = (int)base.counts;
+    a.start[n] = base.cost;
+    a.chunk[n] = (int)(base.counts >> 32);
+    a.meta[0] = n, a.meta[1] = 0;
   }
   // Each token's place in the groups' order, a warp for each request.
   for (int i = warp; i < a.batch; i += kPlanThreads / 32) {
     const int4 x = a.entry[2 * i];
-    const int t0 = a.entry[2 * i + 1].x;
-    for (int j = lane; j < x.y; j += 32) a.token[x.x + j] = make_int2(t0 + j, i);
+    const int first = a.entry[2 * i + 1].x;
+    for (int j = lane; j < x.y; j += 32) a.token[x.x + j] = make_int2(first + j, i);
   }
 }
 
@@ -221,7 +223,6 @@ struct __align__(1024) SmallSmem {
   uint8_t stage[Small<KV>::kStages][Small<KV>::kStage];
   uint8_t q[kPieces][16 * kQStride];
   Piece piece[kPieces];
-  Before before[kPieces];
   float2 ml[2][kWarps][16];
   int page_ok[Small<KV>::kStages];
   uint64_t piece_full[kPieces], piece_empty[kPieces], full[Small<KV>::kStages], empty[Small<KV>::kStages], join;
@@ -295,8 +296,7 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ pieces and Q
-    const Ranges ranges = ranges_of(a, 0), big = ranges_of(a, 1);
-    Walk walk(a, 0, ranges, blockIdx.x);
+    Walk walk(a, blockIdx.x);
     Piece p{};
     int e = -1, row0 = -1;
     uint32_t from[8];  // a lane's eight of the tile's sixteen-byte groups: token of the row, times heads
@@ -308,7 +308,6 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
                 mbar_wait_sleep(&sm.piece_empty[slot], ((np / kPieces) - 1) & 1, fault, kFaultWaitSoftmax, abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      Before f{};
       if (more) {
         // Q's rows of the tile, zeros behind them. A lane has 16 bytes of each
         // second row.
@@ -329,13 +328,11 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
                        "l"(q + ((size_t)from[i] + (r < p.rows ? p.h * G : 0)) * 256), "r"(r < p.rows ? 16 : 0)
                        : "memory");
         }
-        if (p.whole) f = before_of(a, big, p.group, p.tau, p.row0, p.rows, p.h);
-        else if (p.place >= 0) cut = make_int4(p.e, p.tile_head, 0, 0);
+        if (!p.whole && p.place >= 0) cut = make_int4(p.e, p.tile_head, 0, 0);
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sm.piece_full[slot])) : "memory");
       if (lane == 0) {
         sm.piece[slot] = p;
-        sm.before[slot] = f;
         mbar_arrive(&sm.piece_full[slot]);
       }
       __syncwarp();
@@ -647,7 +644,6 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
       for (int c = 0; c < 8; ++c) own.o[c] = fmaf(f, v[c], own.o[c]);
     }
     own.m = M;
-    const Before before = sm.before[slot];
     fence_async_smem();  // the slots are TMA's again
     __syncwarp();
     if (lane == 0) {
@@ -659,20 +655,17 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
     const size_t hq = (size_t)p.h * G + er % G, own_row = (size_t)(p.tau + er / G) * a.num_qo_heads + hq;
     bool odd = false;
     if (live && p.whole) {
-      Joined all;
-      all.add_before(a, before, out_row, own_row, col);
-      all.add(make_float2(own.m, own.l), own.o);
-      odd = a.causal && p.many && !all.finite();
-      all.write(a, (size_t)token * a.num_qo_heads + hq, col);
+      odd = a.causal && p.many && !own.finite();
+      own.write(a, (size_t)token * a.num_qo_heads + hq, col);
     } else if (live) {
-      const size_t at = p.place >= 0 ? own_row : cta_parts(a, 0) + (size_t)blockIdx.x * kSmallRows + out_row;
+      const size_t at = p.place >= 0 ? own_row : a.part_rows + (size_t)blockIdx.x * kSmallRows + out_row;
       float4* to = reinterpret_cast<float4*>(a.part_o + at * kHeadDim + col);
       to[0] = make_float4(own.o[0], own.o[1], own.o[2], own.o[3]);
       to[1] = make_float4(own.o[4], own.o[5], own.o[6], own.o[7]);
       if (col == 0) a.part_ml[at] = make_float2(own.m, own.l);
     }
     const unsigned rows_odd = __ballot_sync(0xffffffffu, odd);
-    if ((lane & 15) == 0 && ((rows_odd >> lane) & 0xffffu)) a.odd[atomicAdd(a.meta + 3, 1)] = (int)own_row;
+    if ((lane & 15) == 0 && ((rows_odd >> lane) & 0xffffu)) a.odd[atomicAdd(a.meta + 1, 1)] = (int)own_row;
   }
 }
 
@@ -732,15 +725,14 @@ __device__ __noinline__ void own_run(const PrefixArgs& a, size_t orow, int b, in
 }
 
 // A row that is not finite: its group's parts, and its own run anew.
-__device__ __noinline__ void odd_row(const PrefixArgs& a, const Ranges& big, int own_row, int lane) {
+__device__ __noinline__ void odd_row(const PrefixArgs& a, const Ranges& ranges, int own_row, int lane) {
   const int G = a.num_qo_heads / a.num_kv_heads, tau = own_row / a.num_qo_heads, hq = own_row - tau * a.num_qo_heads, h = hq / G;
   const int2 token = __ldcg(a.token + tau);
-  const int code = __ldcg(&a.entry[2 * token.y + 1].w);
-  const int4* w = work_of(a, code >= kGroupRun) + 2 * (code & ~kGroupRun);
+  const int4* w = a.work + 2 * __ldcg(&a.entry[2 * token.y + 1].w);
   const int4 x = __ldcg(w), y = __ldcg(w + 1);
   const int row = (tau - x.x) * G + hq - h * G, col = (lane & 15) * 8;
   const size_t orow = (size_t)token.x * a.num_qo_heads + hq;
-  const Before f = before_of(a, big, y.w, x.x, row, 1, h);
+  const Before f = before_of(a, ranges, y.w, x.x, row, 1, h);
   Joined all;
   all.add_before(a, f, 0, own_row, col);
   float m, l, o[4];
@@ -753,74 +745,55 @@ __device__ __noinline__ void odd_row(const PrefixArgs& a, const Ranges& big, int
   if (lane < 16) all.write(a, orow, col);
 }
 
-// Joins what is left: 16 rows at a time of the requests on line 1, of the units
-// of line 0 that ranges cut; 16 threads a row, of eight columns each. First the
-// parts of the group's run, then those of the own one, in the order of the
-// pieces.
+// Joins what is left, 16 rows at a time: of the requests with a group's run
+// before their own, and of the other units that ranges cut. Each warp of a
+// block finds the parts for itself and has two of the rows, 16 lanes each, of
+// eight columns: first the parts of the group's run, then those of the own one,
+// in the order of the pieces.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
     prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
-  __shared__ Piece s_piece;  // the rows' own unit; rows 16, from row0 on
-  __shared__ Before s_before;
-  __shared__ Parts s_parts;
-  __shared__ int s_line;
-  __shared__ uint32_t s_odd;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = a.num_qo_heads / a.num_kv_heads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.num_qo_heads / a.num_kv_heads;
+  const int warps = gridDim.x * (kJoinThreads / 32), per_cut = tile_rows_of(a) / 16, cuts = a.grid * per_cut;
   grid_dependency_wait();
   grid_dependents_launch();
-  const Ranges lines[2] = {ranges_of(a, 0), ranges_of(a, 1)};
-  const int odd = __ldcg(a.meta + 3);
-  for (int i = blockIdx.x * (kJoinThreads / 32) + warp; i < odd; i += gridDim.x * (kJoinThreads / 32))
-    odd_row(a, lines[1], __ldcg(a.odd + i), lane);
-  const int entries = __ldcg(a.meta + 2), chunks = __ldcg(a.chunk + entries);
-  for (int i = blockIdx.x; i < a.small_grid + chunks; i += gridDim.x) {
-    if (warp == 0) {
-      int line = 0, e = -1, tile_head = 0, row0 = 0;
-      if (i < a.small_grid) {
-        const int4 cut = __ldcg(a.cut + i);
-        e = cut.x, tile_head = cut.y;
-        row0 = tile_head / a.num_kv_heads * kSmallRows;
-      } else {
-        line = 1;
-        e = last_upto(a.chunk, entries, i - a.small_grid);
-        const int c = i - a.small_grid - __ldcg(a.chunk + e), r = c / a.num_kv_heads;
-        row0 = r * 16;
-        tile_head = row0 / kBigRows * a.num_kv_heads + c - r * a.num_kv_heads;
-      }
-      Piece p{};
-      p.n = -1;
-      if (e >= 0) {
-        const int4* w = work_of(a, line) + 2 * e;
-        const int4 x = __ldcg(w), y = __ldcg(w + 1);
-        p.n = y.x;
-        p.h = tile_head % a.num_kv_heads;
-        p.row0 = row0, p.rows = min(16, x.y - row0), p.tau = x.x, p.many = x.y > G;
-        const Parts parts = parts_of(a, line, lines[line], e, x.y, y.x, tile_head);
-        const Before f = before_of(a, lines[1], y.w, x.x, row0, p.rows, p.h);
-        if (lane == 0) s_parts = parts, s_before = f;
-      }
-      if (lane == 0) s_piece = p, s_line = line, s_odd = 0u;
+  const int entries = __ldcg(a.meta), odd = __ldcg(a.meta + 1);
+  const Ranges ranges = ranges_of(a, entries);
+  for (int i = warp * gridDim.x + blockIdx.x; i < odd; i += warps) odd_row(a, ranges, __ldcg(a.odd + i), lane);
+  const int chunks = __ldcg(a.chunk + entries);
+  for (int i = blockIdx.x; i < cuts + chunks; i += gridDim.x) {
+    int e, tile_head, row0;
+    if (i < cuts) {
+      const int4 cut = __ldcg(a.cut + i / per_cut);
+      e = cut.x, tile_head = cut.y;
+      row0 = tile_head / a.num_kv_heads * tile_rows_of(a) + i % per_cut * 16;
+      if (e < 0) continue;
+    } else {
+      e = last_upto(a.chunk, entries, i - cuts);
+      const int c = i - cuts - __ldcg(a.chunk + e), r = c / a.num_kv_heads;
+      row0 = r * 16;
+      tile_head = row0 / tile_rows_of(a) * a.num_kv_heads + c - r * a.num_kv_heads;
     }
-    __syncthreads();
-    const Piece p = s_piece;
-    const int row = tid >> 4, er = p.row0 + row, col = (tid & 15) * 8;
-    const bool live = p.n >= 0 && row < p.rows;
-    const size_t hq = (size_t)p.h * G + er % G, own_row = (size_t)(p.tau + er / G) * a.num_qo_heads + hq;
-    if (live) {
-      const int token = __ldcg(&a.token[p.tau + er / G].x), line = s_line, tile_rows = tile_rows_of(line);
+    const int4* w = a.work + 2 * e;
+    const int4 x = __ldcg(w), y = __ldcg(w + 1);
+    if (row0 >= x.y) continue;
+    const int h = tile_head % a.num_kv_heads, rows = min(16, x.y - row0), col = (lane & 15) * 8;
+    const Parts parts = parts_of(a, ranges, e, x.y, y.x, tile_head);
+    const Before f = before_of(a, ranges, y.w, x.x, row0, rows, h);
+    const int r = 2 * warp + (lane >> 4), er = row0 + r;
+    const size_t hq = (size_t)h * G + er % G, own_row = (size_t)(x.x + er / G) * a.num_qo_heads + hq;
+    bool bad = false;
+    if (r < rows) {
+      const int token = __ldcg(&a.token[x.x + er / G].x);
       Joined all;
-      all.add_before(a, s_before, row, own_row, col);
-      all.add_parts(a, own_row, cta_parts(a, line), tile_rows, er % tile_rows, s_parts, col);
-      if (a.causal && p.many && !all.finite()) atomicOr(&s_odd, 1u << row);
+      all.add_before(a, f, r, own_row, col);
+      all.add_parts(a, own_row, er % tile_rows_of(a), parts, col);
+      bad = a.causal && x.y > G && !all.finite();
       all.write(a, (size_t)token * a.num_qo_heads + hq, col);
     }
-    __syncthreads();
-    for (uint32_t left = s_odd; left != 0u; left &= left - 1u) {
-      const int r = __ffs(left) - 1, o = p.row0 + r;
-      if (r % (kJoinThreads / 32) == warp)
-        odd_row(a, lines[1], (int)((p.tau + o / G) * a.num_qo_heads + p.h * G + o % G), lane);
-    }
-    __syncthreads();
+    const unsigned bads = __ballot_sync(0xffffffffu, bad);
+    for (int k = 0; k < 2; ++k)
+      if ((bads >> (16 * k)) & 0xffffu) odd_row(a, ranges, (int)__shfl_sync(0xffffffffu, (unsigned)own_row, 16 * k), lane);
   }
 }
 
@@ -829,7 +802,7 @@ cudaError_t launch_small(const PrefixArgs& a, cudaStream_t s) {
   const int smem = (int)sizeof(SmallSmem<KV>) + 1024;
   cudaError_t e = set_smem_limit((const void*)prefix_small_kernel<KV>, smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(prefix_small_kernel<KV>, dim3(a.small_grid), Small<KV>::kThreads, smem, s, a);
+  return launch_dependent(prefix_small_kernel<KV>, dim3(a.grid), Small<KV>::kThreads, smem, s, a);
 }
 
 }  // namespace
@@ -840,17 +813,14 @@ cudaError_t launch_prefix(const PrefixArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_dependent(prefix_plan_kernel, dim3(1), kPlanThreads, smem, s, a);
   if (e != cudaSuccess) return e;
-  if (a.small_rows < INT_MAX) {
-    e = launch_prefix_big(a, s);
-    if (e != cudaSuccess) return e;
-  }
-  e = a.e4m3 ? launch_small<2>(a, s) : a.f16 ? launch_small<1>(a, s) : launch_small<0>(a, s);
+  e = !a.small ? launch_prefix_big(a, s) : a.e4m3 ? launch_small<2>(a, s) : a.f16 ? launch_small<1>(a, s) : launch_small<0>(a, s);
   if (e != cudaSuccess) return e;
-  // Cut units, and as many chunks as there can be, up to eight blocks an SM.
+  // Cut units, and as many chunks as there can be: a block each, up to eight an
+  // SM.
   const long long chunks = ((long long)a.total_q * a.num_qo_heads + 15) / 16 + (long long)a.batch * a.num_kv_heads;
-  const long long items = a.small_grid + (a.small_rows < INT_MAX ? chunks : 0);
-  return launch_dependent(prefix_join_kernel, dim3((unsigned)(items < 8 * a.small_grid ? items : 8 * a.small_grid)),
-                          kJoinThreads, 0, s, a);
+  const long long items = (long long)a.grid * (a.small ? 1 : kBigRows / 16) + (a.group_rows != nullptr ? chunks : 0);
+  const long long blocks = items < 8 * a.grid ? items : 8 * a.grid;
+  return launch_dependent(prefix_join_kernel, dim3((unsigned)blocks), kJoinThreads, 0, s, a);
 }
 
 }  // namespace msa

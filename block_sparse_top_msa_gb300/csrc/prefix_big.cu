@@ -181,8 +181,9 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
 
   if (warp == R::kSched) {
     // ------------------------------------------------------------------ pieces
-    Walk walk(a, 1, ranges_of(a, 1), blockIdx.x);
+    Walk walk(a, blockIdx.x);
     Piece s{};
+    int4 cut = make_int4(-1, 0, 0, 0);
     for (int n = 0;; ++n) {
       const bool more = walk.next(s);
       const int slot = n % kSegRing;
@@ -195,7 +196,9 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         mbar_arrive(&sm.seg_full[slot]);
       }
       if (!more) break;
+      if (s.alone && !s.whole && s.place >= 0) cut = make_int4(s.e, s.tile_head, 0, 0);
     }
+    if (lane == 0) a.cut[blockIdx.x] = cut;
   } else if (warp == R::kQk || warp == R::kPv) {
     // -------------------------------------------------------------- MMA issue
     // A whole warp runs this, so that what an MMA needs stays in uniform
@@ -569,7 +572,12 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     auto place_of = [&](const Piece& s, int r) -> size_t {
       const int er = s.row0 + r;
       return s.place >= 0 ? (size_t)(s.place + er / G) * a.num_qo_heads + (size_t)s.h * G + er % G
-                          : cta_parts(a, 1) + (size_t)blockIdx.x * kBigRows + r;
+                          : a.part_rows + (size_t)blockIdx.x * kBigRows + r;
+    };
+
+    auto out_row = [&](const Piece& s, int r) -> size_t {
+      const int er = s.row0 + r;
+      return (size_t)__ldcg(&a.token[s.tau + er / G].x) * a.num_qo_heads + (size_t)s.h * G + er % G;
     };
 
     // The next piece with blocks; what rows of pieces without any get is here
@@ -585,7 +593,16 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         ++ni;
         if (blocks_of(p) > 0) return true;
         const int r = st * 128 + row;
-        if (r < p.rows) a.part_ml[place_of(p, r)] = make_float2(-INFINITY, 0.f);
+        if (r >= p.rows) continue;
+        if (p.alone && p.whole) {
+          const size_t orow = out_row(p, r);
+          uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + orow * kHeadDim);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) to[c] = make_uint4(0u, 0u, 0u, 0u);
+          if (a.lse != nullptr) a.lse[orow] = -INFINITY;
+        } else {
+          a.part_ml[place_of(p, r)] = make_float2(-INFINITY, 0.f);
+        }
       }
     };
     bool more = next_piece(next) && load_q(next);
@@ -776,7 +793,12 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       const bool joins = !dual && n > 1;
-      const size_t at = active ? place_of(s, r) : 0;
+      // A unit that is all of its rows' is written, others leave their parts.
+      const bool writes = s.alone && s.whole;
+      const size_t at = !active ? 0 : writes ? out_row(s, r) : place_of(s, r);
+      const bool has = l != 0.f;
+      const float inv = has ? 1.f / l : 0.f;
+      float odd = 0.f;  // NaN once an element is not finite
 #pragma unroll 1
       for (int c0q = 0; c0q < 128; c0q += 32) {
         float o[32];
@@ -798,14 +820,31 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
             if (!dual) mbar_arrive(&sm.o_free[1]);
           }
         }
-        if (active) {
+        if (active && writes) {
+          uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * kHeadDim + c0q);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) odd = fmaf(o[c], 0.f, odd);
+#pragma unroll
+          for (int c = 0; c < 32; c += 8)
+            to[c >> 3] = has ? make_uint4(pack_x2<F16>(o[c] * inv, o[c + 1] * inv), pack_x2<F16>(o[c + 2] * inv, o[c + 3] * inv),
+                                          pack_x2<F16>(o[c + 4] * inv, o[c + 5] * inv), pack_x2<F16>(o[c + 6] * inv, o[c + 7] * inv))
+                             : make_uint4(0u, 0u, 0u, 0u);
+        } else if (active) {
           float* to = a.part_o + at * kHeadDim + c0q;
 #pragma unroll
           for (int c = 0; c < 32; c += 8) store8(to + c, o + c);
         }
         __syncwarp();
       }
-      if (active) a.part_ml[at] = make_float2(m_ref == -INFINITY && !(l == 0.f) ? 0.f : m_ref, l);
+      if (active && writes) {
+        if (a.lse != nullptr) a.lse[at] = has ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        if (a.causal && s.many && has && !(odd == 0.f && l < INFINITY)) {
+          const int er = s.row0 + r;
+          a.odd[atomicAdd(a.meta + 1, 1)] = (s.tau + er / G) * a.num_qo_heads + s.h * G + er % G;
+        }
+      } else if (active) {
+        a.part_ml[at] = make_float2(m_ref == -INFINITY && !(l == 0.f) ? 0.f : m_ref, l);
+      }
     }
   }
 
@@ -825,7 +864,7 @@ cudaError_t launch_t(const PrefixArgs& a, cudaStream_t s) {
   if (smem > (size_t)optin) smem = (size_t)optin;
   const cudaError_t e = set_smem_limit((const void*)prefix_big_kernel<FP8, F16>, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(prefix_big_kernel<FP8, F16>, dim3(a.big_grid), Roles<FP8>::kThreads, smem, s, a);
+  return launch_dependent(prefix_big_kernel<FP8, F16>, dim3(a.grid), Roles<FP8>::kThreads, smem, s, a);
 }
 
 }  // namespace

@@ -1,6 +1,8 @@
-// The work of the attention over shared prefixes, as its kernels walk it: two
-// lines of units' blocks, each cut into ranges, one per CTA.
+// The work of the attention over shared prefixes, as its kernels walk it: a line
+// of units' blocks, cut into ranges, one per CTA.
 #pragma once
+
+#include <math.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -9,20 +11,20 @@
 namespace msa {
 
 // Costs: a block, and what a unit takes besides its blocks (its Q, its
-// epilogue, the change of units). Line 0 counts in halves of a block of 16
-// rows, line 1 in quarters of a block of two tiles of 128.
-MSA_DEV int block_cost(int line, int rows) { return line == 0 ? 2 : rows > 128 ? 4 : 3; }
-MSA_DEV int unit_cost(int line) { return line == 0 ? kSmallUnitCost : kBigUnitCost; }
-MSA_DEV int tile_rows_of(int line) { return line == 0 ? kSmallRows : kBigRows; }
+// epilogue, the change of units), in halves of a block of 16 rows, or in
+// quarters of a block of two tiles of 128.
+MSA_DEV int block_cost(const PrefixArgs& a, int rows) { return a.small ? 2 : rows > 128 ? 4 : 3; }
+MSA_DEV int unit_cost(const PrefixArgs& a) { return a.small ? kSmallUnitCost : kBigUnitCost; }
+MSA_DEV int tile_rows_of(const PrefixArgs& a) { return a.small ? kSmallRows : kBigRows; }
 // Where block j of a unit lies on the line, from the unit's beginning: what the
 // unit takes besides counts with its first block.
-MSA_DEV int block_at(int line, int cost, int j) { return j == 0 ? 0 : unit_cost(line) + j * cost; }
+MSA_DEV int block_at(const PrefixArgs& a, int cost, int j) { return j == 0 ? 0 : unit_cost(a) + j * cost; }
 // The first block that lies at or after `in`.
-MSA_DEV int block_from(int line, int cost, int in) {
-  return in <= 0 ? 0 : max(1, (in - unit_cost(line) + cost - 1) / cost);
+MSA_DEV int block_from(const PrefixArgs& a, int cost, int in) {
+  return in <= 0 ? 0 : max(1, (in - unit_cost(a) + cost - 1) / cost);
 }
 
-// The partition of a line's [0, total) into the CTAs' ranges. A range is never
+// The partition of the line's [0, total) into the CTAs' ranges. A range is never
 // shorter than a unit's first block, so each CTA between those of a unit's first
 // and last block holds one of its blocks.
 struct Ranges {
@@ -32,13 +34,10 @@ struct Ranges {
   // The range that position p < total is in: the last i with start(i) <= p.
   MSA_DEV int holder(long long p) const { return (int)((p * n + n - 1) / total); }
 };
-MSA_DEV const long long* starts_of(const PrefixArgs& a, int line) { return a.start + line * (2 * a.batch + 1); }
-MSA_DEV const int4* work_of(const PrefixArgs& a, int line) { return a.work + line * 4 * a.batch; }
-MSA_DEV Ranges ranges_of(const PrefixArgs& a, int line) {
-  const long long total = __ldcg(starts_of(a, line) + __ldcg(a.meta + 1 + line));
-  const long long most = total / (line ? kBigRange : kSmallRange);
-  const int grid = line ? a.big_grid : a.small_grid;
-  return {total, (int)(most < 1 ? 1 : most < grid ? most : grid)};
+MSA_DEV Ranges ranges_of(const PrefixArgs& a, int entries) {
+  const long long total = __ldcg(a.start + entries);
+  const long long most = total / (a.small ? kSmallRange : kBigRange);
+  return {total, (int)(most < 1 ? 1 : most < a.grid ? most : a.grid)};
 }
 // The last of n ascending numbers, the first of them at most `at`, that is at
 // most `at`; by a whole warp.
@@ -67,7 +66,7 @@ struct Piece {
   int place;       // of row 0's parts: its own, or (below 0) the CTA's
   int keys;        // keys from j0 on that some row sees
   int e, tile_head;  // the unit: entry, tile * heads + head
-  int group;       // whose run comes before this entry's own; -1: none
+  int alone;       // a request's own run, without a group's before it
   int many;        // the entry has rows of more than one token
 };
 
@@ -75,30 +74,29 @@ struct Piece {
 // next entry is read while this one's units are handed out.
 struct Walk {
   const PrefixArgs& a;
-  int line, list;
+  int list;
   long long at, end, unit_at;
   int e, tile, h, len, cost, tiles;
   int4 x, y, nx, ny;
   MSA_DEV void ahead() {
-    const int4* w = work_of(a, line) + 2 * min(e + 1, list - 1);
+    const int4* w = a.work + 2 * min(e + 1, list - 1);
     nx = __ldcg(w), ny = __ldcg(w + 1);
   }
   MSA_DEV void open() {
-    cost = block_cost(line, x.y);
-    len = unit_cost(line) + y.x * cost;
-    tiles = (x.y + tile_rows_of(line) - 1) / tile_rows_of(line);
+    cost = block_cost(a, x.y);
+    len = unit_cost(a) + y.x * cost;
+    tiles = (x.y + tile_rows_of(a) - 1) / tile_rows_of(a);
   }
-  MSA_DEV Walk(const PrefixArgs& args, int l, const Ranges& r, int cta)
-      : a(args), line(l), list(__ldcg(args.meta + 1 + l)), at(0), end(0) {
+  MSA_DEV Walk(const PrefixArgs& args, int cta) : a(args), list(__ldcg(args.meta)), at(0), end(0) {
+    const Ranges r = ranges_of(a, list);
     if (r.total <= 0 || cta >= r.n) return;
     at = r.start(cta), end = r.start(cta + 1);
-    const long long* start = starts_of(a, line);
-    e = last_upto(start, list, at);
-    const int4* w = work_of(a, line) + 2 * e;
+    e = last_upto(a.start, list, at);
+    const int4* w = a.work + 2 * e;
     x = __ldcg(w), y = __ldcg(w + 1);
     open();
     ahead();
-    const long long first = __ldcg(start + e);
+    const long long first = __ldcg(a.start + e);
     const int unit = (int)((at - first) / len);
     unit_at = first + (long long)unit * len;
     tile = unit / a.num_kv_heads;
@@ -112,20 +110,20 @@ struct Walk {
   MSA_DEV void step(Piece& p) {
     const int in = (int)(at - unit_at);
     const bool ends = unit_at + len <= end;  // within the range
-    const int j0 = block_from(line, cost, in), j1 = ends ? y.x : min(y.x, block_from(line, cost, (int)(end - unit_at)));
+    const int j0 = block_from(a, cost, in), j1 = ends ? y.x : min(y.x, block_from(a, cost, (int)(end - unit_at)));
     if (j1 > j0 || in == 0) {
       const int G = a.num_qo_heads / a.num_kv_heads;
       p.n = j1 - j0;
       p.whole = j0 == 0 && j1 == y.x;
       p.b = x.z, p.h = h, p.j0 = (x.w & ~kGroupRun) + j0;
-      p.row0 = tile * tile_rows_of(line), p.rows = min(tile_rows_of(line), x.y - p.row0);
+      p.row0 = tile * tile_rows_of(a), p.rows = min(tile_rows_of(a), x.y - p.row0);
       p.tau = x.x;
       p.hidden = y.y, p.lk = y.z;
       p.place = j0 == 0 ? ((x.w & kGroupRun) ? a.total_q : 0) + x.x : -1;
       const long long last = min((long long)y.z, (long long)y.y + (p.row0 + p.rows - 1) / G + 1) - (long long)p.j0 * kBlk;
       p.keys = (int)max(0ll, min(last, (long long)p.n * kBlk));
       p.e = e, p.tile_head = tile * a.num_kv_heads + h;
-      p.group = y.w;
+      p.alone = y.w < 0 && !(x.w & kGroupRun);
       p.many = x.y > G;
     }
     at = ends ? unit_at + len : end;
@@ -149,15 +147,12 @@ struct Walk {
 struct Parts {
   int c0, n;
 };
-// Of a unit (entry e of a line with these blocks and rows).
-MSA_DEV Parts parts_of(const PrefixArgs& a, int line, const Ranges& r, int e, int rows, int blocks, int tile_head) {
-  const int cost = block_cost(line, rows), len = unit_cost(line) + blocks * cost;
-  const long long at = __ldcg(starts_of(a, line) + e) + (long long)tile_head * len;
-  const int c0 = r.holder(at), c1 = blocks > 1 ? r.holder(at + block_at(line, cost, blocks - 1)) : c0;
+// Of a unit of entry e, which has these rows and blocks.
+MSA_DEV Parts parts_of(const PrefixArgs& a, const Ranges& r, int e, int rows, int blocks, int tile_head) {
+  const int cost = block_cost(a, rows), len = unit_cost(a) + blocks * cost;
+  const long long at = __ldcg(a.start + e) + (long long)tile_head * len;
+  const int c0 = r.holder(at), c1 = blocks > 1 ? r.holder(at + block_at(a, cost, blocks - 1)) : c0;
   return {c0, c1 - c0};
-}
-MSA_DEV size_t cta_parts(const PrefixArgs& a, int line) {
-  return a.part_rows + (line ? (size_t)a.small_grid * kSmallRows : 0);
 }
 
 // The parts of a group's run that rows of one of its requests join: of up to 16
@@ -169,18 +164,18 @@ struct Before {
   Parts parts[2];  // of this tile and the next
 };
 // By a whole warp.
-MSA_DEV Before before_of(const PrefixArgs& a, const Ranges& big, int group, int tau, int row0, int rows, int h) {
+MSA_DEV Before before_of(const PrefixArgs& a, const Ranges& ranges, int group, int tau, int row0, int rows, int h) {
   Before f{};
-  const int code = group < 0 ? -1 : __ldcg(a.group + group);
-  if (code < 0) return f;
-  const int4* w = work_of(a, 1) + 2 * code;
+  const int e = group < 0 ? -1 : __ldcg(a.group + group), tile_rows = tile_rows_of(a);
+  if (e < 0) return f;
+  const int4* w = a.work + 2 * e;
   const int4 x = __ldcg(w);
   const int blocks = __ldcg(&w[1].x), G = a.num_qo_heads / a.num_kv_heads;
   f.on = 1;
   f.row0 = (tau - x.x) * G + row0;
-  f.tile = f.row0 / kBigRows;
-  const int lane = threadIdx.x & 31, last = (f.row0 + rows - 1) / kBigRows;
-  const Parts mine = parts_of(a, 1, big, code, x.y, blocks, min(f.tile + (lane & 1), last) * a.num_kv_heads + h);
+  f.tile = f.row0 / tile_rows;
+  const int lane = threadIdx.x & 31, last = (f.row0 + rows - 1) / tile_rows;
+  const Parts mine = parts_of(a, ranges, e, x.y, blocks, min(f.tile + (lane & 1), last) * a.num_kv_heads + h);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
     f.parts[i] = {__shfl_sync(0xffffffffu, mine.c0, i), __shfl_sync(0xffffffffu, mine.n, i)};
@@ -198,16 +193,16 @@ struct Joined {
 #pragma unroll
     for (int c = 0; c < 8; ++c) o[c] = fmaf(p, v[c], o[c] * f);
   }
-  // Those at `first`, then those of the CTAs; loads of four at a time.
-  MSA_DEV void add_parts(const PrefixArgs& a, size_t first, size_t ctas, int tile_rows, int row, Parts parts, int col) {
-    constexpr int kAhead = 4;
+  // Those at `first`, then those of the CTAs; loads of AHEAD at a time.
+  template <int kAhead>
+  MSA_DEV void add_some(const PrefixArgs& a, size_t first, int row, Parts parts, int col) {
     for (int i0 = 0; i0 <= parts.n; i0 += kAhead) {
       float2 ml[kAhead];
       float4 v[kAhead][2];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int i = min(i0 + u, parts.n);
-        const size_t at = i == 0 ? first : ctas + (size_t)(parts.c0 + i) * tile_rows + row;
+        const size_t at = i == 0 ? first : a.part_rows + (size_t)(parts.c0 + i) * tile_rows_of(a) + row;
         ml[u] = __ldcg(a.part_ml + at);
         const float4* from = reinterpret_cast<const float4*>(a.part_o + at * kHeadDim + col);
         v[u][0] = __ldcg(from), v[u][1] = __ldcg(from + 1);
@@ -220,11 +215,16 @@ struct Joined {
       }
     }
   }
+  // Row `row` of its tile.
+  MSA_DEV void add_parts(const PrefixArgs& a, size_t first, int row, Parts parts, int col) {
+    if (parts.n < 2) add_some<2>(a, first, row, parts, col);
+    else add_some<8>(a, first, row, parts, col);
+  }
   MSA_DEV void add_before(const PrefixArgs& a, const Before& f, int r, size_t own_row, int col) {
     if (!f.on) return;
-    const int row = f.row0 + r, tile = row / kBigRows;
-    add_parts(a, (size_t)a.total_q * a.num_qo_heads + own_row, cta_parts(a, 1), kBigRows, row - tile * kBigRows,
-              f.parts[tile - f.tile], col);
+    const int row = f.row0 + r, tile = row / tile_rows_of(a), second = tile - f.tile;
+    add_parts(a, (size_t)a.total_q * a.num_qo_heads + own_row, row - tile * tile_rows_of(a),
+              Parts{second ? f.parts[1].c0 : f.parts[0].c0, second ? f.parts[1].n : f.parts[0].n}, col);
   }
   MSA_DEV bool finite() const {
     float x = 0.f;
