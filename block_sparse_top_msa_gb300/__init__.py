@@ -132,7 +132,7 @@ def lib():
         L.msa_sample.restype = i32
         L.msa_sample.argtypes = [vp, i32, i64, i32, i32] + [vp] * 8 + [sz, vp]
         L.msa_sample_workspace_size.restype = sz
-        L.msa_sample_workspace_size.argtypes = [i32, i32]
+        L.msa_sample_workspace_size.argtypes = [i32] * 3
         L.msa_draft_path.restype = i32
         L.msa_draft_path.argtypes = [vp, vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, vp]
         L.msa_proxy_score.restype = i32

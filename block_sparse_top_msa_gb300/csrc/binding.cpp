@@ -659,9 +659,10 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Tensor logprobs;
   if (a[8] != Py_None || as_flag(a[6])) logprobs = output("logprobs", a[8], dev, at::kFloat, Shape{rows});
   const int count = size32("logits", rows), width = size32("logits", vocab);
-  const Tensor ws = workspace(a[9], dev, msa_sample_workspace_size(count, width));
+  const msa_dtype_t dtype = x.scalar_type() == at::kFloat ? MSA_FP32 : code(x.scalar_type());
+  const Tensor ws = workspace(a[9], dev, msa_sample_workspace_size(count, width, dtype));
   check("msa_sample",
-        msa_sample(x.data_ptr(), x.scalar_type() == at::kFloat ? MSA_FP32 : code(x.scalar_type()),
+        msa_sample(x.data_ptr(), dtype,
                    rows > 1 ? x.stride(0) : vocab, count, width, ptr<const float>(u), t, k, p, m, ptr<int32_t>(tokens),
                    logprobs.defined() ? ptr<float>(logprobs) : nullptr, ws.data_ptr(), (size_t)ws.numel(),
                    place.stream()));

@@ -213,13 +213,14 @@ struct PrefixArgs {
   float* lse = nullptr;
   int small = 0;  // units of kSmallRows rows (no groups then), else of kBigRows
   int grid = 0;   // CTAs
+  int chunk_rows = 0;  // of the join's chunks: a multiple of 16 that divides kBigRows
   // Workspace. Positions: the requests in the order of the groups. Entries: the
   // positions' own runs, then the groups', those that there are.
   int4* entry = nullptr;       // (batch, 2): first token in that order, tokens, request, group; first row of q, Lk - Lq, Lk, entry or -1
   int* group = nullptr;        // (batch): a group's entry or -1
   int4* work = nullptr;        // (2 batch, 2): first token, rows, page row, first block (| kGroupRun); blocks, keys that all rows see, Lk, group before or -1
   long long* start = nullptr;  // (2 batch + 1): running sums of the entries' costs
-  int* chunk = nullptr;        // (2 batch + 1): running count of what the join does for entries with a group before: 16 rows of one KV head each
+  int* chunk = nullptr;        // (2 batch + 1): running count of what the join does for entries with a group before: chunk_rows rows of one KV head each
   int2* token = nullptr;       // (total_q): each token's row of q, and its position
   int* meta = nullptr;         // entries, odd rows
   int4* cut = nullptr;         // (grid): the unit without a group before that begins in the CTA's range and goes on after it: entry, tile and head; entry -1: none
@@ -468,7 +469,6 @@ cudaError_t launch_draft_path(const DraftPathArgs& a, cudaStream_t s);
 // Tokens from logits (sample.cu).
 constexpr int kMaxVocab = 1 << 19;
 constexpr int kSampleParts = 513;  // of a row's histogram
-constexpr int kSampleList = 256;   // tokens listed of each slice
 struct SampleArgs {
   const void* logits = nullptr;  // (rows, vocab), `stride` values from row to row
   long long stride = 0;
@@ -486,13 +486,14 @@ struct SampleArgs {
   unsigned long long* best = nullptr;    // (rows, slices)
   uint32_t* parts_count = nullptr;       // (rows, kSampleParts)
   unsigned long long* parts_mass = nullptr;
-  uint2* list = nullptr;                 // (rows, slices, kSampleList)
+  int listed = 0;                        // tokens of a slice that its list holds
+  uint2* list = nullptr;                 // (rows, slices, listed)
   int2* list_info = nullptr;             // (rows, slices): tokens listed, parts they are of
 };
 struct SampleSlices {
-  int slice, slices;
+  int slice, slices, listed;
 };
-SampleSlices sample_slices(int rows, int vocab);
+SampleSlices sample_slices(int rows, int vocab, bool wide);
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
 
 }  // namespace msa

@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     Sums mine{};
     if (there) {
       mine.cost = (long long)((x.y + tile - 1) / tile) * a.num_kv_heads * (unit_cost(a) + (long long)y.x * block_cost(a, x.y));
-      mine.counts = 1 + (joined ? (long long)((x.y + 15) / 16) * a.num_kv_heads << 32 : 0);
+      mine.counts = 1 + (joined ? (long long)((x.y + a.chunk_rows - 1) / a.chunk_rows) * a.num_kv_heads << 32 : 0);
     }
     Sums all;
     const Sums upto = block_sums(mine, s_sums, all);
@@ -745,55 +745,58 @@ __device__ __noinline__ void odd_row(const PrefixArgs& a, const Ranges& ranges, 
   if (lane < 16) all.write(a, orow, col);
 }
 
-// Joins what is left, 16 rows at a time: of the requests with a group's run
-// before their own, and of the other units that ranges cut. Each warp of a
-// block finds the parts for itself and has two of the rows, 16 lanes each, of
-// eight columns: first the parts of the group's run, then those of the own one,
-// in the order of the pieces.
+// Joins what is left: of the requests with a group's run before their own, and
+// of the other units that ranges cut. A block takes chunk_rows rows of one KV
+// head at a time; each of its warps finds their parts for itself (ten loads one
+// after the other: what a chunk of 16 rows mostly takes) and has two of each 16
+// rows, 16 lanes each, of eight columns: first the parts of the group's run,
+// then those of the own one, in the order of the pieces.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
     prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.num_qo_heads / a.num_kv_heads;
-  const int warps = gridDim.x * (kJoinThreads / 32), per_cut = tile_rows_of(a) / 16, cuts = a.grid * per_cut;
+  const int warps = gridDim.x * (kJoinThreads / 32);
   grid_dependency_wait();
   grid_dependents_launch();
   const int entries = __ldcg(a.meta), odd = __ldcg(a.meta + 1);
   const Ranges ranges = ranges_of(a, entries);
   for (int i = warp * gridDim.x + blockIdx.x; i < odd; i += warps) odd_row(a, ranges, __ldcg(a.odd + i), lane);
   const int chunks = __ldcg(a.chunk + entries);
-  for (int i = blockIdx.x; i < cuts + chunks; i += gridDim.x) {
-    int e, tile_head, row0;
-    if (i < cuts) {
-      const int4 cut = __ldcg(a.cut + i / per_cut);
+  for (int i = blockIdx.x; i < a.grid + chunks; i += gridDim.x) {
+    int e, tile_head, row0, many;
+    if (i < a.grid) {
+      const int4 cut = __ldcg(a.cut + i);
       e = cut.x, tile_head = cut.y;
-      row0 = tile_head / a.num_kv_heads * tile_rows_of(a) + i % per_cut * 16;
       if (e < 0) continue;
+      row0 = tile_head / a.num_kv_heads * tile_rows_of(a), many = tile_rows_of(a);
     } else {
-      e = last_upto(a.chunk, entries, i - cuts);
-      const int c = i - cuts - __ldcg(a.chunk + e), r = c / a.num_kv_heads;
-      row0 = r * 16;
+      e = last_upto(a.chunk, entries, i - a.grid);
+      const int c = i - a.grid - __ldcg(a.chunk + e), r = c / a.num_kv_heads;
+      row0 = r * a.chunk_rows, many = a.chunk_rows;
       tile_head = row0 / tile_rows_of(a) * a.num_kv_heads + c - r * a.num_kv_heads;
     }
     const int4* w = a.work + 2 * e;
     const int4 x = __ldcg(w), y = __ldcg(w + 1);
-    if (row0 >= x.y) continue;
-    const int h = tile_head % a.num_kv_heads, rows = min(16, x.y - row0), col = (lane & 15) * 8;
+    const int h = tile_head % a.num_kv_heads, rows = min(many, x.y - row0), col = (lane & 15) * 8;
     const Parts parts = parts_of(a, ranges, e, x.y, y.x, tile_head);
     const Before f = before_of(a, ranges, y.w, x.x, row0, rows, h);
-    const int r = 2 * warp + (lane >> 4), er = row0 + r;
-    const size_t hq = (size_t)h * G + er % G, own_row = (size_t)(x.x + er / G) * a.num_qo_heads + hq;
-    bool bad = false;
-    if (r < rows) {
-      const int token = __ldcg(&a.token[x.x + er / G].x);
-      Joined all;
-      all.add_before(a, f, r, own_row, col);
-      all.add_parts(a, own_row, er % tile_rows_of(a), parts, col);
-      bad = a.causal && x.y > G && !all.finite();
-      all.write(a, (size_t)token * a.num_qo_heads + hq, col);
+#pragma unroll 1
+    for (int r0 = 2 * warp; r0 < rows; r0 += kJoinThreads / 16) {
+      const int r = r0 + (lane >> 4), er = row0 + r;
+      const size_t hq = (size_t)h * G + er % G, own_row = (size_t)(x.x + er / G) * a.num_qo_heads + hq;
+      bool bad = false;
+      if (r < rows) {
+        const int token = __ldcg(&a.token[x.x + er / G].x);
+        Joined all;
+        all.add_before(a, f, r, own_row, col);
+        all.add_parts(a, own_row, er % tile_rows_of(a), parts, col);
+        bad = a.causal && x.y > G && !all.finite();
+        all.write(a, (size_t)token * a.num_qo_heads + hq, col);
+      }
+      const unsigned bads = __ballot_sync(0xffffffffu, bad);
+      for (int k = 0; k < 2; ++k)
+        if ((bads >> (16 * k)) & 0xffffu) odd_row(a, ranges, (int)__shfl_sync(0xffffffffu, (unsigned)own_row, 16 * k), lane);
     }
-    const unsigned bads = __ballot_sync(0xffffffffu, bad);
-    for (int k = 0; k < 2; ++k)
-      if ((bads >> (16 * k)) & 0xffffu) odd_row(a, ranges, (int)__shfl_sync(0xffffffffu, (unsigned)own_row, 16 * k), lane);
   }
 }
 
@@ -817,8 +820,8 @@ cudaError_t launch_prefix(const PrefixArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   // Cut units, and as many chunks as there can be: a block each, up to eight an
   // SM.
-  const long long chunks = ((long long)a.total_q * a.num_qo_heads + 15) / 16 + (long long)a.batch * a.num_kv_heads;
-  const long long items = (long long)a.grid * (a.small ? 1 : kBigRows / 16) + (a.group_rows != nullptr ? chunks : 0);
+  const long long chunks = ((long long)a.total_q * a.num_qo_heads + a.chunk_rows - 1) / a.chunk_rows + (long long)a.batch * a.num_kv_heads;
+  const long long items = a.grid + (a.group_rows != nullptr ? chunks : 0);
   const long long blocks = items < 8 * a.grid ? items : 8 * a.grid;
   return launch_dependent(prefix_join_kernel, dim3((unsigned)blocks), kJoinThreads, 0, s, a);
 }

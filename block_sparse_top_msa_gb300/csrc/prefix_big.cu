@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           const int x_end = dual ? 4 : 2;
 #pragma unroll 1
           for (int x = 0; ok && x < x_end; ++x) {
-            const int st = dual ? x & 1 : t & 1, h = dual ? x >> 1 : x;
+            const int st = dual ? x >> 1 : t & 1, h = x & 1;
             wait(&sm.p_full[st][h], (p_phase >> st) & 1u, kFaultWaitSoftmax);
             if (!ok) break;
             tc_fence_after();

@@ -155,8 +155,8 @@ MSA_DEV Parts parts_of(const PrefixArgs& a, const Ranges& r, int e, int rows, in
   return {c0, c1 - c0};
 }
 
-// The parts of a group's run that rows of one of its requests join: of up to 16
-// rows side by side, which lie in one of its tiles or two.
+// The parts of a group's run that rows of one of its requests join: of no more
+// rows side by side than a tile has, which lie in one of its tiles or two.
 struct Before {
   int on;        // the request has a group's run before its own
   int row0;      // of the group's entry: its row of row 0

@@ -19,10 +19,11 @@
 // thread adds first.
 //
 // Three kernels, each launched under the tail of the one before: the largest
-// of each slice of a row; the slices' histograms, added up in the row's, and
-// of each slice its first tokens as a list; and a block a row that answers.
-// It reads the lists where they hold the part that it looks into, else the
-// row again.
+// of each slice of a row; the slices' histograms, added up in the row's; and a
+// block a row that answers. In 16 bits there are few logits: a slice counts how
+// often each of the 65536 comes, one addition a token, and weighs those that
+// come. In 32 bits each token is weighed, and the slice lists its first tokens
+// for the last kernel, which reads the row again for what the lists do not hold.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -36,6 +37,7 @@ using u64 = unsigned long long;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kOctaveBins = 32, kBins = kSampleParts - 1;  // of the first 16 octaves below the maximum; then one for the rest
+constexpr int kCountThreads = 1024;
 constexpr int kOrderCap = 256;       // tokens that are ordered at once
 constexpr float kNoWeight = -45.5f;  // 2^y below half of 2^-44
 constexpr u64 kOne = 1ull << 44;
@@ -80,7 +82,7 @@ struct __align__(16) Mark {
 struct Histogram {
   uint32_t cnt[kBins + 1], lo[kBins + 1], hi[kBins + 1];
   MSA_DEV void clear() {
-    for (int i = threadIdx.x; i <= kBins; i += kThreads) cnt[i] = lo[i] = hi[i] = 0u;
+    for (int i = threadIdx.x; i <= kBins; i += blockDim.x) cnt[i] = lo[i] = hi[i] = 0u;
     __syncthreads();
   }
   MSA_DEV void add(int part, u64 w, uint32_t n = 1u) {
@@ -90,6 +92,15 @@ struct Histogram {
     if (high) atomicAdd(&hi[part], high);
   }
   MSA_DEV Mark at(int part) const { return {cnt[part], ((u64)hi[part] << 32) + lo[part]}; }
+  // To the row's.
+  MSA_DEV void flush(const SampleArgs& a, int row) const {
+    for (int i = threadIdx.x; i <= kBins; i += blockDim.x) {
+      const Mark m = at(i);
+      if (m.count == 0) continue;
+      atomicAdd(a.parts_count + (size_t)row * kSampleParts + i, (uint32_t)m.count);
+      atomicAdd(a.parts_mass + (size_t)row * kSampleParts + i, m.mass);
+    }
+  }
 };
 
 MSA_DEV uint32_t key_of(float f) {
@@ -103,12 +114,15 @@ MSA_DEV float value_of(uint32_t key) { return __uint_as_float(key ^ ((key >> 31)
 struct Scale {
   float m, ch, cl;
   bool at_inf;  // the maximum is infinite: those tokens share all mass
-  // About log2 of w; what the histogram's part goes by. Never rises as f falls.
-  MSA_DEV float log2w(float f) const { return at_inf ? (f == m ? 0.f : -INFINITY) : (f - m) * ch; }
-  MSA_DEV int part(float f) const {
-    const float y = log2w(f);
-    return y > -(float)(kBins / kOctaveBins) ? (int)(y * -(float)kOctaveBins) : kBins;
+  // 1024 times log2 of w, rounded; never rises as f falls. f is not NaN; `far`
+  // at least where the weight is 0.
+  static constexpr int kFar = 1 << 20;
+  MSA_DEV int steps(float f) const {
+    const float y = fmaxf((f - m) * ch, -1000.f);
+    return at_inf ? (f == m ? 0 : -kFar) : __float_as_int(fmaf(y, 1024.f, 12582912.f)) - 0x4b400000;
   }
+  // What part of the histogram it is in.
+  MSA_DEV int part(float f) const { return min(-steps(f) >> 5, kBins); }
   // w in 2^-44. x - m and its product with log2(e) / T in two floats each, so
   // that what is left for the cubic is exact to 2^-36.
   MSA_DEV u64 weight(const u64* table, float f) const {
@@ -150,12 +164,13 @@ struct Values {
     return begin - (int)((reinterpret_cast<uintptr_t>(row + (size_t)begin * kSize) & 15) / kSize);
   }
   MSA_DEV int groups() const { return (end - first() + kGroup - 1) / kGroup; }
-  // Calls f(value, token) for the values of group g, tokens ascending.
+  MSA_DEV bool inside(int at) const { return at >= begin && at + kGroup <= end; }
+  MSA_DEV uint4 load(int at) const { return __ldg(reinterpret_cast<const uint4*>(row + (long long)at * kSize)); }
+  // Calls f(value, token) for the values from `at` on, which are of one group:
+  // those in v, where all of them are there.
   template <class F>
-  MSA_DEV void group(int g, F f) const {
-    const int at = first() + g * kGroup;
-    if (at >= begin && at + kGroup <= end) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + (long long)at * kSize));
+  MSA_DEV void group(int at, const uint4& v, F f) const {
+    if (inside(at)) {
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int j = 0; j < kGroup; ++j) f(element(w, j), at + j);
@@ -165,11 +180,26 @@ struct Values {
         if (at + j >= begin && at + j < end) f(value(row + (long long)(at + j) * kSize), at + j);
     }
   }
-  // Of a thread's groups, ascending.
+  // Groups g0, g0 + step, ... below n, four loads at a time; tokens ascend.
+  template <class F>
+  MSA_DEV void steps(int g0, int n, int step, F f) const {
+    const int at0 = first();
+    for (int g = g0; g < n; g += 4 * step) {
+      uint4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int at = at0 + (g + u * step) * kGroup;
+        v[u] = g + u * step < n && inside(at) ? load(at) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (g + u * step < n) group(at0 + (g + u * step) * kGroup, v[u], f);
+    }
+  }
+  // Of a thread's groups.
   template <class F>
   MSA_DEV void each(F f) const {
-    const int n = groups();
-    for (int g = threadIdx.x; g < n; g += kThreads) group(g, f);
+    steps(threadIdx.x, groups(), blockDim.x, f);
   }
 };
 
@@ -262,10 +292,9 @@ __global__ void __launch_bounds__(kThreads) sample_top_kernel(const __grid_const
   if (threadIdx.x == 0) a.best[(size_t)row * a.slices + slice] = m.count;
 }
 
-// A slice's histogram, and the list of the tokens in its first parts: as many
-// parts as kSampleList tokens fill.
-template <int TYPE>
-__global__ void __launch_bounds__(kThreads, 2) sample_parts_kernel(const __grid_constant__ SampleArgs a) {
+// A slice's histogram, of 32-bit logits, and the list of the tokens in its first
+// parts: as many parts as fill its share of the row's list.
+__global__ void __launch_bounds__(kThreads, 2) sample_weigh_kernel(const __grid_constant__ SampleArgs a) {
   __shared__ u64 table[1024];
   __shared__ Histogram h;
   __shared__ int s_upto[kWarps];
@@ -280,11 +309,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_parts_kernel(const __grid_
   const Settings s = settings_of(a, row);
   if (s.none || (s.one && a.logprobs == nullptr)) return;
   const int begin = slice * a.slice;
-  const Values<TYPE> v{row_of<TYPE>(a, row), begin, min(begin + a.slice, a.vocab)};
+  const Values<2> v{row_of<2>(a, row), begin, min(begin + a.slice, a.vocab)};
   u64 rest_mass = 0;
   uint32_t rest_count = 0;
   v.each([&](float f, int) {
-    if (key_of(f) <= kKeyNegInf) {
+    if (!(f > -INFINITY)) {
       ++rest_count;
       return;
     }
@@ -296,12 +325,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_parts_kernel(const __grid_
   rest_mass = warp_add(rest_mass), rest_count = warp_add(rest_count);
   if (lane == 0 && rest_count > 0) h.add(kBins, rest_mass, rest_count);
   __syncthreads();
-  for (int i = tid; i <= kBins; i += kThreads) {
-    const Mark m = h.at(i);
-    if (m.count == 0) continue;
-    atomicAdd(a.parts_count + (size_t)row * kSampleParts + i, (uint32_t)m.count);
-    atomicAdd(a.parts_mass + (size_t)row * kSampleParts + i, m.mass);
-  }
+  h.flush(a, row);
   if (s.one) return;
   // Where the running count passes what the list holds.
   int upto = (int)h.cnt[tid];
@@ -313,16 +337,86 @@ __global__ void __launch_bounds__(kThreads, 2) sample_parts_kernel(const __grid_
   if (lane == 31) s_upto[warp] = upto;
   __syncthreads();
   for (int w = 0; w < warp; ++w) upto += s_upto[w];
-  const int parts = __syncthreads_count(upto <= kSampleList);
-  uint2* list = a.list + ((size_t)row * a.slices + slice) * kSampleList;
+  const int parts = __syncthreads_count(upto <= a.listed);
+  uint2* list = a.list + ((size_t)row * a.slices + slice) * a.listed;
   v.each([&](float f, int i) {
-    const uint32_t key = key_of(f);
-    if (key <= kKeyNegInf || s.scale.part(f) >= parts) return;
+    if (!(f > -INFINITY) || s.scale.part(f) >= parts) return;
     const uint32_t n = atomicAdd(&s_n, 1u);
-    if (n < kSampleList) list[n] = make_uint2(key, (uint32_t)i);
+    if (n < (uint32_t)a.listed) list[n] = make_uint2(key_of(f), (uint32_t)i);
   });
   __syncthreads();
-  if (tid == 0) a.list_info[(size_t)row * a.slices + slice] = make_int2((int)min(s_n, (uint32_t)kSampleList), parts);
+  if (tid == 0) a.list_info[(size_t)row * a.slices + slice] = make_int2((int)min(s_n, (uint32_t)a.listed), parts);
+}
+
+// A slice's histogram, of 16-bit logits: how often each comes, two counters to a
+// word (a slice has fewer than 65536), then the weight of each that comes.
+template <int TYPE>
+__global__ void __launch_bounds__(kCountThreads, 1) sample_count_kernel(const __grid_constant__ SampleArgs a) {
+  extern __shared__ uint4 counts[];  // 65536 times 16 bits
+  __shared__ u64 table[1024];
+  __shared__ Histogram h;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int slice = blockIdx.x % a.slices, row = blockIdx.x / a.slices;
+  uint32_t* words = reinterpret_cast<uint32_t*>(counts);
+  for (int i = tid; i < 8192; i += kCountThreads) counts[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = tid; i < 1024; i += kCountThreads) table[i] = kPowers.at[i];
+  h.clear();
+  grid_dependency_wait();
+  grid_dependents_launch();
+  const Settings s = settings_of(a, row);
+  if (s.none || (s.one && a.logprobs == nullptr)) return;
+  const int begin = slice * a.slice, end = min(begin + a.slice, a.vocab);
+  const Values<TYPE> v{row_of<TYPE>(a, row), begin, end};
+  auto count = [&](uint32_t bits) { atomicAdd(words + (bits >> 1), (bits & 1u) ? 65536u : 1u); };
+  const int n = v.groups(), at0 = v.first();
+  for (int g = tid; g < n; g += 4 * kCountThreads) {
+    uint4 x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = g + u * kCountThreads, at = at0 + k * 8;
+      x[u] = k < n && v.inside(at) ? v.load(at) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = g + u * kCountThreads, at = at0 + k * 8;
+      if (k >= n) break;
+      if (v.inside(at)) {
+        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) count(w[j] & 0xffffu), count(w[j] >> 16);
+      } else {
+        for (int j = 0; j < 8; ++j)
+          if (at + j >= begin && at + j < end)
+            count(__ldg(reinterpret_cast<const unsigned short*>(v.row + (long long)(at + j) * 2)));
+      }
+    }
+  }
+  __syncthreads();
+  u64 rest_mass = 0;
+  uint32_t rest_count = 0;
+  for (int i = tid; i < 8192; i += kCountThreads) {
+    const uint4 c = counts[i];
+    if ((c.x | c.y | c.z | c.w) == 0u) continue;
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll 1
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t times = (w[j >> 1] >> (16 * (j & 1))) & 0xffffu, bits = 8u * i + j;
+      if (times == 0u) continue;
+      const float f = TYPE == 1 ? __half2float(__ushort_as_half((unsigned short)bits)) : __uint_as_float(bits << 16);
+      if (!(f > -INFINITY)) {
+        rest_count += times;
+        continue;
+      }
+      const u64 mass = s.scale.weight(table, f) * times;
+      const int part = s.scale.part(f);
+      if (part < kBins && !s.one) h.add(part, mass, times);
+      else rest_mass += mass, rest_count += times;
+    }
+  }
+  rest_mass = warp_add(rest_mass), rest_count = warp_add(rest_count);
+  if (lane == 0 && rest_count > 0) h.add(kBins, rest_mass, rest_count);
+  __syncthreads();
+  h.flush(a, row);
 }
 
 struct Shared {
@@ -349,37 +443,65 @@ struct Row {
   int row;
   Values<TYPE> values;
   const Scale& scale;
+  uint32_t top_key;
 
-  // The tokens of a part, wherever they are: f(value, key, token).
+  // The keys of the logits in a part: from the lowest whose part is not above it
+  // up to the last below the next part's.
+  MSA_DEV uint32_t lowest_key(int part) {
+    if (part >= kBins) return 0u;
+    uint32_t lo = kKeyNegInf, hi = top_key;  // the part of lo is above, that of hi is not
+    while (hi - lo > 1u) {
+      const uint32_t step = (hi - lo + kThreads - 1) / kThreads, at = lo + (threadIdx.x + 1) * step;
+      const int above = __syncthreads_count(at > lo && at < hi && scale.part(value_of(at)) > part);
+      lo += above * step;
+      hi = hi - lo > step ? lo + step : hi;
+    }
+    return hi;
+  }
+  struct Keys {
+    uint32_t lo, hi;
+  };
+  MSA_DEV Keys keys_of(int part) {
+    Keys k{lowest_key(part), part > 0 ? lowest_key(part - 1) - 1u : top_key};
+    // Of 16-bit logits, only those that there are: the low bits are all 0, below
+    // zero all 1.
+    if constexpr (TYPE != 2) {
+      constexpr uint32_t low = TYPE == 0 ? 0xffffu : 0x1fffu;
+      k.lo = k.lo >= 0x80000000u ? (k.lo + low) & ~low : k.lo | low;
+      if (k.hi >= 0x80000000u) k.hi &= ~low;
+      else if ((k.hi & low) != low) k.hi = k.hi > low ? (k.hi & ~low) - 1u : 0u;
+    }
+    return k;
+  }
+
+  // The tokens with these keys, which are of one part: f(value, key, token).
   template <class F>
-  MSA_DEV void tokens(int part, F f) const {
+  MSA_DEV void tokens(int part, Keys k, F f) const {
     if (part < sm.listed) {
       // Loads of four steps at a time; what stands behind a list's end is not looked at.
       constexpr int kAhead = 4;
-      const uint2* list = a.list + (size_t)row * a.slices * kSampleList;
+      const uint2* list = a.list + (size_t)row * a.slices * a.listed;
       const int2* info = a.list_info + (size_t)row * a.slices;
-      const int all = a.slices * kSampleList;
+      const int all = a.slices * a.listed;
       for (int i0 = threadIdx.x; i0 < all; i0 += kAhead * kThreads) {
         uint2 x[kAhead];
         int n[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
           const int i = i0 + u * kThreads;
-          n[u] = i < all ? __ldcg(&info[i / kSampleList].x) : 0;
+          n[u] = i < all ? __ldcg(&info[i / a.listed].x) : 0;
           x[u] = i < all ? __ldcg(list + i) : make_uint2(0u, 0u);
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-          if ((i0 + u * kThreads) % kSampleList >= n[u]) continue;
-          const float v = value_of(x[u].x);
-          if (scale.part(v) == part) f(v, x[u].x, (int)x[u].y);
+          if ((i0 + u * kThreads) % a.listed >= n[u] || x[u].x < k.lo || x[u].x > k.hi) continue;
+          f(value_of(x[u].x), x[u].x, (int)x[u].y);
         }
       }
     } else {
       values.each([&](float v, int i) {
         const uint32_t key = key_of(v);
-        const float x = value_of(key);
-        if (scale.part(x) == part) f(x, key, i);
+        if (key >= k.lo && key <= k.hi) f(value_of(key), key, i);
       });
     }
   }
@@ -415,15 +537,16 @@ struct Row {
     const int part = locate(sm.top, Mark{0, 0}, kind, t);
     Mark base = part > 0 ? sm.top[part - 1] : Mark{0, 0}, upto = sm.top[part];
     if (kind == kCount && upto.count == t) return {upto.count, upto.mass, 0u, 0};
-    uint32_t key_lo = 0u, key_hi = 0xffffffffu;
+    if (kind != kMassGt && upto.count - base.count == 1) return {upto.count, upto.mass, 0u, 0};
+    Keys k = keys_of(part);
     while (true) {
+      if (k.lo >= k.hi) return equals(kind, t, base, k.hi);
       const u64 many = upto.count - base.count;
       if (kind != kMassGt && many == 1) return {upto.count, upto.mass, 0u, 0};
       if (many <= kOrderCap) {
         if (threadIdx.x == 0) sm.order_n = 0u;
         __syncthreads();
-        tokens(part, [&](float, uint32_t key, int idx) {
-          if (key < key_lo || key > key_hi) return;
+        tokens(part, k, [&](float, uint32_t key, int idx) {
           const uint32_t n = atomicAdd(&sm.order_n, 1u);
           if (n < kOrderCap) sm.order_key[n] = key, sm.order_idx[n] = idx;
         });
@@ -431,30 +554,23 @@ struct Row {
         return order(kind, t, base);
       }
       // Too many: by their keys.
-      uint32_t least = 0u, most = 0u;  // ~key, key
-      tokens(part, [&](float, uint32_t key, int) {
-        if (key < key_lo || key > key_hi) return;
-        least = max(least, ~key);
-        most = max(most, key);
-      });
-      const Mark ends = block_join<true>(least, most, sm.warp);
-      key_lo = ~(uint32_t)ends.count, key_hi = (uint32_t)ends.mass;
-      if (key_lo == key_hi) return equals(kind, t, base, key_lo);
       int shift = 0;
-      while (((key_hi - key_lo) >> shift) >= (uint32_t)kBins) ++shift;
+      while (((k.hi - k.lo) >> shift) >= (uint32_t)kBins) ++shift;
       sm.h.clear();
-      tokens(part, [&](float v, uint32_t key, int) {
-        if (key >= key_lo && key <= key_hi) sm.h.add((int)((key_hi - key) >> shift), scale.weight(sm.table, v));
-      });
+      tokens(part, k, [&](float v, uint32_t key, int) { sm.h.add((int)((k.hi - key) >> shift), scale.weight(sm.table, v)); });
       __syncthreads();
       run(sm.sub, sm.h.at(threadIdx.x), Mark{0, 0});
       const int p = min(locate(sm.sub, base, kind, t), kBins - 1);
       const Mark start = base;
       if (p > 0) base = {start.count + sm.sub[p - 1].count, start.mass + sm.sub[p - 1].mass};
       upto = {start.count + sm.sub[p].count, start.mass + sm.sub[p].mass};
-      key_hi -= (uint32_t)p << shift;
+      k.hi -= (uint32_t)p << shift;
       const uint32_t width = (1u << shift) - 1u;
-      key_lo = max(key_lo, key_hi - min(key_hi, width));
+      k.lo = max(k.lo, k.hi - min(k.hi, width));
+      if constexpr (TYPE != 2) {  // down to one logit in 16 bits
+        constexpr uint32_t low = TYPE == 0 ? 0xffffu : 0x1fffu;
+        if (k.hi - k.lo <= low) k.lo = k.hi = k.hi >= 0x80000000u ? k.hi & ~low : k.lo | low;
+      }
       __syncthreads();
     }
   }
@@ -505,38 +621,45 @@ struct Row {
     const u64 r = kind == kCount ? t - base.count : w == 0 ? 1 : kind == kMassGe ? (t - base.mass + w - 1) / w : (t - base.mass) / w + 1;
     Answer got{base.count + r, base.mass + r * w, key, -1};
     if (kind != kMassGt) return got;
-    // The r-th of them by number, in the row itself.
+    // The r-th of them by number, in the row itself: each warp counts them in a
+    // sixteenth, and the one that has it is cut up in the same way, down to 32
+    // groups of values, a lane each.
     if (threadIdx.x == 0) sm.answer = got;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, groups = values.groups();
-    u64 left = r;
-    for (int g0 = 0; g0 < groups; g0 += kThreads) {
-      const int g = g0 + threadIdx.x;
-      u64 n = 0;
-      if (g < groups) values.group(g, [&](float f, int) { n += key_of(f) == key; });
-      u64 upto = n;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int g0 = 0, g1 = values.groups();
+    unsigned left = (unsigned)r;
+    while (g1 - g0 > 32) {
+      const int each = (g1 - g0 + kWarps - 1) / kWarps, from = min(g0 + warp * each, g1), to = min(from + each, g1);
+      unsigned mine = 0;
+      values.steps(from + lane, to, 32, [&](float f, int) { mine += key_of(f) == key; });
+      mine = warp_add(mine);
+      __syncthreads();
+      if (lane == 0) sm.warp[warp][0] = mine;
+      __syncthreads();
+      unsigned before = 0;
+      int w = 0;
+      while (w < kWarps - 1 && before + (unsigned)sm.warp[w][0] < left) before += (unsigned)sm.warp[w++][0];
+      left -= before;
+      g0 = min(g0 + w * each, g1), g1 = min(g0 + each, g1);
+    }
+    if (warp == 0) {
+      const int at = values.first() + (g0 + lane) * Values<TYPE>::kGroup;
+      const bool there = g0 + lane < g1;
+      const uint4 v = there && values.inside(at) ? values.load(at) : make_uint4(0u, 0u, 0u, 0u);
+      unsigned n = 0;
+      if (there) values.group(at, v, [&](float f, int) { n += key_of(f) == key; });
+      unsigned upto = n;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const u64 o = __shfl_up_sync(0xffffffffu, upto, d);
+        const unsigned o = __shfl_up_sync(0xffffffffu, upto, d);
         if (lane >= d) upto += o;
       }
-      __syncthreads();
-      if (lane == 31) sm.warp[warp][0] = upto;
-      __syncthreads();
-      u64 all = 0;
-      for (int i = 0; i < kWarps; ++i) {
-        if (i == warp) upto += all;
-        all += sm.warp[i][0];
+      if (left <= upto && left > upto - n) {
+        unsigned k = left - (upto - n);
+        values.group(at, v, [&](float f, int idx) {
+          if (key_of(f) == key && --k == 0u) sm.answer.idx = idx;
+        });
       }
-      if (left <= all) {
-        if (left <= upto && left > upto - n) {
-          u64 k = left - (upto - n);
-          values.group(g, [&](float f, int idx) {
-            if (key_of(f) == key && --k == 0) sm.answer.idx = idx;
-          });
-        }
-        break;
-      }
-      left -= all;
     }
     __syncthreads();
     got = sm.answer;
@@ -551,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   __shared__ Shared sm;
   const int tid = threadIdx.x, row = blockIdx.x;
   for (int i = tid; i < 1024; i += kThreads) sm.table[i] = kPowers.at[i];
-  if (tid == 0) sm.listed = kBins;
+  if (tid == 0) sm.listed = TYPE == 2 ? kBins : 0;
   __syncthreads();
   grid_dependency_wait();
   grid_dependents_launch();
@@ -563,11 +686,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     return;
   }
-  Row<TYPE> r{sm, a, row, {row_of<TYPE>(a, row), 0, a.vocab}, s.scale};
+  Row<TYPE> r{sm, a, row, {row_of<TYPE>(a, row), 0, a.vocab}, s.scale, s.top_key};
   {
     const uint32_t* count = a.parts_count + (size_t)row * kSampleParts;
     const u64* mass = a.parts_mass + (size_t)row * kSampleParts;
-    if (!s.one)
+    if (TYPE == 2 && !s.one)
       for (int i = tid; i < a.slices; i += kThreads)
         atomicMin(&sm.listed, __ldcg(&a.list_info[(size_t)row * a.slices + i].y));
     r.run(sm.top, Mark{__ldcg(count + tid), __ldcg(mass + tid)}, Mark{__ldcg(count + kBins), __ldcg(mass + kBins)});
@@ -604,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       u64 count = 0, mass = 0;
       for (int part = p0; part <= p1; ++part) {
         if (sm.top[part].count == (part > 0 ? sm.top[part - 1].count : 0ull)) continue;
-        r.tokens(part, [&](float v, uint32_t, int) {
+        r.tokens(part, r.keys_of(part), [&](float v, uint32_t, int) {
           const u64 w = s.scale.weight(sm.table, v);
           if (w >= least) mass += w, ++count;
         });
@@ -629,19 +752,29 @@ cudaError_t launch_t(const SampleArgs& a, cudaStream_t s) {
   const dim3 slices((unsigned)a.rows * a.slices);
   cudaError_t e = launch_dependent(sample_top_kernel<TYPE>, slices, kThreads, 0, s, a);
   if (e != cudaSuccess) return e;
-  e = launch_dependent(sample_parts_kernel<TYPE>, slices, kThreads, 0, s, a);
+  if constexpr (TYPE == 2) {
+    e = launch_dependent(sample_weigh_kernel, slices, kThreads, 0, s, a);
+  } else {
+    e = set_smem_limit((const void*)sample_count_kernel<TYPE>, 131072);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(sample_count_kernel<TYPE>, slices, kCountThreads, 131072, s, a);
+  }
   if (e != cudaSuccess) return e;
   return launch_dependent(sample_kernel<TYPE>, dim3(a.rows), kThreads, 0, s, a);
 }
 
 }  // namespace
 
-// Slices of 32768 values, or smaller ones while a row's slices do not fill the
-// SMs (two blocks each).
-SampleSlices sample_slices(int rows, int vocab) {
-  int slice = 32768;
-  while (slice > 2048 && (long long)rows * ((vocab + slice - 1) / slice) < 608) slice /= 2;
-  return {slice, (vocab + slice - 1) / slice};
+// 16 bits: slices of 65528 values at most, and of a quarter of that at least,
+// as each takes 65536 counters to clear and look through. 32 bits: of 32768,
+// and 2048. Smaller ones while the row's slices do not fill the SMs.
+SampleSlices sample_slices(int rows, int vocab, bool wide) {
+  const int most = wide ? 32768 : 65528, least = wide ? 2048 : 16384, fill = wide ? 608 : 304;
+  int n = (vocab + most - 1) / most;
+  while ((long long)rows * n < fill && (vocab + 2 * n - 1) / (2 * n) >= least) n *= 2;
+  const int slice = ((vocab + n - 1) / n + 7) / 8 * 8;
+  n = (vocab + slice - 1) / slice;
+  return {slice, n, wide ? max(32, min(256, 4096 / n)) : 0};
 }
 
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {

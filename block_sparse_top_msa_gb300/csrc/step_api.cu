@@ -341,11 +341,13 @@ msa_status_t msa_step_tables(const int32_t* page_table, int max_pages, int num_r
   return from_cuda(launch_step_tables(a, stream));
 }
 
-size_t msa_sample_workspace_size(int rows, int vocab) {
+size_t msa_sample_workspace_size(int rows, int vocab, msa_dtype_t dtype) {
   if (rows < 0 || vocab < 1 || rows > (1 << 24) || vocab > kMaxVocab) return 0;
-  const size_t n = (size_t)rows * sample_slices(rows, vocab).slices;
+  if (dtype != MSA_BF16 && dtype != MSA_FP16 && dtype != MSA_FP32) return 0;
+  const SampleSlices c = sample_slices(rows, vocab, dtype == MSA_FP32);
+  const size_t n = (size_t)rows * c.slices;
   return up256(n * 8) + up256((size_t)rows * kSampleParts * 4) + up256((size_t)rows * kSampleParts * 8) +
-         up256(n * kSampleList * 8) + up256(n * 8);
+         up256(n * c.listed * 8) + up256(n * 8);
 }
 
 msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride, int rows,
@@ -364,15 +366,15 @@ msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride,
   if (shares({tokens, logprobs}, {logits, uniforms, temperature, top_k, top_p, min_p})) return MSA_INVALID_ARG;
   if (vocab > kMaxVocab || rows > (1 << 24)) return MSA_UNSUPPORTED;
   if (rows == 0) return MSA_OK;
-  if (workspace == nullptr || workspace_bytes < msa_sample_workspace_size(rows, vocab)) return MSA_WORKSPACE_TOO_SMALL;
+  if (workspace == nullptr || workspace_bytes < msa_sample_workspace_size(rows, vocab, dtype)) return MSA_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 256)) return MSA_INVALID_ARG;
-  const SampleSlices c = sample_slices(rows, vocab);
+  const SampleSlices c = sample_slices(rows, vocab, dtype == MSA_FP32);
   SampleArgs a{};
   a.logits = logits, a.stride = stride, a.type = dtype == MSA_BF16 ? 0 : dtype == MSA_FP16 ? 1 : 2;
   a.rows = rows, a.vocab = vocab;
   a.uniforms = uniforms, a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p;
   a.tokens = tokens, a.logprobs = logprobs;
-  a.slice = c.slice, a.slices = c.slices;
+  a.slice = c.slice, a.slices = c.slices, a.listed = c.listed;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   auto place = [&](size_t bytes) {
     uint8_t* at = w;
@@ -383,7 +385,7 @@ msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride,
   a.best = reinterpret_cast<unsigned long long*>(place(n * 8));
   a.parts_count = reinterpret_cast<uint32_t*>(place((size_t)rows * kSampleParts * 4));
   a.parts_mass = reinterpret_cast<unsigned long long*>(place((size_t)rows * kSampleParts * 8));
-  a.list = reinterpret_cast<uint2*>(place(n * kSampleList * 8));
+  a.list = reinterpret_cast<uint2*>(place(n * c.listed * 8));
   a.list_info = reinterpret_cast<int2*>(place(n * 8));
   return from_cuda(launch_sample(a, stream));
 }

@@ -44,7 +44,9 @@ MSA_DEV unsigned page_hash(int page) { return (unsigned)page * 2654435761u; }
 // the lowest request that has it: all that ever stands in a place are requests
 // with one page, so which one is there while others look does not matter, and
 // the lowest one is what is left. The members of a group are put in their order
-// by one warp, 32 requests at a time.
+// by one warp, 32 requests at a time. Bound by the latency of its steps: what
+// they read again stands in shared memory (2048 requests: 31 us with first
+// pages and groups read back from global memory, 12 so).
 __global__ void __launch_bounds__(kPlanThreads)
     step_plan_kernel(const __grid_constant__ StepTablesArgs a) {
   extern __shared__ int dyn[];
@@ -52,16 +54,17 @@ __global__ void __launch_bounds__(kPlanThreads)
   __shared__ int s_int[32];
   const int tid = threadIdx.x, lane = tid & 31;
   const int slots = a.hash_slots;
-  int* hash = dyn;            // (slots); once the groups are known: starts (batch), limits (batch)
-  int* count = dyn + slots;   // (batch): members of each group
-  int32_t* first = a.plan;               // first page of each request that may share, else -1
+  int* hash = dyn;          // (slots), while the groups are looked for
+  int* first = dyn + slots;  // (batch): first page of each request that may share, else -1
+  int* start = dyn;                // (batch) each, after that: where a group's members go,
+  int* least = dyn + a.batch;      // the whole blocks before any new token of it,
+  int* group = dyn + 2 * a.batch;  // its members' count, then each request's group
   int32_t* leader = a.plan + a.batch;
-  int32_t* group = a.plan + 2 * a.batch;  // at a leader, then at every request
-  int32_t* limit = a.plan + 3 * a.batch;  // whole blocks before a request's new tokens
+  int32_t* group_of = a.plan + 2 * a.batch;  // at a leader, then at every request
+  int32_t* limit = a.plan + 3 * a.batch;     // whole blocks before a request's new tokens
   grid_dependency_wait();
   grid_dependents_launch();
   for (int i = tid; i < slots; i += kPlanThreads) hash[i] = -1;
-  for (int i = tid; i < a.batch; i += kPlanThreads) count[i] = 0;
   long long carry = 0;
   int fit = 0;  // the last sum within total_q
   if (tid == 0) a.cu_q[0] = 0;
@@ -69,12 +72,12 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int b = b0 + tid;
     int len = 0, n = 0, page = -1;
     if (b < a.batch) {
-      const int r = __ldg(a.rows + b);
+      const int r = __ldg(a.rows + b), want = __ldg(a.new_lens + b);
       if (r >= 0 && r < a.num_rows) {
+        page = __ldg(a.page_table + (size_t)r * a.max_pages);
         len = max(0, __ldg(a.seqused_k + r));
-        n = min(max(0, __ldg(a.new_lens + b)), len);
-        if (n > 0) page = __ldg(a.page_table + (size_t)r * a.max_pages);
-        if (page >= a.num_pages) page = -1;
+        n = min(max(0, want), len);
+        if (n == 0 || page >= a.num_pages) page = -1;
       }
     }
     long long all;
@@ -92,7 +95,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (b < a.batch) {
       a.cu_q[b + 1] = fits ? (int)upto : fit;
       a.seqused_out[b] = len;
-      first[b] = fits && page >= 0 && n > 0 ? page : -1;
+      first[b] = fits && page >= 0 ? page : -1;
       limit[b] = (len - n) / kBlk;
     }
   }
@@ -125,36 +128,38 @@ __global__ void __launch_bounds__(kPlanThreads)
     int all;
     const int upto = block_sum_upto<int>(leads, s_int, all);
     if (b < a.batch) leader[b] = l;
-    if (leads) group[b] = groups + upto - 1;
+    if (leads) group_of[b] = groups + upto - 1;
     groups += all;
   }
+  __syncthreads();  // the table is done with
+  for (int g = tid; g < a.batch; g += kPlanThreads) group[g] = 0, least[g] = a.max_pages;
   __syncthreads();
   for (int b = tid; b < a.batch; b += kPlanThreads) {
-    const int l = leader[b];
-    if (l == b) atomicAdd(&count[group[b]], 1);
-    else atomicAdd(&count[group[l]], 1);
+    const int l = leader[b], g = group_of[l];
+    atomicAdd(&group[g], 1);
+    atomicMin(&least[g], limit[b]);
   }
   __syncthreads();
-  int* start = hash;
-  int* least = hash + a.batch;
   int placed = 0;
   for (int g0 = 0; g0 <= a.batch; g0 += kPlanThreads) {
     const int g = g0 + tid;
-    const int n = g < a.batch ? count[g] : 0;
+    const int n = g < a.batch ? group[g] : 0;
     int all;
     const int upto = block_sum_upto<int>(n, s_int, all);
     if (g <= a.batch) a.cu_groups[g] = placed + upto - n;
-    if (g < a.batch) start[g] = placed + upto - n, least[g] = n > 1 ? a.max_pages : 0;
+    if (g < a.batch) {
+      start[g] = placed + upto - n;
+      a.group_blocks[g] = n > 1 ? least[g] : 0;
+    }
     placed += all;
   }
   __syncthreads();
   for (int b = tid; b < a.batch; b += kPlanThreads) {
-    const int g = group[leader[b]];
-    if (leader[b] != b) group[b] = g;
-    atomicMin(&least[g], limit[b]);
+    const int l = leader[b], g = group_of[l];
+    group[b] = g;
+    if (l != b) group_of[b] = g;
   }
   __syncthreads();
-  for (int g = tid; g < a.batch; g += kPlanThreads) a.group_blocks[g] = least[g];
   if (tid >= 32) return;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
     const int b = b0 + lane, g = b < a.batch ? group[b] : -1;
@@ -263,7 +268,7 @@ cudaError_t launch_step_tables(const StepTablesArgs& args, cudaStream_t s) {
   StepTablesArgs a = args;
   a.hash_slots = 64;
   while (a.hash_slots < 2 * a.batch) a.hash_slots *= 2;
-  const int smem = (int)sizeof(int) * (a.hash_slots + a.batch);
+  const int smem = (int)sizeof(int) * (a.hash_slots + a.batch);  // three numbers a request at least
   cudaError_t e = set_smem_limit((const void*)step_plan_kernel, smem);
   if (e != cudaSuccess) return e;
   e = launch_dependent(step_plan_kernel, dim3(1), kPlanThreads, smem, s, a);

@@ -545,13 +545,13 @@ msa_status_t msa_step_tables(const int32_t* page_table, int max_pages, int num_r
  *   tokens       device int32 (rows)
  *   logprobs     device float32 (rows) or NULL: ln w - ln S(vocab) of the
  *                token, before the cuts (T = 1 where the largest is taken)
- *   workspace    msa_sample_workspace_size(rows, vocab) bytes, 256-byte aligned,
+ *   workspace    msa_sample_workspace_size(rows, vocab, dtype) bytes, 256-byte aligned,
  *                uninitialised; calls that share one must be ordered on the device
  * MSA_INVALID_ARG for a NULL or misaligned pointer (arrays of rows may be NULL
  * when rows is 0), vocab below 1, a stride below vocab, or an output that is an
  * input; MSA_UNSUPPORTED for another dtype, vocab above 2^19 or rows above 2^24.
  */
-size_t msa_sample_workspace_size(int rows, int vocab);
+size_t msa_sample_workspace_size(int rows, int vocab, msa_dtype_t dtype);
 msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride, int rows,
                         int vocab, const float* uniforms, const float* temperature,
                         const int32_t* top_k, const float* top_p, const float* min_p,
