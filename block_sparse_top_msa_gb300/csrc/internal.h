@@ -486,14 +486,14 @@ struct SampleArgs {
   unsigned long long* best = nullptr;    // (rows, slices)
   uint32_t* parts_count = nullptr;       // (rows, kSampleParts)
   unsigned long long* parts_mass = nullptr;
-  int listed = 0;                        // tokens of a slice that its list holds
-  uint2* list = nullptr;                 // (rows, slices, listed)
-  int2* list_info = nullptr;             // (rows, slices): tokens listed, parts they are of
+  uint16_t* order = nullptr;             // (rows, slices, slice): a slice's tokens by parts
+  uint16_t* starts = nullptr;            // (rows, slices, 520): where the parts begin in it
 };
 struct SampleSlices {
-  int slice, slices, listed;
+  int slice, slices;  // (no slices of 16-bit logits)
 };
 SampleSlices sample_slices(int rows, int vocab, bool wide);
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
+cudaError_t launch_sample_16(const SampleArgs& a, cudaStream_t s);
 
 }  // namespace msa

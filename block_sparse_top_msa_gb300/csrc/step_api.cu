@@ -346,8 +346,10 @@ size_t msa_sample_workspace_size(int rows, int vocab, msa_dtype_t dtype) {
   if (dtype != MSA_BF16 && dtype != MSA_FP16 && dtype != MSA_FP32) return 0;
   const SampleSlices c = sample_slices(rows, vocab, dtype == MSA_FP32);
   const size_t n = (size_t)rows * c.slices;
+  if (rows == 0) return 0;
+  if (c.slices == 0) return 256;  // 16-bit logits need none
   return up256(n * 8) + up256((size_t)rows * kSampleParts * 4) + up256((size_t)rows * kSampleParts * 8) +
-         up256(n * c.listed * 8) + up256(n * 8);
+         up256(n * c.slice * 2) + up256(n * 520 * 2);
 }
 
 msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride, int rows,
@@ -374,7 +376,7 @@ msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride,
   a.rows = rows, a.vocab = vocab;
   a.uniforms = uniforms, a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p;
   a.tokens = tokens, a.logprobs = logprobs;
-  a.slice = c.slice, a.slices = c.slices, a.listed = c.listed;
+  a.slice = c.slice, a.slices = c.slices;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   auto place = [&](size_t bytes) {
     uint8_t* at = w;
@@ -385,8 +387,8 @@ msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride,
   a.best = reinterpret_cast<unsigned long long*>(place(n * 8));
   a.parts_count = reinterpret_cast<uint32_t*>(place((size_t)rows * kSampleParts * 4));
   a.parts_mass = reinterpret_cast<unsigned long long*>(place((size_t)rows * kSampleParts * 8));
-  a.list = reinterpret_cast<uint2*>(place(n * c.listed * 8));
-  a.list_info = reinterpret_cast<int2*>(place(n * 8));
+  a.order = reinterpret_cast<uint16_t*>(place(n * c.slice * 2));
+  a.starts = reinterpret_cast<uint16_t*>(place(n * 520 * 2));
   return from_cuda(launch_sample(a, stream));
 }
 

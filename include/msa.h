@@ -545,7 +545,8 @@ msa_status_t msa_step_tables(const int32_t* page_table, int max_pages, int num_r
  *   tokens       device int32 (rows)
  *   logprobs     device float32 (rows) or NULL: ln w - ln S(vocab) of the
  *                token, before the cuts (T = 1 where the largest is taken)
- *   workspace    msa_sample_workspace_size(rows, vocab, dtype) bytes, 256-byte aligned,
+ *   workspace    msa_sample_workspace_size(rows, vocab, dtype) bytes (about two a
+ *                logit in 32 bits, 256 in all in 16), 256-byte aligned,
  *                uninitialised; calls that share one must be ordered on the device
  * MSA_INVALID_ARG for a NULL or misaligned pointer (arrays of rows may be NULL
  * when rows is 0), vocab below 1, a stride below vocab, or an output that is an

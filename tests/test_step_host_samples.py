@@ -60,7 +60,7 @@ def test_sample_refuses(L, bad, status):
 def test_sample_workspace(L):
     size = L.msa_sample_workspace_size
     assert size(-1, 5, 3) == 0 and size(1, 0, 3) == 0 and size(1, (1 << 19) + 1, 3) == 0 and size(1, 5, 2) == 0 and size(1 << 25, 5, 0) == 0
-    assert size(0, 5, 3) == 0 and size(512, 200019, 0) < 1 << 23 and size(512, 200019, 3) < 1 << 25
+    assert size(0, 5, 3) == 0 and size(512, 200019, 0) == 256 and 2 * 512 * 200019 < size(512, 200019, 3) < 1 << 28  # two bytes a token
 
 
 PATH = "sa dr mask words cu b t w path len nxt s".split()
