@@ -468,7 +468,8 @@ cudaError_t launch_draft_path(const DraftPathArgs& a, cudaStream_t s);
 
 // Tokens from logits (sample.cu).
 constexpr int kMaxVocab = 1 << 19;
-constexpr int kSampleParts = 513;  // of a row's histogram
+constexpr int kSampleParts = 1025;   // of a row's histogram
+constexpr int kSampleStarts = 1032;  // where they begin in a slice's order, and its end; whole 16 bytes
 struct SampleArgs {
   const void* logits = nullptr;  // (rows, vocab), `stride` values from row to row
   long long stride = 0;
@@ -487,12 +488,12 @@ struct SampleArgs {
   uint32_t* parts_count = nullptr;       // (rows, kSampleParts)
   unsigned long long* parts_mass = nullptr;
   uint16_t* order = nullptr;             // (rows, slices, slice): a slice's tokens by parts
-  uint16_t* starts = nullptr;            // (rows, slices, 520): where the parts begin in it
+  uint16_t* starts = nullptr;            // (rows, slices, kSampleStarts): where the parts begin in it
 };
 struct SampleSlices {
   int slice, slices;  // (no slices of 16-bit logits)
 };
-SampleSlices sample_slices(int rows, int vocab, bool wide);
+SampleSlices sample_slices(int rows, int vocab, bool wide, bool aligned);
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s);
 cudaError_t launch_sample_16(const SampleArgs& a, cudaStream_t s);
 

@@ -34,8 +34,8 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kOrderCap = 256;  // tokens that are ordered at once
-constexpr int kStarts = 520;    // first places of the parts in a slice's order, and its end; whole 16 bytes
-static_assert(kBins == kThreads, "a thread for each part");
+constexpr int kStarts = kSampleStarts;
+static_assert(kBins == 2 * kThreads, "a thread for two parts");
 using Row32 = Values<2>;
 
 struct Histogram {
@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_sort_kernel(const __grid_c
     if (live && !rest) place[i] = ((uint32_t)part << 16) | atomicAdd(&sm.h.cnt[part], 1u);
   }
   __syncthreads();
-  int upto = (int)sm.h.cnt[tid];
-  const int own = upto;
+  const int own = (int)sm.h.cnt[2 * tid], two = own + (int)sm.h.cnt[2 * tid + 1];
+  int upto = two;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     const int o = __shfl_up_sync(0xffffffffu, upto, d);
@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_sort_kernel(const __grid_c
   if (lane == 31) sm.upto[warp] = upto;
   __syncthreads();
   for (int w = 0; w < warp; ++w) upto += sm.upto[w];
-  sm.start[tid] = (uint16_t)(upto - own);
+  sm.start[2 * tid] = (uint16_t)(upto - two);
+  sm.start[2 * tid + 1] = (uint16_t)(upto - two + own);
   if (tid == kThreads - 1) sm.start[kBins] = (uint16_t)upto, sm.start[kBins + 1] = (uint16_t)(upto + (int)sm.h.cnt[kBins]);
   __syncthreads();
   const int total = sm.start[kBins + 1];
@@ -246,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_sort_kernel(const __grid_c
   sm.h.flush(a, row);
 }
 
-struct Shared {
+struct __align__(16) Shared {
   u64 table[1024];
   Histogram h;
   Mark top[kBins + 1];  // the row's histogram as running sums
@@ -337,26 +338,30 @@ struct Row {
     }
   }
 
-  // Running sums of the parts; the last one's is all.
-  MSA_DEV void run(Mark* to, Mark m, Mark last) {
+  // Running sums of the parts, of which a thread has two; the last one's is all.
+  MSA_DEV void run(Mark* to, Mark m, Mark next, Mark last) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Mark upto{m.count + next.count, m.mass + next.mass};
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const u64 x = __shfl_up_sync(0xffffffffu, m.count, d), y = __shfl_up_sync(0xffffffffu, m.mass, d);
-      if (lane >= d) m.count += x, m.mass += y;
+      const u64 x = __shfl_up_sync(0xffffffffu, upto.count, d), y = __shfl_up_sync(0xffffffffu, upto.mass, d);
+      if (lane >= d) upto.count += x, upto.mass += y;
     }
     __syncthreads();
-    if (lane == 31) sm.warp[warp][0] = m.count, sm.warp[warp][1] = m.mass;
+    if (lane == 31) sm.warp[warp][0] = upto.count, sm.warp[warp][1] = upto.mass;
     __syncthreads();
-    for (int w = 0; w < warp; ++w) m.count += sm.warp[w][0], m.mass += sm.warp[w][1];
-    to[threadIdx.x] = m;
-    if (threadIdx.x == kThreads - 1) to[kBins] = {m.count + last.count, m.mass + last.mass};
+    for (int w = 0; w < warp; ++w) upto.count += sm.warp[w][0], upto.mass += sm.warp[w][1];
+    to[2 * threadIdx.x] = {upto.count - next.count, upto.mass - next.mass};
+    to[2 * threadIdx.x + 1] = upto;
+    if (threadIdx.x == kThreads - 1) to[kBins] = {upto.count + last.count, upto.mass + last.mass};
     __syncthreads();
   }
+
   // The first part of `marks` whose running sum, with `base`, passes; the last one if none before does.
   MSA_DEV int locate(const Mark* marks, Mark base, Kind kind, u64 t) {
     auto at = [&](int i) { return passes(kind, t, Mark{base.count + marks[i].count, base.mass + marks[i].mass}); };
-    return kBins - __syncthreads_count(at(threadIdx.x));
+    const int thread = kThreads - __syncthreads_count(at(2 * threadIdx.x + 1));
+    return thread == kThreads ? kBins : 2 * thread + !at(2 * thread);
   }
 
   // Where the row's order passes t (which it does, or its end is told).
@@ -387,7 +392,7 @@ struct Row {
       sm.h.clear();
       tokens(part, part, k, [&](float v, uint32_t key, int) { sm.h.add((int)((k.hi - key) >> shift), scale.weight(sm.table, v)); });
       __syncthreads();
-      run(sm.sub, sm.h.at(threadIdx.x), Mark{0, 0});
+      run(sm.sub, sm.h.at(2 * threadIdx.x), sm.h.at(2 * threadIdx.x + 1), Mark{0, 0});
       const int p = min(locate(sm.sub, base, kind, t), kBins - 1);
       const Mark start = base;
       if (p > 0) base = {start.count + sm.sub[p - 1].count, start.mass + sm.sub[p - 1].mass};
@@ -461,7 +466,8 @@ struct Row {
 
 // A block for each row: its cuts, and its token.
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_constant__ SampleArgs a) {
-  __shared__ Shared sm;
+  extern __shared__ uint4 answer_memory[];
+  Shared& sm = *reinterpret_cast<Shared*>(answer_memory);
   const int tid = threadIdx.x, row = blockIdx.x;
   for (int i = tid; i < 1024; i += kThreads) sm.table[i] = kPowers.at[i];
   grid_dependency_wait();
@@ -478,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   {
     const uint32_t* count = a.parts_count + (size_t)row * kSampleParts;
     const u64* mass = a.parts_mass + (size_t)row * kSampleParts;
-    r.run(sm.top, Mark{__ldcg(count + tid), __ldcg(mass + tid)}, Mark{__ldcg(count + kBins), __ldcg(mass + kBins)});
+    r.run(sm.top, Mark{__ldcg(count + 2 * tid), __ldcg(mass + 2 * tid)}, Mark{__ldcg(count + 2 * tid + 1), __ldcg(mass + 2 * tid + 1)},
+          Mark{__ldcg(count + kBins), __ldcg(mass + kBins)});
   }
   const u64 z = sm.top[kBins].mass;
   int token = s.top_idx;
@@ -539,12 +546,12 @@ cudaError_t launch_sort(const SampleArgs& a, dim3 slices, cudaStream_t s) {
 }  // namespace
 
 // 32 bits: slices of 8192 values, or of 2048 while those of 8192 do not fill
-// the SMs twice. A row's first group may begin up to three values before it.
-SampleSlices sample_slices(int rows, int vocab, bool wide) {
+// the SMs twice. A row's first group may begin up to three values before it,
+// unless rows are aligned.
+SampleSlices sample_slices(int rows, int vocab, bool wide, bool aligned) {
   if (!wide) return {vocab, 0};
-  auto count = [&](int slice) { return (vocab + 3 + slice - 1) / slice; };
-  const int slice = (long long)rows * count(8192) >= 304 ? 8192 : 2048;
-  return {slice, count(slice)};
+  const int slice = (long long)rows * ((vocab + 3 + 8191) / 8192) >= 304 ? 8192 : 2048;  // aligned or not
+  return {slice, (vocab + (aligned ? 0 : 3) + slice - 1) / slice};
 }
 
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
@@ -554,7 +561,9 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = a.slice == 2048 ? launch_sort<1>(a, slices, s) : launch_sort<4>(a, slices, s);
   if (e != cudaSuccess) return e;
-  return launch_dependent(sample_kernel, dim3(a.rows), kThreads, 0, s, a);
+  e = set_smem_limit((const void*)sample_kernel, sizeof(Shared));
+  if (e != cudaSuccess) return e;
+  return launch_dependent(sample_kernel, dim3(a.rows), kThreads, sizeof(Shared), s, a);
 }
 
 }  // namespace msa

@@ -12,7 +12,7 @@ namespace {
 
 using u64 = unsigned long long;
 
-constexpr int kOctaveBins = 32, kBins = kSampleParts - 1;  // of the first 16 octaves below the maximum; then one for the rest
+constexpr int kOctaveBins = 32, kBins = kSampleParts - 1;  // of the first 32 octaves below the maximum; then one for the rest
 constexpr float kNoWeight = -45.5f;  // 2^y below half of 2^-44
 constexpr u64 kOne = 1ull << 44;
 constexpr uint32_t kKeyNegInf = 0x007fffffu;

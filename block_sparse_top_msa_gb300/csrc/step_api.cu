@@ -344,12 +344,12 @@ msa_status_t msa_step_tables(const int32_t* page_table, int max_pages, int num_r
 size_t msa_sample_workspace_size(int rows, int vocab, msa_dtype_t dtype) {
   if (rows < 0 || vocab < 1 || rows > (1 << 24) || vocab > kMaxVocab) return 0;
   if (dtype != MSA_BF16 && dtype != MSA_FP16 && dtype != MSA_FP32) return 0;
-  const SampleSlices c = sample_slices(rows, vocab, dtype == MSA_FP32);
+  const SampleSlices c = sample_slices(rows, vocab, dtype == MSA_FP32, false);
   const size_t n = (size_t)rows * c.slices;
   if (rows == 0) return 0;
   if (c.slices == 0) return 256;  // 16-bit logits need none
   return up256(n * 8) + up256((size_t)rows * kSampleParts * 4) + up256((size_t)rows * kSampleParts * 8) +
-         up256(n * c.slice * 2) + up256(n * 520 * 2);
+         up256(n * c.slice * 2) + up256(n * kSampleStarts * 2);
 }
 
 msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride, int rows,
@@ -370,7 +370,8 @@ msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride,
   if (rows == 0) return MSA_OK;
   if (workspace == nullptr || workspace_bytes < msa_sample_workspace_size(rows, vocab, dtype)) return MSA_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 256)) return MSA_INVALID_ARG;
-  const SampleSlices c = sample_slices(rows, vocab, dtype == MSA_FP32);
+  const bool row_aligned = aligned(logits, 16) && (rows == 1 || stride % 4 == 0);
+  const SampleSlices c = sample_slices(rows, vocab, dtype == MSA_FP32, row_aligned);
   SampleArgs a{};
   a.logits = logits, a.stride = stride, a.type = dtype == MSA_BF16 ? 0 : dtype == MSA_FP16 ? 1 : 2;
   a.rows = rows, a.vocab = vocab;
@@ -388,7 +389,7 @@ msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride,
   a.parts_count = reinterpret_cast<uint32_t*>(place((size_t)rows * kSampleParts * 4));
   a.parts_mass = reinterpret_cast<unsigned long long*>(place((size_t)rows * kSampleParts * 8));
   a.order = reinterpret_cast<uint16_t*>(place(n * c.slice * 2));
-  a.starts = reinterpret_cast<uint16_t*>(place(n * 520 * 2));
+  a.starts = reinterpret_cast<uint16_t*>(place(n * kSampleStarts * 2));
   return from_cuda(launch_sample(a, stream));
 }
 
