@@ -259,7 +259,6 @@ struct __align__(16) Shared {
   int rank[kOrderCap];
   u64 sorted[kOrderCap];
   u64 sorted_w[kOrderCap];
-  u64 ask;
   Answer answer;
 };
 
@@ -491,14 +490,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
   int token = s.top_idx;
   float chosen = s.scale.m;
   if (!s.one) {
-    // What one thread works out in 64 bits, for all.
-    auto ask = [&](auto f) -> u64 {
-      if (tid == 0) sm.ask = f();
-      __syncthreads();
-      const u64 t = sm.ask;
-      __syncthreads();
-      return t;
-    };
     u64 sum = z, n = (u64)a.vocab;
     if (s.k > 0 && s.k < a.vocab) {
       const Answer x = r.find(kCount, (u64)s.k);
@@ -506,13 +497,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
     }
     const float p = a.top_p != nullptr ? __ldg(a.top_p + row) : 1.f;
     if (p < 1.f) {
-      const u64 t = ask([&] { return max((u64)ceil((double)fmaxf(p, 0.f) * (double)sum), 1ull); });
-      const Answer x = r.find(kMassGe, t);
+      const Answer x = r.find(kMassGe, max(share_of(sum, fmaxf(p, 0.f), true), 1ull));
       sum = x.s, n = x.n;
     }
-    const float mp = a.min_p != nullptr ? fminf(__ldg(a.min_p + row), 1.f) : 0.f;
-    if (mp > 0.f) {
-      const u64 least = ask([&] { return max((u64)ceil((double)mp * (double)kOne), 1ull); });
+    const float min_p = a.min_p != nullptr ? __ldg(a.min_p + row) : 0.f;
+    if (min_p > 0.f) {
+      const float mp = fminf(min_p, 1.f);
+      const u64 least = max(share_of(kOne, mp, true), 1ull);
       // The parts that the border may be in, token by token.
       const int mid = (int)fminf(log2f(mp) * -(float)kOctaveBins, (float)kBins), p0 = max(mid - 1, 0), p1 = min(mid + 1, kBins);
       const Mark before = p0 > 0 ? sm.top[p0 - 1] : Mark{0, 0};
@@ -525,8 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const __grid_consta
       if (before.count + m.count < n) n = before.count + m.count, sum = before.mass + m.mass;
     }
     const float u = __ldg(a.uniforms + row);
-    const u64 at = ask([&] { return u < 1.f ? min((u64)floor((double)fmaxf(u, 0.f) * (double)sum), sum - 1) : sum - 1; });
-    const Answer x = r.find(kMassGt, at);
+    const Answer x = r.find(kMassGt, u < 1.f ? min(share_of(sum, fmaxf(u, 0.f), false), sum - 1) : sum - 1);
     token = x.idx;
     chosen = value_of(x.key);
   }

@@ -55,10 +55,24 @@ struct __align__(16) Mark {
 MSA_DEV bool passes(Kind kind, u64 t, Mark m) {
   return kind == kCount ? m.count >= t : kind == kMassGe ? m.mass >= t : m.mass > t;
 }
-// How many tokens of weight w, behind `base`, until it passes t.
+// How many tokens of weight w, behind `base`, until it passes t: at most 2^19,
+// so that the quotient of two floats is off by one at most.
 MSA_DEV u64 equals_upto(Kind kind, u64 t, Mark base, u64 w) {
   if (kind == kCount) return t - base.count;
-  return w == 0 ? 1 : kind == kMassGe ? (t - base.mass + w - 1) / w : (t - base.mass) / w + 1;
+  if (w == 0) return 1;
+  const u64 rest = t - base.mass;
+  u64 n = (u64)((float)rest / (float)w);
+  while (n > 0 && n * w > rest) --n;
+  while ((n + 1) * w <= rest) ++n;
+  return kind == kMassGe ? n + (n * w < rest) : n + 1;  // at least, or more than, the rest
+}
+// f times the sum, f in [0, 1], rounded down, or up: exact.
+MSA_DEV u64 share_of(u64 sum, float f, bool up) {
+  const uint32_t bits = __float_as_uint(f);
+  const int e = (int)(bits >> 23) & 255, shift = 150 - max(e, 1);  // f = m 2^-shift, shift >= 23
+  const u64 m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u), lo = sum * m, hi = __umul64hi(sum, m);
+  if (shift >= 64) return (shift >= 128 ? 0ull : hi >> (shift - 64)) + (up && (hi | lo) != 0 ? 1 : 0);  // hi has 24 bits
+  return ((hi << (64 - shift)) | (lo >> shift)) + (up && (lo & ((1ull << shift) - 1)) != 0 ? 1 : 0);
 }
 
 MSA_DEV uint32_t key_of(float f) {
@@ -193,10 +207,10 @@ MSA_DEV const uint8_t* row_of(const SampleArgs& a, int row) {
   return static_cast<const uint8_t*>(a.logits) + (size_t)row * (size_t)a.stride * Values<TYPE>::kSize;
 }
 
-// The left-th token with this key, in the row itself: each of WARPS warps counts
-// them in its share, and the share that has it is cut up in the same way, down
-// to 32 groups of values, a lane each. counts: a word a warp; the block waits
-// before and after.
+// The left-th token with this key, in the row itself: WARPS warps count them in
+// a part of it, each in its share, until they have come to it; the share that
+// has it is cut up in the same way, down to 32 groups of values, a lane each.
+// counts: a word a warp; the block waits before and after.
 template <int TYPE, int WARPS>
 MSA_DEV int nth_of_key(const Values<TYPE>& v, uint32_t key, unsigned left, uint32_t* counts, int* answer) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -211,25 +225,29 @@ MSA_DEV int nth_of_key(const Values<TYPE>& v, uint32_t key, unsigned left, uint3
   auto count = [&](int at, const uint4& x) -> unsigned {
     unsigned n = 0;
     if (v.inside(at)) {
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      const uint32_t d[4] = {(x.x ^ pat) & mask, (x.y ^ pat) & mask, (x.z ^ pat) & mask, (x.w ^ pat) & mask};
+      if constexpr (TYPE != 2) {  // none of the eight, mostly
+        const uint32_t least = __vminu2(__vminu2(d[0], d[1]), __vminu2(d[2], d[3]));
+        if ((least & 0xffffu) != 0u && (least >> 16) != 0u) return 0u;
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t d = (w[j] ^ pat) & mask;
-        if constexpr (TYPE == 2) n += d == 0u;
-        else n += ((d & 0xffffu) == 0u) + ((d >> 16) == 0u);
+        if constexpr (TYPE == 2) n += d[j] == 0u;
+        else n += ((d[j] & 0xffffu) == 0u) + ((d[j] >> 16) == 0u);
       }
     } else {
       v.group(at, x, [&](float g, int) { n += g == f; });
     }
     return n;
   };
+  constexpr int kAhead = 8;
   const int at0 = v.first();
   int g0 = 0, g1 = v.groups();
   while (g1 - g0 > 32) {
-    const int each = (g1 - g0 + WARPS - 1) / WARPS, from = min(g0 + warp * each, g1), to = min(from + each, g1);
+    const int each = min((g1 - g0 + WARPS - 1) / WARPS, 32 * kAhead), from = min(g0 + warp * each, g1), to = min(from + each, g1);
     unsigned mine = 0;
-    constexpr int kAhead = 8;
-    for (int g = from + lane; g < to; g += 32 * kAhead) {
+    {
+      const int g = from + lane;
       uint4 x[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
@@ -244,11 +262,17 @@ MSA_DEV int nth_of_key(const Values<TYPE>& v, uint32_t key, unsigned left, uint3
     __syncthreads();
     if (lane == 0) counts[warp] = mine;
     __syncthreads();
-    unsigned before = 0;
-    int w = 0;
-    while (w < WARPS - 1 && before + counts[w] < left) before += counts[w++];
-    left -= before;
-    g0 = min(g0 + w * each, g1), g1 = min(g0 + each, g1);
+    unsigned upto = lane < WARPS ? counts[lane] : 0u;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const unsigned o = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += o;
+    }
+    const int w = __popc(__ballot_sync(0xffffffffu, upto < left));  // warps that end before it
+    const unsigned before = __shfl_sync(0xffffffffu, upto, max(w - 1, 0));
+    if (w > 0) left -= before;
+    if (w < 32) g0 = min(g0 + w * each, g1), g1 = min(g0 + each, g1);
+    else g0 = min(g0 + WARPS * each, g1);  // not in this part
   }
   __syncthreads();
   if (warp == 0) {

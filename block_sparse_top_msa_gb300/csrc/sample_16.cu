@@ -38,8 +38,11 @@ struct Shared16 {
   uint32_t spilled;
   uint32_t spilled_at[kSpilled], spilled_n[kSpilled];
   uint32_t top;
-  u64 ask;
+  Answer answer;
   int idx;
+  uint32_t some[kChunks / 32];  // chunks with any logit, a bit each
+  uint16_t list[kChunks];
+  uint32_t listed;
 };
 
 template <int TYPE>
@@ -52,7 +55,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_16_kernel(const __grid_con
   uint32_t* words = reinterpret_cast<uint32_t*>(counters);
   for (int i = tid; i < 8192; i += kThreads) counters[i] = make_uint4(0u, 0u, 0u, 0u);
   for (int i = tid; i < 1024; i += kThreads) sm.table[i] = kPowers.at[i];
-  if (tid == 0) sm.spilled = 0u, sm.top = ~0u, sm.idx = 0;
+  if (tid == 0) sm.spilled = 0u, sm.top = ~0u, sm.idx = 0, sm.listed = 0u;
+  if (tid < kChunks / 32) sm.some[tid] = 0u;
   __syncthreads();
   grid_dependency_wait();
   grid_dependents_launch();
@@ -134,9 +138,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_16_kernel(const __grid_con
   __syncthreads();
   {
     uint32_t top = ~0u;
+#pragma unroll
     for (int i = tid; i < 8192; i += kThreads) {
       const uint4 c = counters[i];
-      if ((c.x | c.y | c.z | c.w) == 0u || 8u * i > top) continue;
+      const bool any = (c.x | c.y | c.z | c.w) != 0u;
+      const unsigned bits = __ballot_sync(0xffffffffu, any);  // of four chunks, eight lanes each
+      if (bits != 0u && lane < 4 && (bits >> (8 * lane) & 0xffu)) atomicOr(&sm.some[i >> 8], 1u << (((i >> 5) * 4 + lane) & 31));
+      if (!any || 8u * i > top) continue;
       const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
       for (int j = 7; j >= 0; --j) {
@@ -144,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_16_kernel(const __grid_con
         if (((w[j >> 1] >> (16 * (j & 1))) & 0xffffu) != 0u && place >= kFirst && place < kEnd) top = min(top, place);
       }
     }
+    if (tid < spilled) atomicOr(&sm.some[sm.spilled_at[tid] >> 11], 1u << (sm.spilled_at[tid] >> 6 & 31));
     if (tid < spilled && sm.spilled_at[tid] >= kFirst && sm.spilled_at[tid] < kEnd) top = min(top, sm.spilled_at[tid]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = min(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -170,7 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_16_kernel(const __grid_con
     const uint32_t word = words[chunk * 32 + lane], place = (uint32_t)chunk * 64u + 2u * lane;
     Two x{{word & 0xffffu, word >> 16}, {0ull, 0ull}};
     for (int e = 0; e < spilled; ++e)
-      if ((sm.spilled_at[e] & ~1u) == place) x.n[sm.spilled_at[e] & 1u] += sm.spilled_n[e];
+      if (sm.spilled_at[e] == place) x.n[0] += sm.spilled_n[e];
+      else if (sm.spilled_at[e] == place + 1u) x.n[1] += sm.spilled_n[e];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       if (place + j < kFirst || place + j >= kEnd) x.n[j] = 0u;
@@ -178,13 +188,20 @@ __global__ void __launch_bounds__(kThreads, 1) sample_16_kernel(const __grid_con
     }
     return x;
   };
-  for (int chunk = warp; chunk < kChunks; chunk += kWarps) {
-    Mark m{0, 0};
-    if (spilled > 0 || __any_sync(0xffffffffu, words[chunk * 32 + lane] != 0u)) {
-      const Two x = two_of(chunk);
-      m = {warp_add(x.n[0] + x.n[1]), warp_add(x.n[0] * x.w[0] + x.n[1] * x.w[1])};
-    }
-    if (lane == 0) sm.run[chunk] = m;
+  // Sums of the warp's lanes by 26 bits at a time, so that 32 of them fit in 32.
+  auto add_lanes = [](u64 x) -> u64 {
+    const u64 low = __reduce_add_sync(0xffffffffu, (uint32_t)x & 0x3ffffffu), mid = __reduce_add_sync(0xffffffffu, (uint32_t)(x >> 26) & 0x3ffffffu);
+    return low + (mid << 26) + ((u64)__reduce_add_sync(0xffffffffu, (uint32_t)(x >> 52)) << 52);
+  };
+  sm.run[tid] = {0, 0};
+  if (sm.some[warp] >> lane & 1u) sm.list[atomicAdd(&sm.listed, 1u)] = (uint16_t)tid;
+  __syncthreads();
+  for (int i = warp; i < (int)sm.listed; i += kWarps) {
+    const int chunk = sm.list[i];
+    const Two x = two_of(chunk);
+    const u64 mass = add_lanes(x.n[0] * x.w[0] + x.n[1] * x.w[1]);
+    const uint32_t count = __reduce_add_sync(0xffffffffu, x.n[0] + x.n[1]);
+    if (lane == 0) sm.run[chunk] = {count, mass};
   }
   __syncthreads();
   {
@@ -203,39 +220,35 @@ __global__ void __launch_bounds__(kThreads, 1) sample_16_kernel(const __grid_con
   const u64 z = sm.run[kChunks - 1].mass;
 
   // ---------------------------------------------------------------- questions
-  // Where the row's order passes p: every warp works it out.
+  // Where the row's order passes p. One warp looks into the chunk.
   auto find = [&](Kind kind, u64 p) -> Answer {
     const int chunk = kChunks - __syncthreads_count(passes(kind, p, sm.run[tid]));
     if (chunk == kChunks) return {sm.run[kChunks - 1].count, z, 0u, 0};
-    const Two x = two_of(chunk);
-    const Mark base = chunk > 0 ? sm.run[chunk - 1] : Mark{0, 0};
-    Mark upto{x.n[0] + x.n[1], x.n[0] * x.w[0] + x.n[1] * x.w[1]};
-    const Mark own = upto;
+    if (warp == 0) {
+      const Two x = two_of(chunk);
+      const Mark base = chunk > 0 ? sm.run[chunk - 1] : Mark{0, 0};
+      Mark upto{x.n[0] + x.n[1], x.n[0] * x.w[0] + x.n[1] * x.w[1]};
+      const Mark own = upto;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const u64 c = __shfl_up_sync(0xffffffffu, upto.count, d), m = __shfl_up_sync(0xffffffffu, upto.mass, d);
-      if (lane >= d) upto.count += c, upto.mass += m;
+      for (int d = 1; d < 32; d <<= 1) {
+        const u64 c = __shfl_up_sync(0xffffffffu, upto.count, d), m = __shfl_up_sync(0xffffffffu, upto.mass, d);
+        if (lane >= d) upto.count += c, upto.mass += m;
+      }
+      upto.count += base.count, upto.mass += base.mass;
+      const unsigned hits = __ballot_sync(0xffffffffu, passes(kind, p, upto));
+      if (lane == __ffs(hits) - 1) {
+        Mark before{upto.count - own.count, upto.mass - own.mass};
+        const Mark mid{before.count + x.n[0], before.mass + x.n[0] * x.w[0]};
+        const int j = passes(kind, p, mid) ? 0 : 1;
+        if (j == 1) before = mid;
+        const u64 w = j == 0 ? x.w[0] : x.w[1], r = equals_upto(kind, p, before, w);
+        sm.answer = {before.count + r, before.mass + r * w, (uint32_t)chunk * 64u + 2u * lane + j, (int)r};
+      }
     }
-    upto.count += base.count, upto.mass += base.mass;
-    const unsigned hits = __ballot_sync(0xffffffffu, passes(kind, p, upto));
-    Mark before{upto.count - own.count, upto.mass - own.mass};
-    int j = 0;
-    const Mark mid{before.count + x.n[0], before.mass + x.n[0] * x.w[0]};
-    if (!passes(kind, p, mid)) j = 1, before = mid;
-    u64 r = 0;
-    if (lane == __ffs(hits) - 1) r = equals_upto(kind, p, before, x.w[j]);
-    const Answer got{before.count + r, before.mass + r * x.w[j], (uint32_t)chunk * 64u + 2u * lane + j, (int)r};
-    const int from = __ffs(hits) - 1;
-    return {__shfl_sync(0xffffffffu, got.n, from), __shfl_sync(0xffffffffu, got.s, from),
-            __shfl_sync(0xffffffffu, got.key, from), __shfl_sync(0xffffffffu, got.idx, from)};
-  };
-  // What one thread works out in 64 bits, for all.
-  auto ask = [&](auto f) -> u64 {
-    if (tid == 0) sm.ask = f();
     __syncthreads();
-    const u64 x = sm.ask;
+    const Answer got = sm.answer;
     __syncthreads();
-    return x;
+    return got;
   };
   uint32_t place = top;
   unsigned which = 1;  // of its equals
@@ -247,12 +260,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_16_kernel(const __grid_con
     }
     const float p = a.top_p != nullptr ? __ldg(a.top_p + row) : 1.f;
     if (p < 1.f) {
-      const Answer x = find(kMassGe, ask([&] { return max((u64)ceil((double)fmaxf(p, 0.f) * (double)sum), 1ull); }));
+      const Answer x = find(kMassGe, max(share_of(sum, fmaxf(p, 0.f), true), 1ull));
       sum = x.s, kept = x.n;
     }
-    const float mp = a.min_p != nullptr ? fminf(__ldg(a.min_p + row), 1.f) : 0.f;
-    if (mp > 0.f) {
-      const u64 least = ask([&] { return max((u64)ceil((double)mp * (double)kOne), 1ull); });
+    const float min_p = a.min_p != nullptr ? __ldg(a.min_p + row) : 0.f;
+    if (min_p > 0.f) {
+      const float mp = fminf(min_p, 1.f);
+      const u64 least = max(share_of(kOne, mp, true), 1ull);
       // The last chunk whose first logit has that weight, and those of its logits.
       const uint32_t first = 64u * tid;
       const int chunk =
@@ -262,13 +276,12 @@ __global__ void __launch_bounds__(kThreads, 1) sample_16_kernel(const __grid_con
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         if (x.w[j] >= least) count += x.n[j], mass += x.n[j] * x.w[j];
-      count = warp_add(count), mass = warp_add(mass);
+      count = warp_add(count), mass = add_lanes(mass);
       if (chunk > 0) count += sm.run[chunk - 1].count, mass += sm.run[chunk - 1].mass;
       if (count < kept) kept = count, sum = mass;
     }
     const float u = __ldg(a.uniforms + row);
-    const Answer x =
-        find(kMassGt, ask([&] { return u < 1.f ? min((u64)floor((double)fmaxf(u, 0.f) * (double)sum), sum - 1) : sum - 1; }));
+    const Answer x = find(kMassGt, u < 1.f ? min(share_of(sum, fmaxf(u, 0.f), false), sum - 1) : sum - 1);
     place = x.key, which = (unsigned)x.idx;
   }
   const float chosen = logit_at<TYPE>(place);
