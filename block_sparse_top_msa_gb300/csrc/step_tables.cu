@@ -44,9 +44,10 @@ MSA_DEV unsigned page_hash(int page) { return (unsigned)page * 2654435761u; }
 // the lowest request that has it: all that ever stands in a place are requests
 // with one page, so which one is there while others look does not matter, and
 // the lowest one is what is left. The members of a group are put in their order
-// by one warp, 32 requests at a time. Bound by the latency of its steps: what
-// they read again stands in shared memory (2048 requests: 31 us with first
-// pages and groups read back from global memory, 12 so).
+// by one warp, 32 requests at a time, for which all warps have counted what
+// stands before each among its 32. Bound by the latency of its
+// steps, of which the order is the longest: 2048 requests take 17 us (28 where
+// the one warp counts too: 480 clocks for each 32 requests), 16 take 7.
 __global__ void __launch_bounds__(kPlanThreads)
     step_plan_kernel(const __grid_constant__ StepTablesArgs a) {
   extern __shared__ int dyn[];
@@ -154,23 +155,34 @@ __global__ void __launch_bounds__(kPlanThreads)
     placed += all;
   }
   __syncthreads();
-  for (int b = tid; b < a.batch; b += kPlanThreads) {
-    const int l = leader[b], g = group_of[l];
-    group[b] = g;
-    if (l != b) group_of[b] = g;
+  // Of 32 requests each: its group, how many of them stand before it there, and
+  // at the first of a group how many there are.
+  static_assert(kMaxCacheRows <= 1 << 14, "a group's number has 14 bits");
+  for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int g = -1;
+    if (b < a.batch) {
+      const int l = leader[b];
+      g = group_of[l];
+      if (l != b) group_of[b] = g;
+    }
+    const unsigned same = __match_any_sync(0xffffffffu, g);
+    const int before = __popc(same & ((1u << lane) - 1u));
+    if (b < a.batch) group[b] = g | before << 14 | (before == 0 ? __popc(same) : 0) << 19;
   }
   __syncthreads();
   if (tid >= 32) return;
+  int x = lane < a.batch ? group[lane] : -1;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int b = b0 + lane, g = b < a.batch ? group[b] : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, g);
-    const int at = g >= 0 ? start[g] : 0;
+    const int b = b0 + lane, next = b + 32 < a.batch ? group[b + 32] : -1, g = x & 0x3fff;
+    const int at = x >= 0 ? start[g] : 0;
     __syncwarp();
-    if (g >= 0) {
-      a.group_rows[at + __popc(same & ((1u << lane) - 1u))] = b;
-      if ((int)(__ffs(same) - 1) == lane) start[g] = at + __popc(same);
+    if (x >= 0) {
+      a.group_rows[at + ((x >> 14) & 31)] = b;
+      if (x >> 19) start[g] = at + (x >> 19);
     }
     __syncwarp();
+    x = next;
   }
 }
 
