@@ -1,5 +1,5 @@
-// Python calls of the serving step's operators (norm and rotation, tree
-// attention, the cache's pages): argument checks, output allocation and the
+// Python calls of the serving step's operators (norm and rotation, attention of
+// trees and over shared prefixes, the cache's pages, a step's tables, sampling): argument checks, output allocation and the
 // call of the C entry point of the same name in libmsa.so. A call of these
 // takes a few microseconds on the GPU for a decode step, less than checking a
 // dozen tensors does in Python, hence a compiled binding: against the same

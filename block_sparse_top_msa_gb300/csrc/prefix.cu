@@ -74,7 +74,8 @@ MSA_DEV Sums block_sums(Sums x, Sums* s_warp, Sums& all) {
 
 // The work, by one block: the requests in the order of their groups, where
 // their tokens begin in that order, the blocks that each group attends for
-// all, the entries and the running sums of what they cost.
+// all, the entries and the running sums of what they cost. Bound by the latency
+// of its loads and sums: 7 us for 8 requests, 10 for 128 of 4 prompts.
 __global__ void __launch_bounds__(kPlanThreads)
     prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ int dyn[];
@@ -205,7 +206,9 @@ __global__ void __launch_bounds__(kPlanThreads)
 // joined. Bound by memory: a block of 64 KB takes an SM's share of the
 // bandwidth 3000 clocks. One warp hands out the pieces with their Q, another
 // brings K and V by TMA through a ring of blocks; the join borrows the next
-// free slots of that ring.
+// free slots of that ring. 32 requests of 4096 to 65536 keys, 4 KV heads,
+// 16 bits: 338 to 345 us, 6.6 to 6.75 TB/s, what a copy reaches. E4M3 caches have half the
+// bytes and the same MMAs, 256 a block, which bound them then (2000 clocks).
 constexpr int kWarps = 8;
 template <int KV>  // 0 bf16, 1 f16, 2 E4M3 with bf16 q
 struct Small {
@@ -750,7 +753,8 @@ __device__ __noinline__ void odd_row(const PrefixArgs& a, const Ranges& ranges, 
 // head at a time; each of its warps finds their parts for itself (ten loads one
 // after the other: what a chunk of 16 rows mostly takes) and has two of each 16
 // rows, 16 lanes each, of eight columns: first the parts of the group's run,
-// then those of the own one, in the order of the pieces.
+// then those of the own one, in the order of the pieces. Alone 8 to 19 us for up to
+// 8192 rows, bound by that search; 34 for 32768.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
     prefix_join_kernel(const __grid_constant__ PrefixArgs a) {

@@ -24,6 +24,16 @@
 // its largest value just below f16's largest; it comes back with the softmax
 // scale. V rows behind a sequence's end are zeroed in shared memory, as P = 0
 // times what a page may hold there need not be 0.
+//
+// 64 requests of 4 to 12 drafts over 32000 shared tokens, 64/4 heads: 463 us,
+// 1.18 PFLOP/s, the tensor cores 52% busy, issue slots 34%. What bounds it is a
+// stream's chain: of the 3770 clocks from one S of it to the next its products
+// take 1140, the softmax of both halves 1960, the rest lies between the roles.
+// Eight warps a stream, two threads a row that read S twice, took 511 us.
+// A unit of one block takes 8700 clocks: its masked block's softmax 3000, its Q
+// 1900 (a token's place, then the row), its epilogue 2300, and 1700 until its
+// first S. Of 4 prompts' 32 samples (E4M3, 182 us) 112 are left with prompts of
+// one block.
 #include <cuda_fp16.h>
 #include <math.h>
 

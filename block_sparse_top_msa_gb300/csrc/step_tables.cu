@@ -45,9 +45,9 @@ MSA_DEV unsigned page_hash(int page) { return (unsigned)page * 2654435761u; }
 // with one page, so which one is there while others look does not matter, and
 // the lowest one is what is left. The members of a group are put in their order
 // by one warp, 32 requests at a time, for which all warps have counted what
-// stands before each among its 32. Bound by the latency of its
-// steps, of which the order is the longest: 2048 requests take 17 us (28 where
-// the one warp counts too: 480 clocks for each 32 requests), 16 take 7.
+// stands before each among its 32. Bound by the latency of its steps: 2048
+// requests take 17 us (28 where the one warp counts too, 480 clocks for each 32
+// requests), 16 take 7.
 __global__ void __launch_bounds__(kPlanThreads)
     step_plan_kernel(const __grid_constant__ StepTablesArgs a) {
   extern __shared__ int dyn[];
@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 }
 
 // A block per request: its row of the page table, its tokens' places, and how
-// many of its blocks are its leader's too.
+// many of its blocks are its leader's too. 2048 requests with 1024 places each:
+// 8.8 us; they begin under the plan's end.
 constexpr int kRowThreads = 256;
 __global__ void __launch_bounds__(kRowThreads)
     step_rows_kernel(const __grid_constant__ StepTablesArgs a) {
@@ -231,7 +232,8 @@ __global__ void __launch_bounds__(kRowThreads)
 // The accepted path of each request, a warp for each. Nodes follow their
 // parents, so one pass over a request's nodes finds the path: of the nodes not
 // passed yet, the lowest child of the path's last node that the sample there
-// names. A lane holds a node; its parent is its highest ancestor below it.
+// names. A lane holds a node; its parent is its highest ancestor below it. Bound by
+// the latency of its loads: 7 us a call for 8 requests and for 256.
 constexpr int kPathWarps = 4;
 __global__ void __launch_bounds__(kPathWarps * 32)
     draft_path_kernel(const __grid_constant__ DraftPathArgs a) {

@@ -280,7 +280,7 @@ def test_hundreds_of_requests_and_pages_past_32_bits(msa):
 @pytest.mark.parametrize("prompts,samples,hq,hkv,kv", [([1300], [[(0, 1), (150, 1)]], 16, 2, "fp16"), ([300, 260], [[(0, 1), (40, 1)], [(5, 1), (200, 1)]], 4, 1, "bf16"),
                                                        ([400], [[(0, 4), (140, 4), (3, 5)]], 2, 2, "e4m3"), ([520, 40], [[(0, 0), (7, 2), (9, 1)], [(0, 1)]], 12, 3, "bf16")])
 def test_few_rows_in_all(msa, prompts, samples, hq, hkv, kv):
-    """At most 16 rows for each KV head: groups and requests by the one kernel, joined by the last."""
+    """At most 16 rows for each KV head in all: units of 256 rows with the groups, of 16 without."""
     c = make(prompts, samples, hq, hkv, kv, seed=20 + hq)
     assert int(c["cu"][-1]) * (hq // hkv) <= 16
     check(c, *run(msa, c))
