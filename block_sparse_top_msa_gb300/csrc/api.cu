@@ -901,9 +901,11 @@ msa_status_t build_prefix(
   a.lse = lse;
   a.small = !groups && max_seqlen_q > 0 && (long long)max_seqlen_q * (num_qo_heads / num_kv_heads) <= kSmallRows ? 1 : 0;
   a.grid = kPlanSMs;
-  // Chunks of 16 rows spread few rows over the SMs; of many rows larger ones
-  // save the search for their parts.
-  a.chunk_rows = (long long)total_q * num_qo_heads < 16384 ? 16 : 64;
+  // Small chunks spread few rows over the SMs, larger ones save the search for
+  // their parts: the smallest of which at most 512 are needed (8192 rows take 181
+  // us in all with chunks of 16, 192 with chunks of 8).
+  a.chunk_rows = 4;
+  while (a.chunk_rows < 64 && (long long)total_q * num_qo_heads > 512ll * a.chunk_rows) a.chunk_rows *= 2;
   a.entry = reinterpret_cast<int4*>(ws);
   a.work = reinterpret_cast<int4*>(ws + L.off_work);
   a.start = reinterpret_cast<long long*>(ws + L.off_start);

@@ -213,7 +213,7 @@ struct PrefixArgs {
   float* lse = nullptr;
   int small = 0;  // units of kSmallRows rows (no groups then), else of kBigRows
   int grid = 0;   // CTAs
-  int chunk_rows = 0;  // of the join's chunks: a multiple of 16 that divides kBigRows
+  int chunk_rows = 0;  // of the join's chunks: 4 to 64, a power of two
   // Workspace. Positions: the requests in the order of the groups. Entries: the
   // positions' own runs, then the groups', those that there are.
   int4* entry = nullptr;       // (batch, 2): first token in that order, tokens, request, group; first row of q, Lk - Lq, Lk, entry or -1

@@ -753,13 +753,17 @@ __device__ __noinline__ void odd_row(const PrefixArgs& a, const Ranges& ranges, 
 // head at a time; each of its warps finds their parts for itself (ten loads one
 // after the other: what a chunk of 16 rows mostly takes) and has two of each 16
 // rows, 16 lanes each, of eight columns: first the parts of the group's run,
-// then those of the own one, in the order of the pieces. Alone 8 to 19 us for up to
-// 8192 rows, bound by that search; 34 for 32768.
+// then those of the own one, in the order of the pieces. In a chunk of fewer rows
+// several half-warps take a row's parts by turns, where it has eight or more (8
+// samples of 32768 tokens, 38 parts a row: the call 48 -> 41 us; split like that, rows
+// of few parts cost the pair of 1300 tokens 1 us). Alone 8 to 19 us for up to 8192
+// rows, bound by that search; 34 for 32768.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
     prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.num_qo_heads / a.num_kv_heads;
   const int warps = gridDim.x * (kJoinThreads / 32);
+  __shared__ Joined s_joined[kJoinThreads / 16][16];
   grid_dependency_wait();
   grid_dependents_launch();
   const int entries = __ldcg(a.meta), odd = __ldcg(a.meta + 1);
@@ -784,6 +788,37 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int h = tile_head % a.num_kv_heads, rows = min(many, x.y - row0), col = (lane & 15) * 8;
     const Parts parts = parts_of(a, ranges, e, x.y, y.x, tile_head);
     const Before f = before_of(a, ranges, y.w, x.x, row0, rows, h);
+    auto odd_rows = [&](bool bad, size_t own_row) {
+      const unsigned bads = __ballot_sync(0xffffffffu, bad);
+      for (int k = 0; k < 2; ++k)
+        if ((bads >> (16 * k)) & 0xffffu) odd_row(a, ranges, (int)__shfl_sync(0xffffffffu, (unsigned)own_row, 16 * k), lane);
+    };
+    if (i >= a.grid && a.chunk_rows < kJoinThreads / 16 && max(parts.n, max(f.parts[0].n, f.parts[1].n)) >= 8) {
+      // Few rows of many parts: several half-warps to a row, whose first joins
+      // what the others have.
+      const int chunk = a.chunk_rows, step = kJoinThreads / 16 / chunk;
+      const int half = 2 * warp + (lane >> 4), from = half / chunk, r = half % chunk, er = row0 + r;
+      const size_t hq = (size_t)h * G + er % G, own_row = (size_t)(x.x + er / G) * a.num_qo_heads + hq;
+      Joined all;
+      if (r < rows) {
+        all.add_before(a, f, r, own_row, col, from, step);
+        all.add_parts(a, own_row, er % tile_rows_of(a), parts, col, from, step);
+      }
+      __syncthreads();  // the chunk before is done with
+      s_joined[half][lane & 15] = all;
+      __syncthreads();
+      bool bad = false;
+      if (r < rows && from == 0) {
+        for (int k = 1; k < step; ++k) {
+          const Joined& other = s_joined[half + k * chunk][lane & 15];
+          all.add(make_float2(other.m, other.l), other.o);
+        }
+        bad = a.causal && x.y > G && !all.finite();
+        all.write(a, (size_t)__ldcg(&a.token[x.x + er / G].x) * a.num_qo_heads + hq, col);
+      }
+      odd_rows(bad, own_row);
+      continue;
+    }
 #pragma unroll 1
     for (int r0 = 2 * warp; r0 < rows; r0 += kJoinThreads / 16) {
       const int r = r0 + (lane >> 4), er = row0 + r;
@@ -797,9 +832,7 @@ __global__ void __launch_bounds__(kJoinThreads)
         bad = a.causal && x.y > G && !all.finite();
         all.write(a, (size_t)token * a.num_qo_heads + hq, col);
       }
-      const unsigned bads = __ballot_sync(0xffffffffu, bad);
-      for (int k = 0; k < 2; ++k)
-        if ((bads >> (16 * k)) & 0xffffu) odd_row(a, ranges, (int)__shfl_sync(0xffffffffu, (unsigned)own_row, 16 * k), lane);
+      odd_rows(bad, own_row);
     }
   }
 }

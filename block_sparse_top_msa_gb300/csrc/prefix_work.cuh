@@ -193,15 +193,16 @@ struct Joined {
 #pragma unroll
     for (int c = 0; c < 8; ++c) o[c] = fmaf(p, v[c], o[c] * f);
   }
-  // Those at `first`, then those of the CTAs; loads of AHEAD at a time.
+  // Those at `first`, then those of the CTAs, from the from-th in steps; loads of
+  // AHEAD at a time.
   template <int kAhead>
-  MSA_DEV void add_some(const PrefixArgs& a, size_t first, int row, Parts parts, int col) {
-    for (int i0 = 0; i0 <= parts.n; i0 += kAhead) {
+  MSA_DEV void add_some(const PrefixArgs& a, size_t first, int row, Parts parts, int col, int from, int step) {
+    for (int i0 = from; i0 <= parts.n; i0 += kAhead * step) {
       float2 ml[kAhead];
       float4 v[kAhead][2];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int i = min(i0 + u, parts.n);
+        const int i = min(i0 + u * step, parts.n);
         const size_t at = i == 0 ? first : a.part_rows + (size_t)(parts.c0 + i) * tile_rows_of(a) + row;
         ml[u] = __ldcg(a.part_ml + at);
         const float4* from = reinterpret_cast<const float4*>(a.part_o + at * kHeadDim + col);
@@ -209,22 +210,22 @@ struct Joined {
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        if (i0 + u > parts.n) break;
+        if (i0 + u * step > parts.n) break;
         const float x[8] = {v[u][0].x, v[u][0].y, v[u][0].z, v[u][0].w, v[u][1].x, v[u][1].y, v[u][1].z, v[u][1].w};
         add(ml[u], x);
       }
     }
   }
   // Row `row` of its tile.
-  MSA_DEV void add_parts(const PrefixArgs& a, size_t first, int row, Parts parts, int col) {
-    if (parts.n < 2) add_some<2>(a, first, row, parts, col);
-    else add_some<8>(a, first, row, parts, col);
+  MSA_DEV void add_parts(const PrefixArgs& a, size_t first, int row, Parts parts, int col, int from = 0, int step = 1) {
+    if (parts.n < 2 * step) add_some<2>(a, first, row, parts, col, from, step);
+    else add_some<8>(a, first, row, parts, col, from, step);
   }
-  MSA_DEV void add_before(const PrefixArgs& a, const Before& f, int r, size_t own_row, int col) {
+  MSA_DEV void add_before(const PrefixArgs& a, const Before& f, int r, size_t own_row, int col, int from = 0, int step = 1) {
     if (!f.on) return;
     const int row = f.row0 + r, tile = row / tile_rows_of(a), second = tile - f.tile;
     add_parts(a, (size_t)a.total_q * a.num_qo_heads + own_row, row - tile * tile_rows_of(a),
-              Parts{second ? f.parts[1].c0 : f.parts[0].c0, second ? f.parts[1].n : f.parts[0].n}, col);
+              Parts{second ? f.parts[1].c0 : f.parts[0].c0, second ? f.parts[1].n : f.parts[0].n}, col, from, step);
   }
   MSA_DEV bool finite() const {
     float x = 0.f;
