@@ -27,7 +27,7 @@
 // returns is the token's place in it, so that one such addition a token is all,
 // and the weights are added up along the order, a thread 16 neighbours.
 //
-// 64 rows of 131072: 68 to 71 us (alone 11, 48 and 17); one row 17 to 19 (4, 9,
+// 64 rows of 131072: 68 to 71 us (alone 11, 48 and 17); one row 17 to 20 (4, 9,
 // 28). Neither memory nor one pipe bounds them: a slice of 8192 goes through its
 // steps one after the other, 27000 clocks with another beside it, 10500 of them
 // the weights, with issue slots 55% busy at 135 instructions a token; one row's
