@@ -58,8 +58,8 @@ struct Histogram {
     const uint32_t high = (uint32_t)(w >> 32) + (old + low < old ? 1u : 0u);
     if (high) atomicAdd(&hi[part], high);
   }
-  MSA_DEV void add(int part, u64 w, uint32_t n = 1u) {
-    atomicAdd(&cnt[part], n);
+  MSA_DEV void add(int part, u64 w) {
+    atomicAdd(&cnt[part], 1u);
     add_mass(part, w);
   }
   MSA_DEV Mark at(int part) const { return {cnt[part], ((u64)hi[part] << 32) + lo[part]}; }
