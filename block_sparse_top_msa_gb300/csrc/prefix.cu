@@ -600,8 +600,7 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-      if (m[r] == -INFINITY && !(l[r] == 0.f)) m[r] = 0.f;  // nothing but NaN
-      if (t == 0) sm.ml[ms][warp][g + 8 * r] = make_float2(m[r], l[r]);
+      if (t == 0) sm.ml[ms][warp][g + 8 * r] = part_of_sum(m[r], l[r]);
     }
     // Warp w's O: row r, column c at r * 128 + (c ^ 8 (r & 3)) of its 8 KB.
     auto o_of = [&](int w) -> float* {

@@ -182,6 +182,11 @@ MSA_DEV Before before_of(const PrefixArgs& a, const Ranges& ranges, int group, i
   return f;
 }
 
+// (m, l) of a part as it is joined: the part of a row that saw NaN has a sum of
+// NaN, and a maximum that is a number, as -inf says that it saw nothing and
+// maxima of parts drop NaN.
+MSA_DEV float2 part_of_sum(float m, float l) { return make_float2(m > -INFINITY || l == 0.f ? m : 0.f, l); }
+
 // Running sum of eight columns of a row's parts, by one thread.
 struct Joined {
   float m = -INFINITY, l = 0.f, o[8] = {};
