@@ -853,7 +853,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           a.odd[atomicAdd(a.meta + 1, 1)] = (s.tau + er / G) * a.num_qo_heads + s.h * G + er % G;
         }
       } else if (active) {
-        a.part_ml[at] = make_float2(m_ref == -INFINITY && !(l == 0.f) ? 0.f : m_ref, l);
+        a.part_ml[at] = part_of_sum(m_ref, l);
       }
     }
   }

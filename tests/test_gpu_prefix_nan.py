@@ -49,3 +49,28 @@ def test_a_page_of_nan_wherever_a_part_begins(msa, kv):
             nan_page(c, 0, block, 0)
         out, lse = run(msa, c, groups=False, max_seqlen_q=1)
         check_nan(c, out, lse)
+
+
+def pieces(blocks, cost, before, grid=152, least=16, unit=12):
+    """The blocks of the last unit on the line as its CTAs have them; `before` is what lies before it there."""
+    total = before + unit + cost * blocks
+    n = max(1, min(total // least, grid))
+    where = [before + (unit + cost * j if j else 0) for j in range(blocks)]
+    starts = [total * i // n for i in range(n + 1)]
+    got = [[j for j, at in enumerate(where) if starts[i] <= at < starts[i + 1]] for i in range(n)]
+    return [p for p in got if p]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("turn", [0, 1, 2, 3])
+def test_parts_of_nan_that_one_half_warp_joins(msa, kv, turn):
+    """Few rows of a long prefix: several half-warps join a row's parts by turns. All parts of one turn are NaN."""
+    c = make([20000], [[(0, 1), (17, 1)]], 4, 1, kv, seed=34, garbage=False)
+    cut = pieces(156, 3, 2 * 15)
+    assert len(cut) >= 16
+    for p in cut[turn::4]:
+        for block in p:
+            nan_page(c, int(c["rows"][0]), block, 0)
+    out, lse = run(msa, c)
+    check_nan(c, out, lse)
+    assert bool(lse.isnan().all())
