@@ -71,7 +71,8 @@ MSA_DEV u64 share_of(u64 sum, float f, bool up) {
   const uint32_t bits = __float_as_uint(f);
   const int e = (int)(bits >> 23) & 255, shift = 150 - max(e, 1);  // f = m 2^-shift, shift >= 23
   const u64 m = (bits & 0x7fffffu) | (e ? 0x800000u : 0u), lo = sum * m, hi = __umul64hi(sum, m);
-  if (shift >= 64) return (shift >= 128 ? 0ull : hi >> (shift - 64)) + (up && (hi | lo) != 0 ? 1 : 0);  // hi has 24 bits
+  if (shift >= 128) return up && m != 0 && sum != 0 ? 1 : 0;  // hi has 24 bits
+  if (shift >= 64) return (hi >> (shift - 64)) + (up && (lo | (hi & ((1ull << (shift - 64)) - 1))) != 0 ? 1 : 0);
   return ((hi << (64 - shift)) | (lo >> shift)) + (up && (lo & ((1ull << shift) - 1)) != 0 ? 1 : 0);
 }
 
