@@ -803,7 +803,7 @@ msa_status_t build_tree(
 
 // Workspace of the attention over shared prefixes.
 struct PrefixLayout {
-  size_t off_group, off_work, off_start, off_chunk, off_token, off_meta, off_cut, off_odd, off_ml, off_o, part_rows, total;
+  size_t off_group, off_work, off_start, off_chunk, off_token, off_meta, off_cut, off_ml, off_o, part_rows, total;
 };
 constexpr int kPrefixMaxPages = 1 << 23;  // tokens of a row's pages are counted in 32 bits
 
@@ -820,9 +820,8 @@ PrefixLayout prefix_layout(int batch, int total_q, int hq, bool groups) {
   L.off_start = place((2 * (size_t)batch + 1) * sizeof(long long));
   L.off_chunk = place((2 * (size_t)batch + 1) * sizeof(int));
   L.off_token = place((size_t)total_q * sizeof(int2));
-  L.off_meta = place(2 * sizeof(int));
+  L.off_meta = place(sizeof(int));
   L.off_cut = place((size_t)kPlanSMs * sizeof(int4));
-  L.off_odd = place((size_t)total_q * hq * sizeof(int));
   L.part_rows = (size_t)total_q * hq * (groups ? 2 : 1);
   const size_t rows = L.part_rows + (size_t)kPlanSMs * kBigRows;
   L.off_ml = place(rows * sizeof(float2));
@@ -866,7 +865,7 @@ msa_status_t build_prefix(
   if (workspace == nullptr || workspace_bytes < L.total) return MSA_WORKSPACE_TOO_SMALL;
   plan->empty = total_q == 0;
   if (plan->empty) return MSA_OK;
-  if (out == q) return MSA_INVALID_ARG;  // rows that are not finite read Q again
+  if (out == q) return MSA_INVALID_ARG;
   unsigned* fault = fault_word();
   if (fault == nullptr) return MSA_CUDA_ERROR;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -914,7 +913,6 @@ msa_status_t build_prefix(
   a.chunk = reinterpret_cast<int*>(ws + L.off_chunk);
   a.meta = reinterpret_cast<int*>(ws + L.off_meta);
   a.cut = reinterpret_cast<int4*>(ws + L.off_cut);
-  a.odd = reinterpret_cast<int*>(ws + L.off_odd);
   a.part_rows = L.part_rows;
   a.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
   a.part_o = reinterpret_cast<float*>(ws + L.off_o);

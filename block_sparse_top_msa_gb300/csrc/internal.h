@@ -222,9 +222,8 @@ struct PrefixArgs {
   long long* start = nullptr;  // (2 batch + 1): running sums of the entries' costs
   int* chunk = nullptr;        // (2 batch + 1): running count of what the join does for entries with a group before: chunk_rows rows of one KV head each
   int2* token = nullptr;       // (total_q): each token's row of q, and its position
-  int* meta = nullptr;         // entries, odd rows
+  int* meta = nullptr;         // entries
   int4* cut = nullptr;         // (grid): the unit without a group before that begins in the CTA's range and goes on after it: entry, tile and head; entry -1: none
-  int* odd = nullptr;          // (total_q * Hq): rows that are not finite, by token in the groups' order and head
   size_t part_rows = 0;        // rows of parts before the CTAs' own
   float2* part_ml = nullptr;   // (part_rows + grid * kBigRows)
   float* part_o = nullptr;     // the same, 128 each

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int n = (int)base.counts;
     a.start[n] = base.cost;
     a.chunk[n] = (int)(base.counts >> 32);
-    a.meta[0] = n, a.meta[1] = 0;
+    a.meta[0] = n;
   }
   // Each token's place in the groups' order, a warp for each request.
   for (int i = warp; i < a.batch; i += kPlanThreads / 32) {
@@ -267,6 +267,12 @@ MSA_DEV uint32_t e4m3x2_to_f16(uint32_t pair) {
 }
 // Of two keys' 16 bits each: those below `n` kept.
 MSA_DEV uint32_t keep_keys(int first, int n) { return (first < n ? 0xffffu : 0u) | (first + 1 < n ? 0xffff0000u : 0u); }
+// Of two 16-bit values: all bits of those that are not finite.
+template <bool F16>
+MSA_DEV uint32_t not_finite2(uint32_t x) {
+  constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u;
+  return __vcmpeq2(x & kExp, kExp);
+}
 
 template <int KV>
 __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
@@ -478,7 +484,6 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
       sees[r] = (int)max(0ll, min(lim, (long long)p.keys));
     }
     const int all_see = (int)max(0ll, min(min((long long)p.lk, (long long)p.hidden + p.row0 / G + 1) - base, (long long)p.keys));
-    const int here = (int)max(0ll, min((long long)p.lk - base, (long long)p.n * kBlk));  // keys of the sequence
     float o[16][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 16; ++i)
@@ -549,9 +554,19 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
             l[r] += p0 + p1;
             pa[2 * nt + r] = pack_x2<kF16>(p0, p1);
           }
-        // What the page holds behind the sequence's end may be anything.
-        const bool tail = k0 + 16 > here;
-        const uint32_t keep0 = keep_keys(k0 + 2 * t, here), keep1 = keep_keys(k0 + 8 + 2 * t, here);
+        // P = 0 times what a page may hold need not be 0. Values that no row sees
+        // are zeroed, and of those that some see what is not finite: the rows that
+        // see it get it below.
+        const bool edge = k0 + 16 > all_see;
+        const uint32_t keep0 = keep_keys(k0 + 2 * t, p.keys), keep1 = keep_keys(k0 + 8 + 2 * t, p.keys);
+        const uint32_t some0 = ~keep_keys(k0 + 2 * t, all_see), some1 = ~keep_keys(k0 + 8 + 2 * t, all_see);
+        uint32_t cleaned = 0u;
+        auto clean = [&](uint32_t& x, uint32_t keep, uint32_t some) {
+          x &= keep;
+          const uint32_t m = not_finite2<kF16>(x) & some;
+          cleaned |= m;
+          x &= ~m;
+        };
         const int vrow = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7);
         if constexpr (KV == 2) {
 #pragma unroll
@@ -565,7 +580,7 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
               for (int k = 0; k < 2; ++k) {
                 b[0][k] = e4m3x2_to_f16(__byte_perm(v[2 * h + k], 0u, 0x4420));
                 b[1][k] = e4m3x2_to_f16(__byte_perm(v[2 * h + k], 0u, 0x4431));
-                if (tail) b[0][k] &= k ? keep1 : keep0, b[1][k] &= k ? keep1 : keep0;
+                if (edge) clean(b[0][k], k ? keep1 : keep0, k ? some1 : some0), clean(b[1][k], k ? keep1 : keep0, k ? some1 : some0);
               }
               mma16816<kF16>(o[4 * cc + 2 * h], pa, b[0][0], b[0][1]);
               mma16816<kF16>(o[4 * cc + 2 * h + 1], pa, b[1][0], b[1][1]);
@@ -577,9 +592,34 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
             const int c = dn * 2 + (lane >> 4);
             uint32_t v[4];
             ldmatrix4_trans(v, vs0 + (c >> 3) * 16384 + sw128_offset(vrow, c & 7));
-            if (tail) v[0] &= keep0, v[1] &= keep1, v[2] &= keep0, v[3] &= keep1;
+            if (edge) clean(v[0], keep0, some0), clean(v[1], keep1, some1), clean(v[2], keep0, some0), clean(v[3], keep1, some1);
             mma16816<kF16>(o[2 * dn], pa, v[0], v[1]);
             mma16816<kF16>(o[2 * dn + 1], pa, v[2], v[3]);
+          }
+        }
+        if (__any_sync(0xffffffffu, cleaned != 0u)) {
+          // Infinite or NaN times any probability is that.
+#pragma unroll 1
+          for (int k = max(k0, all_see); k < min(k0 + 16, p.keys); ++k) {
+            const int row = k - j * kBlk;
+            const uint8_t* at = sm.stage[stage] + C::kTile;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                // A thread's columns of o[i]: values e and 2 + e are of rows g and g + 8.
+                float x;
+                if constexpr (KV == 2) {
+                  const int col = 16 * (i >> 1) + 4 * t + (i & 1) + 2 * e;
+                  x = (at[row * 128 + ((((col >> 4) ^ (row & 7)) << 4) | (col & 15))] & 0x7f) == 0x7f ? NAN : 0.f;
+                } else {
+                  const int col = 8 * i + 2 * t + e;
+                  const uint16_t w = *reinterpret_cast<const uint16_t*>(at + (col >> 6) * 16384 + sw128_offset(row, (col >> 3) & 7) + (col & 7) * 2);
+                  x = not_finite2<kF16>(w) == 0u ? 0.f : kF16 ? __half2float(__ushort_as_half(w)) : __uint_as_float((uint32_t)w << 16);
+                }
+                if (k < sees[0]) o[i][e] += x;
+                if (k < sees[1]) o[i][2 + e] += x;
+              }
           }
         }
       }
@@ -655,9 +695,7 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
     // The row: written where the unit is whole, else its parts.
     const bool live = out_row < p.rows;
     const size_t hq = (size_t)p.h * G + er % G, own_row = (size_t)(p.tau + er / G) * a.num_qo_heads + hq;
-    bool odd = false;
     if (live && p.whole) {
-      odd = a.causal && p.many && !own.finite();
       own.write(a, (size_t)token * a.num_qo_heads + hq, col);
     } else if (live) {
       const size_t at = p.place >= 0 ? own_row : a.part_rows + (size_t)blockIdx.x * kSmallRows + out_row;
@@ -666,87 +704,10 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
       to[1] = make_float4(own.o[4], own.o[5], own.o[6], own.o[7]);
       if (col == 0) a.part_ml[at] = make_float2(own.m, own.l);
     }
-    const unsigned rows_odd = __ballot_sync(0xffffffffu, odd);
-    if ((lane & 15) == 0 && ((rows_odd >> lane) & 0xffffu)) a.odd[atomicAdd(a.meta + 1, 1)] = (int)own_row;
   }
 }
 
 // ------------------------------------------------------------------ the join
-// One row's own run from its own visible keys, in fp32, by a warp: a lane takes
-// a key of 32, and then four columns of their V. Rows of a tile share the
-// products, so a row also multiplies, by P = 0, later tokens' values, which may
-// be infinite or NaN: such rows are computed anew here.
-__device__ __noinline__ void own_run(const PrefixArgs& a, size_t orow, int b, int h, int block0, int sees, int lane,
-                                     float& m, float& l, float (&acc)[4]) {
-  auto value = [&](const uint8_t* rows, int i, bool e4m3) {
-    if (e4m3) {
-      const uint32_t h2 = e4m3x2_to_f16(__ldg(rows + i));
-      return __low2float(*reinterpret_cast<const __half2*>(&h2));
-    }
-    const uint16_t w = __ldg(reinterpret_cast<const uint16_t*>(rows) + i);
-    return a.f16 ? __half2float(__ushort_as_half(w)) : __uint_as_float((uint32_t)w << 16);
-  };
-  const uint8_t* q = static_cast<const uint8_t*>(a.q) + orow * kHeadDim * 2;
-  m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) acc[c] = 0.f;
-  for (int k0 = block0 * kBlk; k0 < sees; k0 += 32) {
-    const int page = k0 / kBlk < a.max_pages ? __ldg(a.page_table + (size_t)b * a.max_pages + k0 / kBlk) : -1;
-    if (page < 0 || page >= a.num_pages) continue;
-    const size_t at = ((size_t)page * a.num_kv_heads + h) * kBlk * kHeadDim * (a.e4m3 ? 1 : 2);
-    const int in = k0 % kBlk, n = min(32, sees - k0);
-    float s = -INFINITY;
-    if (lane < n) {
-      s = 0.f;
-#pragma unroll 8
-      for (int c = 0; c < kHeadDim; ++c)
-        s = fmaf(value(q, c, false), value(a.k_pool + at, (in + lane) * kHeadDim + c, a.e4m3), s);
-      s *= a.scale_log2;
-    }
-    float top = s;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    top = fmaxf(top, m);
-    const bool nan = __any_sync(0xffffffffu, s != s);
-    if (top == -INFINITY && !nan) continue;
-    const float alpha = m == -INFINITY ? 0.f : ex2(m - top);
-    const float p = s == -INFINITY ? 0.f : ex2(s - top);
-    m = top;
-    l *= alpha;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] *= alpha;
-    for (int x = 0; x < n; ++x) {
-      const float px = __shfl_sync(0xffffffffu, p, x);
-      l += px;
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        acc[c] = fmaf(px, value(a.v_pool + at, (in + x) * kHeadDim + 4 * lane + c, a.e4m3), acc[c]);
-    }
-  }
-  if (m == -INFINITY && !(l == 0.f)) m = 0.f;
-}
-
-// A row that is not finite: its group's parts, and its own run anew.
-__device__ __noinline__ void odd_row(const PrefixArgs& a, const Ranges& ranges, int own_row, int lane) {
-  const int G = a.num_qo_heads / a.num_kv_heads, tau = own_row / a.num_qo_heads, hq = own_row - tau * a.num_qo_heads, h = hq / G;
-  const int2 token = __ldcg(a.token + tau);
-  const int4* w = a.work + 2 * __ldcg(&a.entry[2 * token.y + 1].w);
-  const int4 x = __ldcg(w), y = __ldcg(w + 1);
-  const int row = (tau - x.x) * G + hq - h * G, col = (lane & 15) * 8;
-  const size_t orow = (size_t)token.x * a.num_qo_heads + hq;
-  const Before f = before_of(a, ranges, y.w, x.x, row, 1, h);
-  Joined all;
-  all.add_before(a, f, 0, own_row, col);
-  float m, l, o[4];
-  const int sees = (int)min((long long)y.z, (long long)y.y + (tau - x.x) + 1);
-  own_run(a, orow, x.z, h, x.w & ~kGroupRun, sees, lane, m, l, o);
-  float v[8];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) v[c] = __shfl_sync(0xffffffffu, o[c & 3], 2 * (lane & 15) + (c >> 2));
-  all.add(make_float2(m, l), v);
-  if (lane < 16) all.write(a, orow, col);
-}
-
 // Joins what is left: of the requests with a group's run before their own, and
 // of the other units that ranges cut. A block takes chunk_rows rows of one KV
 // head at a time; each of its warps finds their parts for itself (ten loads one
@@ -761,13 +722,11 @@ constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
     prefix_join_kernel(const __grid_constant__ PrefixArgs a) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.num_qo_heads / a.num_kv_heads;
-  const int warps = gridDim.x * (kJoinThreads / 32);
   __shared__ Joined s_joined[kJoinThreads / 16][16];
   grid_dependency_wait();
   grid_dependents_launch();
-  const int entries = __ldcg(a.meta), odd = __ldcg(a.meta + 1);
+  const int entries = __ldcg(a.meta);
   const Ranges ranges = ranges_of(a, entries);
-  for (int i = warp * gridDim.x + blockIdx.x; i < odd; i += warps) odd_row(a, ranges, __ldcg(a.odd + i), lane);
   const int chunks = __ldcg(a.chunk + entries);
   for (int i = blockIdx.x; i < a.grid + chunks; i += gridDim.x) {
     int e, tile_head, row0, many;
@@ -787,11 +746,6 @@ __global__ void __launch_bounds__(kJoinThreads)
     const int h = tile_head % a.num_kv_heads, rows = min(many, x.y - row0), col = (lane & 15) * 8;
     const Parts parts = parts_of(a, ranges, e, x.y, y.x, tile_head);
     const Before f = before_of(a, ranges, y.w, x.x, row0, rows, h);
-    auto odd_rows = [&](bool bad, size_t own_row) {
-      const unsigned bads = __ballot_sync(0xffffffffu, bad);
-      for (int k = 0; k < 2; ++k)
-        if ((bads >> (16 * k)) & 0xffffu) odd_row(a, ranges, (int)__shfl_sync(0xffffffffu, (unsigned)own_row, 16 * k), lane);
-    };
     if (i >= a.grid && a.chunk_rows < kJoinThreads / 16 && max(parts.n, max(f.parts[0].n, f.parts[1].n)) >= 8) {
       // Few rows of many parts: several half-warps to a row, whose first joins
       // what the others have.
@@ -806,32 +760,26 @@ __global__ void __launch_bounds__(kJoinThreads)
       __syncthreads();  // the chunk before is done with
       s_joined[half][lane & 15] = all;
       __syncthreads();
-      bool bad = false;
       if (r < rows && from == 0) {
         for (int k = 1; k < step; ++k) {
           const Joined& other = s_joined[half + k * chunk][lane & 15];
           all.add(make_float2(other.m, other.l), other.o);
         }
-        bad = a.causal && x.y > G && !all.finite();
         all.write(a, (size_t)__ldcg(&a.token[x.x + er / G].x) * a.num_qo_heads + hq, col);
       }
-      odd_rows(bad, own_row);
       continue;
     }
 #pragma unroll 1
     for (int r0 = 2 * warp; r0 < rows; r0 += kJoinThreads / 16) {
       const int r = r0 + (lane >> 4), er = row0 + r;
       const size_t hq = (size_t)h * G + er % G, own_row = (size_t)(x.x + er / G) * a.num_qo_heads + hq;
-      bool bad = false;
       if (r < rows) {
         const int token = __ldcg(&a.token[x.x + er / G].x);
         Joined all;
         all.add_before(a, f, r, own_row, col);
         all.add_parts(a, own_row, er % tile_rows_of(a), parts, col);
-        bad = a.causal && x.y > G && !all.finite();
         all.write(a, (size_t)token * a.num_qo_heads + hq, col);
       }
-      odd_rows(bad, own_row);
     }
   }
 }

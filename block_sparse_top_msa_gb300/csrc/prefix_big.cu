@@ -22,8 +22,10 @@
 //
 // With E4M3 keys Q is f16 too, each row scaled by the power of two that puts
 // its largest value just below f16's largest; it comes back with the softmax
-// scale. V rows behind a sequence's end are zeroed in shared memory, as P = 0
-// times what a page may hold there need not be 0.
+// scale. P = 0 times what a page may hold need not be 0: V rows that no row of the
+// unit sees are zeroed in shared memory, and of those that some see (a causal
+// unit's last tokens) what is not finite; the rows that see it get it in the
+// epilogue (add_not_finite).
 //
 // 64 requests of 4 to 12 drafts over 32000 shared tokens, 64/4 heads: 463 us,
 // 1.18 PFLOP/s, the tensor cores 52% busy, issue slots 34%. What bounds it is a
@@ -68,7 +70,8 @@ struct Roles {
 
 // What a raw E4M3 slot holds; g == -1: no more.
 struct RawTile {
-  int g, is_v, rows;  // rows: keys of the block within the sequence (0: no page)
+  int g, is_v, rows;  // rows: keys of the block that some row of the unit sees (0: no page)
+  int open;           // V: of those, that all rows see
 };
 
 template <bool FP8>
@@ -94,6 +97,7 @@ struct __align__(1024) Smem {
   float q_scale[2][128];          // E4M3, one tile: the rows' softmax scales, of this piece and the next
   uint32_t tmem_base;
   int abort;
+  int cleaned;                    // values that are not finite were zeroed in some unit of this CTA
 };
 // A CTA's shared memory, which begins on 1024 bytes (the kernel looks).
 static_assert(sizeof(Smem<false>) <= 227 * 1024 && sizeof(Smem<true>) <= 227 * 1024, "too much shared memory");
@@ -103,6 +107,54 @@ MSA_DEV void store8(float* p, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
+}
+
+// Keys from a piece's first block on that all rows of it see: those of its first row.
+MSA_DEV int open_keys(const PrefixArgs& a, const Piece& s) {
+  const int G = a.num_qo_heads / a.num_kv_heads;
+  const long long lim = min((long long)s.lk, (long long)s.hidden + s.row0 / G + 1) - (long long)s.j0 * kBlk;
+  return (int)max(0ll, min(lim, (long long)s.keys));
+}
+// Of two 16-bit values, or of four of E4M3: all bits of those that are not finite.
+template <bool F16>
+MSA_DEV uint32_t not_finite2(uint32_t x) {
+  constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u;
+  return __vcmpeq2(x & kExp, kExp);
+}
+MSA_DEV uint32_t not_finite_e4m3(uint32_t x) { return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu); }
+// Adds to a row, which its thread has written to `out` or `part`, the values that
+// are not finite of the keys [from, to) of its page row: infinite or NaN times any
+// probability is that.
+template <bool FP8, bool F16>
+__device__ __noinline__ void add_not_finite(const PrefixArgs& a, const int32_t* pages, int h, int from, int to, uint16_t* out,
+                                            float* part) {
+  constexpr int kSize = FP8 ? 1 : 2, kChunk = 16 / kSize;
+  for (int key = from; key < to; ++key) {
+    const int page = __ldg(pages + key / kBlk);
+    if (page < 0 || page >= a.num_pages) continue;
+    const uint8_t* at = a.v_pool + (((size_t)page * a.num_kv_heads + h) * kBlk + key % kBlk) * kHeadDim * kSize;
+    for (int c0 = 0; c0 < kHeadDim; c0 += kChunk) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(at + c0 * kSize));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      uint32_t any = 0u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) any |= FP8 ? not_finite_e4m3(w[i]) : not_finite2<F16>(w[i]);
+      if (any == 0u) continue;
+#pragma unroll 1
+      for (int i = 0; i < kChunk; ++i) {
+        const uint32_t word = i < kChunk / 4 ? w[0] : i < kChunk / 2 ? w[1] : i < 3 * kChunk / 4 ? w[2] : w[3];
+        const uint32_t bits = word >> (8 * kSize * (i % (kChunk / 4))) & (FP8 ? 0xffu : 0xffffu);
+        if (FP8 ? (bits & 0x7fu) != 0x7fu : not_finite2<F16>(bits) == 0u) continue;
+        const float v = FP8 ? NAN : F16 ? __half2float(__ushort_as_half((unsigned short)bits)) : __uint_as_float(bits << 16);
+        if (part != nullptr) {
+          part[c0 + i] += v;
+        } else {
+          const float o = F16 ? __half2float(__ushort_as_half(out[c0 + i])) : __uint_as_float((uint32_t)out[c0 + i] << 16);
+          out[c0 + i] = (uint16_t)pack_x2<F16>(o + v, 0.f);
+        }
+      }
+    }
+  }
 }
 
 template <bool FP8, bool F16>
@@ -151,7 +203,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         mbar_init(&sm.p_full[s][h], 4);
         mbar_init(&sm.pv_done[s][h], 1);
       }
-      mbar_init(&sm.o_done[s], 1);
+      mbar_init(&sm.o_done[s], 2);
       mbar_init(&sm.o_free[s], 4);
     }
     mbar_init(&sm.ml_full, 4);
@@ -163,6 +215,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       mbar_init(&sm.raw_empty[s], FP8 ? R::kDecodeWarps : 1);
     }
     sm.abort = 0;
+    sm.cleaned = 0;
     fence_mbar_init();
   }
   if (warp == R::kPv) {
@@ -315,7 +368,11 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
             commit(&sm.pv_done[st][h]);
             if (h == 1) {
               p_phase ^= 1u << st;
-              if (t + ahead >= n) commit(&sm.o_done[st]);
+              if (t + ahead >= n) {
+                commit(&sm.o_done[st]);
+                // And what this warp waited for: sm.cleaned of this piece.
+                if (lane == 0) mbar_arrive(&sm.o_done[st]);
+              }
             }
           }
           if (!ok) break;
@@ -343,8 +400,9 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     const int32_t* prow = nullptr;
     int page_k = -1, page_v = -1;
     struct Tile {
-      int g, page, blk, is_v, h, lk;
+      int g, page, is_v, h, rows, open;  // rows, open: as of a raw tile
     };
+    int open = 0;
     // The next tile, warp-wide; false at the end.
     auto take = [&](Tile& t) -> bool {
       while (more && x == 2 * n) {
@@ -359,6 +417,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         if (lane == 0) release_seg(ni);
         ++ni;
         n = blocks_of(s);
+        open = open_keys(a, s);
         prow = a.page_table + (size_t)s.b * a.max_pages + s.j0;
       }
       if (!more) return false;
@@ -374,11 +433,11 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       if (is_v) fetch(page_v);
       else fetch(page_k);
       t.page = __shfl_sync(0xffffffffu, is_v ? page_v : page_k, j & 31);
-      t.blk = s.j0 + j;
       t.g = g0 + j;
       t.is_v = is_v;
       t.h = s.h;
-      t.lk = s.lk;
+      t.rows = min(s.keys - j * kBlk, kBlk);
+      t.open = open - j * kBlk;
       return true;
     };
     if constexpr (!FP8) {
@@ -444,15 +503,14 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       Tile t;
       while (ok && take(t)) {
         if (lane == 0) {
-          const long long left = (long long)t.lk - (long long)t.blk * kBlk;
-          const int rows = t.page >= a.num_pages || left <= 0 ? 0 : left < kBlk ? (int)left : kBlk;
-          ok = put(RawTile{t.g, t.is_v, rows},
+          const int rows = t.page >= a.num_pages ? 0 : t.rows;
+          ok = put(RawTile{t.g, t.is_v, rows, t.is_v ? t.open : kBlk},
                    (t.is_v ? a.v_pool : a.k_pool) + ((size_t)(rows > 0 ? t.page : 0) * a.num_kv_heads + t.h) * kHalf);
         }
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       }
       if (lane == 0) {
-        if (ok) ok = put(RawTile{-1, 0, 0}, nullptr);
+        if (ok) ok = put(RawTile{-1, 0, 0, kBlk}, nullptr);
         // Copies in flight land before the CTA's shared memory is given back.
         if (!ok)
           for (int i = y < kRawSlots ? 0 : y - kRawSlots; i < y; ++i)
@@ -462,8 +520,8 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
   } else if (FP8 && warp >= R::kDecode) {
     // ------------------------------------------------------------- E4M3 to f16
     // 128 threads take a block's 128 rows of 128 bytes as eight 16-byte groups
-    // each, give the raw slot back, and write f16. Rows past the sequence's end
-    // become zeros.
+    // each, give the raw slot back, and write f16. Rows that no row of the unit sees
+    // become zeros, NaN of those that not all see too.
     // Of eight threads four take the first half of a row and four the second
     // half of its neighbour, which keeps reads and writes off each other's
     // banks.
@@ -485,6 +543,17 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.raw_empty[rs]);
       if (t.g < 0) break;
+      if (t.open < t.rows) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          if (r0 + c * 16 < t.open) continue;
+          const uint4 x = raw[c], m = make_uint4(not_finite_e4m3(x.x), not_finite_e4m3(x.y), not_finite_e4m3(x.z), not_finite_e4m3(x.w));
+          if (m.x | m.y | m.z | m.w) {
+            raw[c] = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
+            *const_cast<volatile int*>(&sm.cleaned) = 1;
+          }
+        }
+      }
       const int ring = t.is_v ? kVSlots : kKSlots, slot = t.g % ring, round = t.g / ring;
       ok = round == 0 || mbar_wait_sleep(t.is_v ? &sm.v_empty[slot] : &sm.k_empty[slot], (round - 1) & 1, fault,
                                  kFaultWaitMma, abort);
@@ -630,14 +699,13 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       }
       const int n = blocks_of(s), own = dual ? n : (n + 1 - st) / 2, step = dual ? 1 : 2;
       const int32_t* prow = a.page_table + (size_t)s.b * a.max_pages + s.j0;
-      // Keys that the row sees, and that the sequence has, from the piece's first on.
-      int sees, here;
+      // Keys that the row sees, and that all rows see, from the piece's first on.
+      int sees;
       {
-        const long long base = (long long)s.j0 * kBlk;
-        const long long lim = min((long long)s.lk, (long long)s.hidden + (s.row0 + r) / G + 1) - base;
+        const long long lim = min((long long)s.lk, (long long)s.hidden + (s.row0 + r) / G + 1) - (long long)s.j0 * kBlk;
         sees = active ? (int)max(0ll, min(lim, (long long)n * kBlk)) : 0;
-        here = (int)max(0ll, min((long long)s.lk - base, (long long)n * kBlk));
       }
+      const int open = open_keys(a, s);
       float m_ref = -INFINITY, l = 0.f;
       int j = dual ? 0 : st;
       int pg1 = own > 0 ? __ldg(prow + j) : 0;
@@ -645,13 +713,12 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         const int pg = pg1;
         if (t + 1 < own) pg1 = __ldg(prow + j + step);
         const int cols = pg >= 0 && pg < a.num_pages ? min(sees - j * kBlk, kBlk) : 0;  // that the row sees
-        const int tail = min(here - j * kBlk, kBlk);                                     // that are the sequence's
         const bool mem = cols > 0;
         const bool warp_mem = __any_sync(0xffffffffu, mem);
         const bool warp_hides = __any_sync(0xffffffffu, active && cols < kBlk);
-        if (!FP8 && tail < kBlk && (st == 0 || !dual)) {
-          // V rows past the end, before the first PV that reads the block (in
-          // a unit of two tiles stream 0's, which is issued first). The wait
+        if (!FP8 && open - j * kBlk < kBlk && (st == 0 || !dual)) {
+          // V rows that not all rows see, before the first PV that reads the block
+          // (in a unit of two tiles stream 0's, which is issued first). The wait
           // for the slot's phase needs the phase before it complete: V of the
           // block kVSlots earlier is there once this block's S is, as S of a
           // stream waits for the PV of its block before, and PVs are issued in
@@ -661,9 +728,19 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
                mbar_wait_sleep(&sm.v_full[vs], (g / kVSlots) & 1, fault, kFaultWaitTma, abort);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
-          for (int i = max(tail, 0) * 16 + row; i < 128 * 16; i += 128)
-            *reinterpret_cast<uint4*>(&sm.v[vs][(i >> 3) & 1][(i >> 4) * 128 + (i & 7) * 16]) =
-                make_uint4(0u, 0u, 0u, 0u);
+          const int seen = s.keys - j * kBlk;  // by some row
+          for (int i = max(open - j * kBlk, 0) * 16 + row; i < 128 * 16; i += 128) {
+            uint4* at = reinterpret_cast<uint4*>(&sm.v[vs][(i >> 3) & 1][(i >> 4) * 128 + (i & 7) * 16]);
+            if ((i >> 4) >= seen) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            const uint4 x = *at, m = make_uint4(not_finite2<F16>(x.x), not_finite2<F16>(x.y), not_finite2<F16>(x.z), not_finite2<F16>(x.w));
+            if (m.x | m.y | m.z | m.w) {
+              *at = make_uint4(x.x & ~m.x, x.y & ~m.y, x.z & ~m.z, x.w & ~m.w);
+              *const_cast<volatile int*>(&sm.cleaned) = 1;
+            }
+          }
           fence_async_smem();
         }
         ok = mbar_wait_sleep(&sm.qk_done[st], nqk & 1, fault, kFaultWaitMma, abort);
@@ -808,7 +885,6 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       const size_t at = !active ? 0 : writes ? out_row(s, r) : place_of(s, r);
       const bool has = l != 0.f;
       const float inv = has ? 1.f / l : 0.f;
-      float odd = 0.f;  // NaN once an element is not finite
 #pragma unroll 1
       for (int c0q = 0; c0q < 128; c0q += 32) {
         float o[32];
@@ -833,8 +909,6 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
         if (active && writes) {
           uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * kHeadDim + c0q);
 #pragma unroll
-          for (int c = 0; c < 32; ++c) odd = fmaf(o[c], 0.f, odd);
-#pragma unroll
           for (int c = 0; c < 32; c += 8)
             to[c >> 3] = has ? make_uint4(pack_x2<F16>(o[c] * inv, o[c + 1] * inv), pack_x2<F16>(o[c + 2] * inv, o[c + 3] * inv),
                                           pack_x2<F16>(o[c + 4] * inv, o[c + 5] * inv), pack_x2<F16>(o[c + 6] * inv, o[c + 7] * inv))
@@ -848,13 +922,12 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
       }
       if (active && writes) {
         if (a.lse != nullptr) a.lse[at] = has ? (m_ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
-        if (a.causal && s.many && has && !(odd == 0.f && l < INFINITY)) {
-          const int er = s.row0 + r;
-          a.odd[atomicAdd(a.meta + 1, 1)] = (s.tau + er / G) * a.num_qo_heads + s.h * G + er % G;
-        }
       } else if (active) {
         a.part_ml[at] = part_of_sum(m_ref, l);
       }
+      if (active && has && open < sees && *const_cast<volatile int*>(&sm.cleaned))
+        add_not_finite<FP8, F16>(a, prow, s.h, open, sees, writes ? static_cast<uint16_t*>(a.out) + at * kHeadDim : nullptr,
+                                 writes ? nullptr : a.part_o + at * kHeadDim);
     }
   }
 

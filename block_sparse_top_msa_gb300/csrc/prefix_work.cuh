@@ -67,7 +67,6 @@ struct Piece {
   int keys;        // keys from j0 on that some row sees
   int e, tile_head;  // the unit: entry, tile * heads + head
   int alone;       // a request's own run, without a group's before it
-  int many;        // the entry has rows of more than one token
 };
 
 // Walks a CTA's range, piece by piece; by a whole warp, whose lanes agree. The
@@ -124,7 +123,6 @@ struct Walk {
       p.keys = (int)max(0ll, min(last, (long long)p.n * kBlk));
       p.e = e, p.tile_head = tile * a.num_kv_heads + h;
       p.alone = y.w < 0 && !(x.w & kGroupRun);
-      p.many = x.y > G;
     }
     at = ends ? unit_at + len : end;
     if (ends) {
@@ -231,12 +229,6 @@ struct Joined {
     const int row = f.row0 + r, tile = row / tile_rows_of(a), second = tile - f.tile;
     add_parts(a, (size_t)a.total_q * a.num_qo_heads + own_row, row - tile * tile_rows_of(a),
               Parts{second ? f.parts[1].c0 : f.parts[0].c0, second ? f.parts[1].n : f.parts[0].n}, col, from, step);
-  }
-  MSA_DEV bool finite() const {
-    float x = 0.f;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) x = fmaf(o[c], 0.f, x);
-    return x == 0.f && l < INFINITY;
   }
   // Output row `orow` (token and head of q).
   MSA_DEV void write(const PrefixArgs& a, size_t orow, int col) const {
