@@ -40,17 +40,28 @@ MSA_DEV T warp_upto(T v, int lane) {
   return v;
 }
 constexpr int kPlanThreads = 1024;
-template <class T>
-MSA_DEV T block_upto(T v, T* s_warp, T& all) {
+// Running sums that stop at kMany, above any number of tokens there is: those of
+// requests that are listed over and over would pass 32 bits. Every thread has to
+// come to the block's.
+constexpr unsigned kMany = 1u << 30;
+MSA_DEV unsigned warp_tokens_upto(unsigned v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const unsigned o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v = min(v + o, kMany);
+  }
+  return v;
+}
+MSA_DEV unsigned block_tokens_upto(unsigned v, unsigned* s_warp, unsigned& all) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const T inc = warp_upto(v, lane);
+  const unsigned inc = warp_tokens_upto(v, lane);
   __syncthreads();
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
-  const T w = warp_upto(s_warp[lane], lane);
+  const unsigned w = warp_tokens_upto(s_warp[lane], lane);
   all = __shfl_sync(0xffffffffu, w, 31);
-  const T before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
-  return inc + (warp > 0 ? before : T(0));
+  const unsigned before = __shfl_sync(0xffffffffu, w, warp > 0 ? warp - 1 : 0);
+  return min(inc + (warp > 0 ? before : 0u), kMany);
 }
 
 // Two running sums over a block; every thread has to come.
@@ -80,9 +91,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     prefix_plan_kernel(const __grid_constant__ PrefixArgs a) {
   extern __shared__ int dyn[];
   __shared__ Sums s_sums[32];
-  __shared__ int s_int[32];
-  int* least = dyn;             // (batch): blocks that a group attends for all
-  int* tokens = dyn + a.batch;  // (batch): a group's tokens
+  __shared__ unsigned s_int[32];
+  int* least = dyn;           // (batch): blocks that a group attends for all
+  int* upto = dyn + a.batch;  // (batch): a group's tokens end before this one
   uint32_t* several = reinterpret_cast<uint32_t*>(dyn + 2 * a.batch);             // a bit per group: more than one request has some
   uint16_t* begins = reinterpret_cast<uint16_t*>(several + (a.batch + 31) / 32);  // (batch): cu_groups
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -104,13 +115,14 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (tid < a.batch) request(tid);
   for (int g = tid; g < a.batch; g += kPlanThreads) {
     least[g] = groups ? max(0, min(__ldg(a.group_blocks + g), a.max_pages)) : 0;
-    tokens[g] = 0;
+    upto[g] = 0;
     begins[g] = (uint16_t)(groups ? max(0, min(__ldg(a.cu_groups + g), 65535)) : g);
     if ((g & 31) == 0) several[g >> 5] = 0u;
   }
   for (int i = tid; i < a.grid; i += kPlanThreads) a.cut[i] = make_int4(-1, 0, 0, 0);
   __syncthreads();
-  int before = 0, tau = 0, lq = 0, g = 0;
+  unsigned before = 0u;
+  int tau = 0, lq = 0, g = 0;
   for (int i0 = 0; i0 < a.batch; i0 += kPlanThreads) {
     const int i = i0 + tid;
     lq = 0;
@@ -124,21 +136,25 @@ __global__ void __launch_bounds__(kPlanThreads)
           const int mid = (lo + hi) >> 1;
           if (begins[mid] <= i) lo = mid; else hi = mid;
         }
-        g = lo;
+        // Requests listed before any group begins are in none. (Groups that do
+        // not ascend break the contract, but every place that is read lies among
+        // the tokens there are: a group's run goes from its first request's on to
+        // the last that is found to be in it.)
+        g = begins[lo] <= i ? lo : -1;
       }
     }
-    int all;
-    tau = before + block_upto<int>(lq, s_int, all) - lq;
-    before += all;
+    unsigned all;
+    tau = (int)min(before + block_tokens_upto((unsigned)lq, s_int, all), kMany) - lq;
+    before = min(before + all, kMany);
     if (i < a.batch) {
       // With requests listed twice the sums may pass the tokens there are: the
       // rest is left out.
-      if (tau < 0 || lq > a.total_q - tau) lq = 0;
+      if (lq > a.total_q - tau) lq = 0;
       a.entry[2 * i] = make_int4(tau, lq, b, g);
       a.entry[2 * i + 1] = make_int4(t0, lk - lq, lk, -1);
-      if (lq > 0) {
+      if (lq > 0 && g >= 0) {
         atomicMin(&least[g], max(0, lk - lq) / kBlk);
-        if (atomicAdd(&tokens[g], lq) > 0) atomicOr(&several[g >> 5], 1u << (g & 31));
+        if (atomicMax(&upto[g], tau + lq) > 0) atomicOr(&several[g >> 5], 1u << (g & 31));
       }
     }
   }
@@ -153,7 +169,7 @@ __global__ void __launch_bounds__(kPlanThreads)
       int4 r, s;
       if (e0 == 0 && a.batch <= kPlanThreads) r = make_int4(tau, lq, b, g), s = make_int4(t0, lk - lq, lk, -1);
       else r = a.entry[2 * e], s = a.entry[2 * e + 1];
-      const bool shares = (several[r.w >> 5] >> (r.w & 31)) & 1u;
+      const bool shares = r.w >= 0 && ((several[r.w >> 5] >> (r.w & 31)) & 1u);
       const int from = shares ? least[r.w] : 0;
       const int blocks = (int)min((long long)a.max_pages, ((long long)s.z + kBlk - 1) / kBlk);
       x = make_int4(r.x, r.y * G, r.z, from);
@@ -162,7 +178,8 @@ __global__ void __launch_bounds__(kPlanThreads)
       joined = there && from > 0;
     } else if (e < 2 * a.batch && groups && ((several[eg >> 5] >> (eg & 31)) & 1u) && least[eg] > 0) {
       const int first = min((int)begins[eg], a.batch - 1), lead = __ldg(a.group_rows + first);
-      x = make_int4(a.entry[2 * first].x, tokens[eg] * G, max(0, min(lead, a.batch - 1)), kGroupRun);
+      const int tau0 = a.entry[2 * first].x;
+      x = make_int4(tau0, (upto[eg] - tau0) * G, max(0, min(lead, a.batch - 1)), kGroupRun);
       y = make_int4(least[eg], least[eg] * kBlk, least[eg] * kBlk, -1);
       there = true;
     }
@@ -172,11 +189,11 @@ __global__ void __launch_bounds__(kPlanThreads)
       mine.counts = 1 + (joined ? (long long)((x.y + a.chunk_rows - 1) / a.chunk_rows) * a.num_kv_heads << 32 : 0);
     }
     Sums all;
-    const Sums upto = block_sums(mine, s_sums, all);
-    const long long counts = base.counts + upto.counts - mine.counts;
+    const Sums sums = block_sums(mine, s_sums, all);
+    const long long counts = base.counts + sums.counts - mine.counts;
     const int at = (int)counts;
     if (there) {
-      a.start[at] = base.cost + upto.cost - mine.cost;
+      a.start[at] = base.cost + sums.cost - mine.cost;
       a.chunk[at] = (int)(counts >> 32);
       a.work[2 * at] = x;
       a.work[2 * at + 1] = y;

@@ -286,7 +286,8 @@ msa_status_t msa_tree_attention_prepare(
  *                seqused_k device int32 (B), Lk
  *   group_rows, cu_groups, group_blocks  device int32 (B), (B + 1), (B), as
  *                msa_step_tables writes them, or NULL all three (each request
- *                by itself). Each request is listed once. The rows of
+ *                by itself). cu_groups ascends; each request is listed once,
+ *                and one listed before cu_groups[0] is in no group. The rows of
  *                page_table of a group's requests agree in its first
  *                group_blocks blocks (the first request's pages are read); of
  *                those, the ones that lie before every new token of the group
