@@ -865,7 +865,12 @@ msa_status_t build_prefix(
   if (workspace == nullptr || workspace_bytes < L.total) return MSA_WORKSPACE_TOO_SMALL;
   plan->empty = total_q == 0;
   if (plan->empty) return MSA_OK;
-  if (out == q) return MSA_INVALID_ARG;
+  const size_t rows = (size_t)total_q * num_qo_heads, n4 = 4 * (size_t)batch;
+  const size_t pool = (size_t)num_pages * num_kv_heads * 128 * 128 * (kv_dtype == MSA_FP8_E4M3 ? 1 : 2);
+  if (spans_clash({{out, rows * 256}, {lse, rows * 4}, {workspace, L.total}},
+                  {{q, rows * 256}, {k, pool}, {v, pool}, {cu_seqlens_q, n4 + 4}, {page_table, n4 * max_pages}, {seqused_k, n4},
+                   {group_rows, n4}, {cu_groups, n4 + 4}, {group_blocks, n4}}))
+    return MSA_INVALID_ARG;
   unsigned* fault = fault_word();
   if (fault == nullptr) return MSA_CUDA_ERROR;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

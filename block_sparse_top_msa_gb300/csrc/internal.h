@@ -7,7 +7,36 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 namespace msa {
+
+// Memory that an argument of a call covers: `rows` rows of `bytes`, `pitch` bytes
+// from one to the next. NULL is none.
+struct Span {
+  const void* at;
+  size_t bytes;
+  size_t rows = 1, pitch = 0;
+};
+// Whether two of them meet, the first of which is one row.
+inline bool spans_meet(const Span& a, const Span& b) {
+  if (a.at == nullptr || b.at == nullptr) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.at), b0 = reinterpret_cast<uintptr_t>(b.at);
+  const uintptr_t a1 = a0 + (a.bytes > 0 ? a.bytes : 1), row = b.bytes > 0 ? b.bytes : 1;
+  if (b.rows <= 1 || b.pitch == 0) return a0 < b0 + row && b0 < a1;
+  const uintptr_t first = a0 < b0 + row ? 0 : (a0 - b0 - row) / b.pitch + 1;  // row that ends behind a0
+  return first < b.rows && b0 + first * b.pitch < a1;
+}
+// Whether what a call writes meets what it reads, or is given twice.
+inline bool spans_clash(std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (const Span* w = written.begin(); w != written.end(); ++w) {
+    for (const Span& r : read)
+      if (spans_meet(*w, r)) return true;
+    for (const Span* o = written.begin(); o != w; ++o)
+      if (spans_meet(*w, *o)) return true;
+  }
+  return false;
+}
 
 // Device address of the library's fault word on the current device (host).
 unsigned* fault_word();

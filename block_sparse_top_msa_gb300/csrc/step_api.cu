@@ -3,7 +3,6 @@
 // pages (cache.cu), of a step's tables and drafted paths (step_tables.cu) and
 // of sampling (sample.cu).
 #include <cmath>
-#include <initializer_list>
 
 #include "../../include/msa.h"
 #include "internal.h"
@@ -90,18 +89,6 @@ msa_status_t place_plan(CacheTableArgs* a, void* workspace, size_t bytes) {
   a->plan = static_cast<int32_t*>(workspace);
   a->list = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + up256((size_t)a->n * 4));
   return MSA_OK;
-}
-
-// Whether an output is an input, or given twice.
-bool shares(std::initializer_list<const void*> outputs, std::initializer_list<const void*> inputs) {
-  for (auto o = outputs.begin(); o != outputs.end(); ++o) {
-    if (*o == nullptr) continue;
-    for (const void* i : inputs)
-      if (*o == i) return true;
-    for (auto other = outputs.begin(); other != o; ++other)
-      if (*o == *other) return true;
-  }
-  return false;
 }
 
 }  // namespace
@@ -325,10 +312,12 @@ msa_status_t msa_step_tables(const int32_t* page_table, int max_pages, int num_r
     if (!aligned(p, 4)) return MSA_INVALID_ARG;
   if (!token_data(token_rows, 4, total_q) || !token_data(positions, 4, total_q) || !token_data(slots, 8, total_q))
     return MSA_INVALID_ARG;
-  if (shares({cu_seqlens_q, seqused_out, table_out, token_rows, positions, slots, group_rows, cu_groups, group_blocks},
-             {page_table, seqused_k, rows, new_lens}))
-    return MSA_INVALID_ARG;
   if (batch > kMaxCacheRows) return MSA_UNSUPPORTED;
+  const size_t b = batch, t = total_q, width = max_pages;
+  if (spans_clash({{cu_seqlens_q, 4 * (b + 1)}, {seqused_out, 4 * b}, {table_out, 4 * b * width}, {token_rows, 4 * t}, {positions, 4 * t}, {slots, 8 * t},
+                   {group_rows, 4 * b}, {cu_groups, 4 * (b + 1)}, {group_blocks, 4 * b}, {workspace, msa_step_tables_workspace_size(batch)}},
+                  {{page_table, 4 * (size_t)num_rows * width}, {seqused_k, 4 * (size_t)num_rows}, {rows, 4 * b}, {new_lens, 4 * b}}))
+    return MSA_INVALID_ARG;
   if (workspace == nullptr || workspace_bytes < msa_step_tables_workspace_size(batch)) return MSA_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 256)) return MSA_INVALID_ARG;
   StepTablesArgs a{};
@@ -365,8 +354,11 @@ msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride,
   for (const void* p : {(const void*)temperature, (const void*)top_k, (const void*)top_p, (const void*)min_p,
                         (const void*)logprobs})
     if (p != nullptr && !aligned(p, 4)) return MSA_INVALID_ARG;
-  if (shares({tokens, logprobs}, {logits, uniforms, temperature, top_k, top_p, min_p})) return MSA_INVALID_ARG;
   if (vocab > kMaxVocab || rows > (1 << 24)) return MSA_UNSUPPORTED;
+  const size_t size = dtype == MSA_FP32 ? 4 : 2, r4 = 4 * (size_t)rows;
+  if (spans_clash({{tokens, r4}, {logprobs, r4}, {workspace, msa_sample_workspace_size(rows, vocab, dtype)}},
+                  {{logits, size * vocab, (size_t)rows, size * (size_t)stride}, {uniforms, r4}, {temperature, r4}, {top_k, r4}, {top_p, r4}, {min_p, r4}}))
+    return MSA_INVALID_ARG;
   if (rows == 0) return MSA_OK;
   if (workspace == nullptr || workspace_bytes < msa_sample_workspace_size(rows, vocab, dtype)) return MSA_WORKSPACE_TOO_SMALL;
   if (!aligned(workspace, 256)) return MSA_INVALID_ARG;
@@ -402,7 +394,10 @@ msa_status_t msa_draft_path(const int32_t* sampled, const int32_t* drafts,
   if (!token_data(sampled, 4, total_q) || !token_data(drafts, 4, total_q) || !token_data(tree_mask, 4, total_q) ||
       !aligned(cu_seqlens_q, 4) || !aligned(path, 4) || !aligned(path_len, 4) || !aligned(next_tokens, 4))
     return MSA_INVALID_ARG;
-  if (shares({path, path_len, next_tokens}, {sampled, drafts, tree_mask, cu_seqlens_q})) return MSA_INVALID_ARG;
+  const size_t b = batch, t = total_q;
+  if (spans_clash({{path, 4 * b * max_path}, {path_len, 4 * b}, {next_tokens, 4 * b}},
+                  {{sampled, 4 * t}, {drafts, 4 * t}, {tree_mask, 4 * t * mask_words}, {cu_seqlens_q, 4 * (b + 1)}}))
+    return MSA_INVALID_ARG;
   DraftPathArgs a{};
   a.sampled = sampled, a.drafts = drafts, a.mask = tree_mask, a.mask_words = mask_words;
   a.cu_q = cu_seqlens_q, a.batch = batch, a.total_q = total_q, a.max_path = max_path;

@@ -294,7 +294,7 @@ msa_status_t msa_tree_attention_prepare(
  *                are attended for all, the others by each request.
  *   max_seqlen_q host bound on every Lq, or 0 when unknown
  *   softmax_scale  0 or below: 1 / sqrt(128)
- *   out          device, as q; another tensor than q
+ *   out          device, as q
  *   lse          device float32 (total_q, Hq) or NULL: natural log
  *   workspace    msa_prefix_attention_workspace_size(...) bytes (groups: whether
  *                they are given), 256-byte aligned, uninitialised; calls that
@@ -303,8 +303,9 @@ msa_status_t msa_tree_attention_prepare(
  * are left as they were. What a token does not see may hold anything,
  * infinities and NaN included; one that sees a NaN gets NaN. The same inputs
  * give the same bits. MSA_INVALID_ARG for a NULL or misaligned pointer, some of
- * the group arrays without the others, sizes below 1 (total_q may be 0) or q as
- * out; MSA_UNSUPPORTED for head_dim != 128, another dtype, Hq / Hkv above 128,
+ * the group arrays without the others, sizes below 1 (total_q may be 0), or an
+ * output or the workspace that meets an input's memory or another's;
+ * MSA_UNSUPPORTED for head_dim != 128, another dtype, Hq / Hkv above 128,
  * more than 16384 requests, max_pages above 2^23 or total_q * Hq >= 2^30.
  * msa_prefix_attention_prepare binds the call into a plan that
  * msa_sparse_attention_run launches.
@@ -505,8 +506,8 @@ msa_status_t msa_cache_accept(void* const* pools, int num_pools, int row_bytes, 
  * uninitialised; calls that share one must be ordered on the device.
  * MSA_INVALID_ARG for a NULL or misaligned pointer (4 bytes, slots 8;
  * per-token arrays may be NULL when total_q is 0), sizes below 1 (total_q may
- * be 0) or an output that is an input; MSA_UNSUPPORTED for more than 16384
- * requests.
+ * be 0) or an output or the workspace that meets an input's memory or
+ * another's; MSA_UNSUPPORTED for more than 16384 requests.
  */
 size_t msa_step_tables_workspace_size(int batch);
 msa_status_t msa_step_tables(const int32_t* page_table, int max_pages, int num_rows,
@@ -550,8 +551,10 @@ msa_status_t msa_step_tables(const int32_t* page_table, int max_pages, int num_r
  *                logit in 32 bits, 256 in all in 16), 256-byte aligned,
  *                uninitialised; calls that share one must be ordered on the device
  * MSA_INVALID_ARG for a NULL or misaligned pointer (arrays of rows may be NULL
- * when rows is 0), vocab below 1, a stride below vocab, or an output that is an
- * input; MSA_UNSUPPORTED for another dtype, vocab above 2^19 or rows above 2^24.
+ * when rows is 0), vocab below 1, a stride below vocab, or an output or the
+ * workspace that meets an input's memory (what lies between two rows of logits
+ * is none) or another's; MSA_UNSUPPORTED for another dtype, vocab above 2^19 or
+ * rows above 2^24.
  */
 size_t msa_sample_workspace_size(int rows, int vocab, msa_dtype_t dtype);
 msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride, int rows,
@@ -579,7 +582,8 @@ msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride,
  *                next root; -1 for a request without tokens
  * Tokens at or past total_q are not read. MSA_INVALID_ARG for a NULL or
  * misaligned pointer (4 bytes; per-token arrays may be NULL when total_q is 0),
- * sizes below 1 (total_q may be 0) or an output that is an input.
+ * sizes below 1 (total_q may be 0) or an output that meets an input's memory or
+ * another's.
  */
 msa_status_t msa_draft_path(const int32_t* sampled, const int32_t* drafts,
                             const uint32_t* tree_mask, int mask_words,
