@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
         const int e = (int)(big >> 7), k = e == 255 ? 0 : min(120, 142 - e);
         const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-        scale[r] = a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
+        scale[r] = scale_down(a.scale_log2, k);
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           q[i >> 1][r + 2 * (i & 1)] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);

@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
           const int e = (int)(big >> 7);  // exponent field of the row's largest value
           const int k = e == 255 ? 0 : min(120, 142 - e);
           const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-          own_scale = a.scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23);
+          own_scale = scale_down(a.scale_log2, k);
           if (!dual) sm.q_scale[loaded & 1][row] = own_scale;
 #pragma unroll
           for (int c = 0; c < 16; ++c) {

@@ -55,6 +55,11 @@ MSA_DEV void update_max(bool mem, float mx, float scale_log2, float& m_ref, floa
   }
 }
 
+// The softmax scale of a row of Q that was multiplied by 2^k: a number above 0,
+// however small the caller's scale, as a hidden key's -inf times 0 is NaN.
+// (Logits of the least scale there is are 0 to float32's last bit either way.)
+MSA_DEV float scale_down(float scale_log2, int k) { return fmaxf(scale_log2 * __uint_as_float((uint32_t)(127 - k) << 23), 0x1p-126f); }
+
 // P = 2^(s * scale_log2 + neg_m) for N columns, packed to 16-bit pairs (the
 // type of V) and stored to TMEM at pcol (N/2 columns); the fp32 values are
 // summed into acc. P <= 2^8, well inside the f16 range.
