@@ -188,7 +188,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // A block per request: its row of the page table, its tokens' places, and how
 // many of its blocks are its leader's too. 2048 requests with 1024 places each:
-// 8.8 us; they begin under the plan's end.
+// 8.8 us; they begin under the plan's end. Counters are unsigned, as counts go up
+// to 2^31 - 1 and a step past the last one has to stay above it.
 constexpr int kRowThreads = 256;
 __global__ void __launch_bounds__(kRowThreads)
     step_rows_kernel(const __grid_constant__ StepTablesArgs a) {
@@ -206,23 +207,23 @@ __global__ void __launch_bounds__(kRowThreads)
   const int most = lead != b ? __ldcg(a.group_blocks + g) : 0;
   // A leader's own holes end what the others may share with it: each of them
   // sees those too.
-  int differs = INT_MAX;
-  for (int j = tid; j < a.max_pages; j += kRowThreads) {
-    int page = j < used ? __ldg(row + j) : -1;
+  unsigned differs = UINT_MAX;
+  for (unsigned j = tid; j < (unsigned)a.max_pages; j += kRowThreads) {
+    int page = j < (unsigned)used ? __ldg(row + j) : -1;
     if (page < 0 || page >= a.num_pages) page = -1;
     out[j] = page;
-    if (j < most && differs == INT_MAX && (page < 0 || page != __ldg(other + j))) differs = j;
+    if (j < (unsigned)most && differs == UINT_MAX && (page < 0 || page != __ldg(other + j))) differs = j;
   }
-  if (differs < most) atomicMin(a.group_blocks + g, differs);
-  for (int i = tid; i < n; i += kRowThreads) {
-    const int pos = len - n + i;
+  if (differs < (unsigned)most) atomicMin(a.group_blocks + g, (int)differs);
+  for (unsigned i = tid; i < (unsigned)n; i += kRowThreads) {
+    const int pos = len - n + (int)i;
     int page = pos / kBlk < a.max_pages ? __ldg(row + pos / kBlk) : -1;
     if (page >= a.num_pages) page = -1;
     a.token_rows[t0 + i] = b;
     a.positions[t0 + i] = pos;
     a.slots[t0 + i] = page < 0 ? -1 : (long long)page * kBlk + pos % kBlk;
   }
-  for (int t = __ldcg(a.cu_q + a.batch) + b * kRowThreads + tid; t < a.total_q; t += gridDim.x * kRowThreads) {
+  for (unsigned t = __ldcg(a.cu_q + a.batch) + b * kRowThreads + tid; t < (unsigned)a.total_q; t += gridDim.x * kRowThreads) {
     a.token_rows[t] = -1;
     a.positions[t] = -1;
     a.slots[t] = -1;
@@ -249,10 +250,11 @@ __global__ void __launch_bounds__(kPathWarps * 32)
     if (lane == 0) path[0] = 0;
     len = 1;
   }
-  for (int c0 = 0; c0 < n && len < a.max_path; c0 += 32) {
-    const int c = c0 + lane;
+  const unsigned nodes = max(n, 0);
+  for (unsigned c0 = 0; c0 < nodes && len < a.max_path; c0 += 32) {
+    const int c = (int)(c0 + lane);
     int parent = -1, draft = 0;
-    if (c < n) {
+    if (c0 + lane < nodes) {
       draft = __ldg(a.drafts + t0 + c);
       const uint32_t* row = a.mask + (size_t)(t0 + c) * a.mask_words;
       int w = min(c >> 5, a.mask_words - 1);
@@ -263,13 +265,13 @@ __global__ void __launch_bounds__(kPathWarps * 32)
     while (len < a.max_path) {
       const unsigned m = __ballot_sync(0xffffffffu, parent == at && c > at && draft == want);
       if (m == 0u) break;
-      at = c0 + __ffs(m) - 1;
+      at = (int)c0 + __ffs(m) - 1;
       want = __ldg(a.sampled + t0 + at);
       if (lane == 0) path[len] = at;
       ++len;
     }
   }
-  for (int i = len + lane; i < a.max_path; i += 32) path[i] = -1;
+  for (unsigned i = len + lane; i < (unsigned)a.max_path; i += 32) path[i] = -1;
   if (lane == 0) {
     a.path_len[b] = len;
     a.next[b] = want;
