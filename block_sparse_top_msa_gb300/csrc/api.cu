@@ -822,7 +822,11 @@ PrefixLayout prefix_layout(int batch, int total_q, int hq, bool groups) {
   L.off_token = place((size_t)total_q * sizeof(int2));
   L.off_meta = place(sizeof(int));
   L.off_cut = place((size_t)kPlanSMs * sizeof(int4));
-  L.part_rows = (size_t)total_q * hq * (groups ? 2 : 1);
+  // With groups a row's own run and its group's may each leave parts, at a place
+  // of the row's. Without, only units that a range's end cuts do, one a CTA: more
+  // rows than those units have need no places of their own.
+  const size_t all = (size_t)total_q * hq, cut = (size_t)kPlanSMs * kBigRows;
+  L.part_rows = groups ? 2 * all : all < cut ? all : cut;
   const size_t rows = L.part_rows + (size_t)kPlanSMs * kBigRows;
   L.off_ml = place(rows * sizeof(float2));
   L.off_o = place(rows * 128 * sizeof(float));
@@ -919,6 +923,7 @@ msa_status_t build_prefix(
   a.meta = reinterpret_cast<int*>(ws + L.off_meta);
   a.cut = reinterpret_cast<int4*>(ws + L.off_cut);
   a.part_rows = L.part_rows;
+  a.at_cta = L.part_rows < (size_t)total_q * num_qo_heads ? 1 : 0;
   a.part_ml = reinterpret_cast<float2*>(ws + L.off_ml);
   a.part_o = reinterpret_cast<float*>(ws + L.off_o);
   return MSA_OK;

@@ -253,7 +253,8 @@ struct PrefixArgs {
   int2* token = nullptr;       // (total_q): each token's row of q, and its position
   int* meta = nullptr;         // entries
   int4* cut = nullptr;         // (grid): the unit without a group before that begins in the CTA's range and goes on after it: entry, tile and head; entry -1: none
-  size_t part_rows = 0;        // rows of parts before the CTAs' own
+  int at_cta = 0;              // units' first pieces leave their parts at the CTA's too, not at the rows' own places
+  size_t part_rows = 0;        // rows of parts before those of the CTAs' later pieces
   float2* part_ml = nullptr;   // (part_rows + grid * kBigRows)
   float* part_o = nullptr;     // the same, 128 each
 };

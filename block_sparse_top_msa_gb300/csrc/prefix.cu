@@ -11,7 +11,9 @@
 // blocks, laid end to end, are cut into equal ranges, one per CTA, wherever
 // they end: a long run is split over many CTAs, short ones share one. The first
 // piece of a unit leaves its parts at the rows' own places, the others (a CTA
-// has one at most, its first) at the CTA's.
+// has one at most, its first) at the CTA's. Without groups only units that are
+// cut leave parts, so that a CTA has at most one first piece that does (its last):
+// where rows are many, those lie at the CTA's too.
 //
 // Where requests have at most 16 rows for each KV head and share nothing, the
 // units are of 16 rows and this file's kernel takes them; else they are of 256,
@@ -715,7 +717,7 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
     if (live && p.whole) {
       own.write(a, (size_t)token * a.num_qo_heads + hq, col);
     } else if (live) {
-      const size_t at = p.place >= 0 ? own_row : a.part_rows + (size_t)blockIdx.x * kSmallRows + out_row;
+      const size_t at = p.place >= 0 ? first_part(a, own_row, blockIdx.x, out_row) : a.part_rows + (size_t)blockIdx.x * kSmallRows + out_row;
       float4* to = reinterpret_cast<float4*>(a.part_o + at * kHeadDim + col);
       to[0] = make_float4(own.o[0], own.o[1], own.o[2], own.o[3]);
       to[1] = make_float4(own.o[4], own.o[5], own.o[6], own.o[7]);
@@ -794,7 +796,8 @@ __global__ void __launch_bounds__(kJoinThreads)
         const int token = __ldcg(&a.token[x.x + er / G].x);
         Joined all;
         all.add_before(a, f, r, own_row, col);
-        all.add_parts(a, own_row, er % tile_rows_of(a), parts, col);
+        const int row = er % tile_rows_of(a);
+        all.add_parts(a, first_part(a, own_row, parts.c0, row), row, parts, col);
         all.write(a, (size_t)token * a.num_qo_heads + hq, col);
       }
     }

@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(Roles<FP8>::kThreads, 1)
     // Where a row's parts of a piece go.
     auto place_of = [&](const Piece& s, int r) -> size_t {
       const int er = s.row0 + r;
-      return s.place >= 0 ? (size_t)(s.place + er / G) * a.num_qo_heads + (size_t)s.h * G + er % G
+      return s.place >= 0 ? first_part(a, (size_t)(s.place + er / G) * a.num_qo_heads + (size_t)s.h * G + er % G, blockIdx.x, r)
                           : a.part_rows + (size_t)blockIdx.x * kBigRows + r;
     };
 

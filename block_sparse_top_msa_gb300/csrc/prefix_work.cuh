@@ -161,6 +161,11 @@ struct Before {
   int tile;      // and the tile of that row
   Parts parts[2];  // of this tile and the next
 };
+// Where the first of a unit's pieces leaves a row's parts: at the row's own place,
+// or in CTA c0's row `row` of the tile.
+MSA_DEV size_t first_part(const PrefixArgs& a, size_t own_row, int c0, int row) {
+  return a.at_cta ? (size_t)c0 * tile_rows_of(a) + row : own_row;
+}
 // By a whole warp.
 MSA_DEV Before before_of(const PrefixArgs& a, const Ranges& ranges, int group, int tau, int row0, int rows, int h) {
   Before f{};

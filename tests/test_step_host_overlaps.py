@@ -62,3 +62,11 @@ def test_prefix_attention(L, clash):
 
 def test_prefix_attention_of_no_tokens_covers_nothing(L):
     assert call(L.msa_prefix_attention, PREFIX, dict(PREFIX_GOOD, t=0), out=by(0, 16)) == OK
+
+
+def test_prefix_attention_workspace_without_groups(L):
+    """Only units that a range cuts leave parts: two pieces of 256 rows a CTA, and eight bytes a token."""
+    size = L.msa_prefix_attention_workspace_size
+    assert size(1, 32768, 64, 4, 128, 0) < 50 << 20
+    assert size(1, 1 << 20, 64, 4, 128, 0) - size(1, 32768, 64, 4, 128, 0) == 8 * ((1 << 20) - 32768)
+    assert size(4, 600, 64, 4, 128, 0) < size(4, 700, 64, 4, 128, 0)
