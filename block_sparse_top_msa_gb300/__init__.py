@@ -791,8 +791,9 @@ def msa_prefix_attention(q, k, v, cu_seqlens_q, *, page_table, seqused_k, group_
     first pages that groups of requests share are attended once for all of a
     group; see ``msa_prefix_attention`` in include/msa.h. The groups are those of
     a ``StepTables``; without them each request is by itself. ``max_seqlen_q`` bounds
-    every request's tokens; None (nothing known) does not read the device. Returns
-    ``out`` or ``(out, lse)``."""
+    every request's tokens; None (nothing known) does not read the device, but then
+    few tokens a request without groups take the kernel for many. Returns ``out`` or
+    ``(out, lse)``."""
     out, lse, _, _ = (_native or _step()).prefix_attention(
         q, k, v, cu_seqlens_q, page_table, seqused_k, group_rows, cu_groups, group_blocks,
         max_seqlen_q, causal, softmax_scale, return_softmax_lse, out, lse, workspace, stream, False)

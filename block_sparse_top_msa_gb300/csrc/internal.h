@@ -476,7 +476,7 @@ struct StepTablesArgs {
   int32_t* group_rows = nullptr;   // (batch)
   int32_t* cu_groups = nullptr;    // (batch + 1)
   int32_t* group_blocks = nullptr;  // (batch)
-  int32_t* plan = nullptr;         // workspace (4, batch): first page, leader, group, whole blocks before the new tokens
+  int32_t* plan = nullptr;         // workspace (4, batch): nothing, leader, group, whole blocks before the new tokens
   int hash_slots = 0;
 };
 cudaError_t launch_step_tables(const StepTablesArgs& a, cudaStream_t s);

@@ -15,9 +15,11 @@
 // cut leave parts, so that a CTA has at most one first piece that does (its last):
 // where rows are many, those lie at the CTA's too.
 //
-// Where requests have at most 16 rows for each KV head and share nothing, the
-// units are of 16 rows and this file's kernel takes them; else they are of 256,
-// prefix_big.cu's. A unit that is a request's alone and that one CTA has whole
+// Where the call names no groups and bounds every request's rows by 16 for each
+// KV head, the units are of 16 rows and this file's kernel takes them; else they
+// are of 256, prefix_big.cu's (the host does not read the arrays: with groups that
+// share nothing, 32 requests of 4096 to 65536 keys take 338 us by the one and the
+// other, with E4M3 keys 284 by this and 298 by that). A unit that is a request's alone and that one CTA has whole
 // is written there and then; what is left is joined by the last kernel.
 #include <cuda_fp16.h>
 #include <math.h>
@@ -223,11 +225,15 @@ __global__ void __launch_bounds__(kPlanThreads)
 // (the rows are too few for a tile of 128), its own softmax (m, l) and its own
 // O, so a warp waits for no other until the piece ends, where the eight are
 // joined. Bound by memory: a block of 64 KB takes an SM's share of the
-// bandwidth 3000 clocks. One warp hands out the pieces with their Q, another
+// bandwidth 3000 clocks. P is rounded to the products' type (bf16, or f16 for f16
+// and E4M3 caches: below 2^-25 of a part's largest it is 0 there), l is a sum in 32
+// bits of P before that: half a step of the type on each, which the output's own
+// rounding equals. One warp hands out the pieces with their Q, another
 // brings K and V by TMA through a ring of blocks; the join borrows the next
 // free slots of that ring. 32 requests of 4096 to 65536 keys, 4 KV heads,
 // 16 bits: 338 to 345 us, 6.6 to 6.75 TB/s, what a copy reaches. E4M3 caches have half the
-// bytes and the same MMAs, 256 a block, which bound them then (2000 clocks).
+// bytes and the same MMAs, 256 a block, which bound them then (2000 clocks): 284
+// us, 4.0 TB/s.
 constexpr int kWarps = 8;
 template <int KV>  // 0 bf16, 1 f16, 2 E4M3 with bf16 q
 struct Small {
@@ -735,8 +741,8 @@ __global__ void __launch_bounds__(Small<KV>::kThreads, 1)
 // then those of the own one, in the order of the pieces. In a chunk of fewer rows
 // several half-warps take a row's parts by turns, where it has eight or more (8
 // samples of 32768 tokens, 38 parts a row: the call 48 -> 41 us; split like that, rows
-// of few parts cost the pair of 1300 tokens 1 us). Alone 8 to 19 us for up to 8192
-// rows, bound by that search; 34 for 32768.
+// of few parts cost the pair of 1300 tokens 1 us). Alone 7 to 18 us for up to 8192
+// rows, bound by that search; 32 for 32768.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads)
     prefix_join_kernel(const __grid_constant__ PrefixArgs a) {

@@ -287,26 +287,31 @@ msa_status_t msa_tree_attention_prepare(
  *   group_rows, cu_groups, group_blocks  device int32 (B), (B + 1), (B), as
  *                msa_step_tables writes them, or NULL all three (each request
  *                by itself). cu_groups ascends; each request is listed once,
- *                and one listed before cu_groups[0] is in no group. The rows of
+ *                and one listed before cu_groups[0] is by itself. The rows of
  *                page_table of a group's requests agree in its first
  *                group_blocks blocks (the first request's pages are read); of
  *                those, the ones that lie before every new token of the group
  *                are attended for all, the others by each request.
- *   max_seqlen_q host bound on every Lq, or 0 when unknown
+ *   max_seqlen_q host bound on every Lq, or 0 when unknown. Without groups and
+ *                with at most 16 / (Hq / Hkv) a kernel for few rows runs, else one
+ *                for many (with unshared E4M3 requests 5% slower, 16 bits alike)
  *   softmax_scale  0 or below: 1 / sqrt(128)
  *   out          device, as q
  *   lse          device float32 (total_q, Hq) or NULL: natural log
  *   workspace    msa_prefix_attention_workspace_size(...) bytes (groups: whether
  *                they are given), 256-byte aligned, uninitialised; calls that
  *                share one must be ordered on the device
- * Rows at or past cu_seqlens_q[B], and those of requests that no group lists,
- * are left as they were. What a token does not see may hold anything,
- * infinities and NaN included; one that sees a NaN gets NaN. The same inputs
- * give the same bits. MSA_INVALID_ARG for a NULL or misaligned pointer, some of
- * the group arrays without the others, sizes below 1 (total_q may be 0), or an
- * output or the workspace that meets an input's memory or another's;
- * MSA_UNSUPPORTED for head_dim != 128, another dtype, Hq / Hkv above 128,
- * more than 16384 requests, max_pages above 2^23 or total_q * Hq >= 2^30.
+ * Rows at or past cu_seqlens_q[B], and those of requests that group_rows does
+ * not list, are left as they were. What a token does not see may hold anything,
+ * infinities and NaN included; one that sees a NaN gets NaN. Sums are in 32
+ * bits; probabilities are rounded to the products' type, bf16 or (fp16 and E4M3
+ * caches) f16, where those below 2^-25 of the largest that was seen with them
+ * weigh nothing in out. The same inputs give the same bits. MSA_INVALID_ARG for
+ * a NULL or misaligned pointer, some of the group arrays without the others,
+ * sizes below 1 (total_q may be 0), or an output or the workspace that meets an
+ * input's memory or another's; MSA_UNSUPPORTED for head_dim != 128, another
+ * dtype, Hq / Hkv above 128, more than 16384 requests, max_pages above 2^23 or
+ * total_q * Hq >= 2^30.
  * msa_prefix_attention_prepare binds the call into a plan that
  * msa_sparse_attention_run launches.
  */
@@ -546,7 +551,8 @@ msa_status_t msa_step_tables(const int32_t* page_table, int max_pages, int num_r
  *                (rows); each may be NULL (1 and no cut)
  *   tokens       device int32 (rows)
  *   logprobs     device float32 (rows) or NULL: ln w - ln S(vocab) of the
- *                token, before the cuts (T = 1 where the largest is taken)
+ *                token, before the cuts (T = 1 where a temperature takes the
+ *                largest; top_k = 1 takes it too, with its own T)
  *   workspace    msa_sample_workspace_size(rows, vocab, dtype) bytes (about two a
  *                logit in 32 bits, 256 in all in 16), 256-byte aligned,
  *                uninitialised; calls that share one must be ordered on the device
@@ -573,7 +579,9 @@ msa_status_t msa_sample(const void* logits, msa_dtype_t dtype, long long stride,
  * the nodes' logits). A node's parent is the highest of the nodes before it
  * that its row of tree_mask (as msa_tree_attention takes it) names; one that
  * names none has no parent. From the root on, the path goes to the lowest
- * child whose draft is what was sampled at its parent.
+ * child whose draft is what was sampled at its parent. Numbers are compared as
+ * they are: where sampled may be -1 (no token), drafts that pad a tree have to be
+ * another number, or stand behind no parent.
  *   tree_mask    device uint32 (total_q, mask_words)
  *   path         device int32 (B, max_path): the path's nodes, -1 behind it;
  *                it ends with its max_path-th node
