@@ -402,10 +402,12 @@ PyObject* prefix_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Tensor ws = workspace(a[15], dev, msa_prefix_attention_workspace_size(batch, total, hq, hkv, 128, given));
   const bool prepare = as_flag(a[17]);
   msa_attention_plan_t* plan = nullptr;
+  // Tensors without tokens have no memory: the workspace stands for them, and is not followed.
+  void *qp = total > 0 ? q.data_ptr() : ws.data_ptr(), *op = total > 0 ? out.data_ptr() : ws.data_ptr();
 #define MSA_PREFIX_CALL                                                                                          \
-  q.data_ptr(), qt, k.data_ptr(), v.data_ptr(), kt, ptr<const int32_t>(cu), ptr<const int32_t>(pt), max_pages,   \
+  qp, qt, k.data_ptr(), v.data_ptr(), kt, ptr<const int32_t>(cu), ptr<const int32_t>(pt), max_pages,   \
       pages, ptr<const int32_t>(used), group_rows, cu_groups, blocks, batch, total, hq, hkv, 128, max_q, causal, \
-      scale, out.data_ptr(), lse.defined() ? ptr<float>(lse) : nullptr, ws.data_ptr(), (size_t)ws.numel()
+      scale, op, lse.defined() ? ptr<float>(lse) : nullptr, ws.data_ptr(), (size_t)ws.numel()
   if (prepare) check("msa_prefix_attention_prepare", msa_prefix_attention_prepare(MSA_PREFIX_CALL, &plan));
   else if (total > 0) check("msa_prefix_attention", msa_prefix_attention(MSA_PREFIX_CALL, place.stream()));
 #undef MSA_PREFIX_CALL
