@@ -19,8 +19,9 @@
 // KV head, the units are of 16 rows and this file's kernel takes them; else they
 // are of 256, prefix_big.cu's (the host does not read the arrays: with groups that
 // share nothing, 32 requests of 4096 to 65536 keys take 338 us by the one and the
-// other, with E4M3 keys 284 by this and 298 by that). A unit that is a request's alone and that one CTA has whole
-// is written there and then; what is left is joined by the last kernel.
+// other, with E4M3 keys 284 by this and 298 by that). A unit that is a request's
+// alone and that one CTA has whole is written there and then; what is left is
+// joined by the last kernel.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -292,12 +293,6 @@ MSA_DEV uint32_t e4m3x2_to_f16(uint32_t pair) {
 }
 // Of two keys' 16 bits each: those below `n` kept.
 MSA_DEV uint32_t keep_keys(int first, int n) { return (first < n ? 0xffffu : 0u) | (first + 1 < n ? 0xffff0000u : 0u); }
-// Of two 16-bit values: all bits of those that are not finite.
-template <bool F16>
-MSA_DEV uint32_t not_finite2(uint32_t x) {
-  constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u;
-  return __vcmpeq2(x & kExp, kExp);
-}
 
 template <int KV>
 __global__ void __launch_bounds__(Small<KV>::kThreads, 1)

@@ -117,12 +117,7 @@ MSA_DEV int open_keys(const PrefixArgs& a, const Piece& s) {
   const long long lim = min((long long)s.lk, (long long)s.hidden + s.row0 / G + 1) - (long long)s.j0 * kBlk;
   return (int)max(0ll, min(lim, (long long)s.keys));
 }
-// Of two 16-bit values, or of four of E4M3: all bits of those that are not finite.
-template <bool F16>
-MSA_DEV uint32_t not_finite2(uint32_t x) {
-  constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u;
-  return __vcmpeq2(x & kExp, kExp);
-}
+// Of four E4M3 values: all bits of those that are NaN.
 MSA_DEV uint32_t not_finite_e4m3(uint32_t x) { return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu); }
 // Adds to a row, which its thread has written to `out` or `part`, the values that
 // are not finite of the keys [from, to) of its page row: infinite or NaN times any
@@ -130,29 +125,43 @@ MSA_DEV uint32_t not_finite_e4m3(uint32_t x) { return __vcmpeq4(x & 0x7f7f7f7fu,
 template <bool FP8, bool F16>
 __device__ __noinline__ void add_not_finite(const PrefixArgs& a, const int32_t* pages, int h, int from, int to, uint16_t* out,
                                             float* part) {
-  constexpr int kSize = FP8 ? 1 : 2, kChunk = 16 / kSize;
+  constexpr int kSize = FP8 ? 1 : 2, kChunk = 16 / kSize, kAhead = 8;
+  auto load = [](const uint8_t* at) { return __ldg(reinterpret_cast<const uint4*>(at)); };
   for (int key = from; key < to; ++key) {
     const int page = __ldg(pages + key / kBlk);
     if (page < 0 || page >= a.num_pages) continue;
     const uint8_t* at = a.v_pool + (((size_t)page * a.num_kv_heads + h) * kBlk + key % kBlk) * kHeadDim * kSize;
-    for (int c0 = 0; c0 < kHeadDim; c0 += kChunk) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(at + c0 * kSize));
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      uint32_t any = 0u;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) any |= FP8 ? not_finite_e4m3(w[i]) : not_finite2<F16>(w[i]);
-      if (any == 0u) continue;
+    uint32_t chunks = 0u;  // a bit for each with such a value
 #pragma unroll 1
-      for (int i = 0; i < kChunk; ++i) {
-        const uint32_t word = i < kChunk / 4 ? w[0] : i < kChunk / 2 ? w[1] : i < 3 * kChunk / 4 ? w[2] : w[3];
-        const uint32_t bits = word >> (8 * kSize * (i % (kChunk / 4))) & (FP8 ? 0xffu : 0xffffu);
-        if (FP8 ? (bits & 0x7fu) != 0x7fu : not_finite2<F16>(bits) == 0u) continue;
-        const float v = FP8 ? NAN : F16 ? __half2float(__ushort_as_half((unsigned short)bits)) : __uint_as_float(bits << 16);
-        if (part != nullptr) {
-          part[c0 + i] += v;
+    for (int b0 = 0; b0 < kHeadDim / kChunk; b0 += kAhead) {
+      uint4 x[kAhead];
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) x[b] = load(at + (b0 + b) * 16);
+#pragma unroll
+      for (int b = 0; b < kAhead; ++b) {
+        const uint32_t any = FP8 ? not_finite_e4m3(x[b].x) | not_finite_e4m3(x[b].y) | not_finite_e4m3(x[b].z) | not_finite_e4m3(x[b].w)
+                                 : not_finite2<F16>(x[b].x) | not_finite2<F16>(x[b].y) | not_finite2<F16>(x[b].z) | not_finite2<F16>(x[b].w);
+        chunks |= (any != 0u ? 1u : 0u) << (b0 + b);
+      }
+    }
+    for (; chunks != 0u; chunks &= chunks - 1) {
+      const int c0 = (__ffs(chunks) - 1) * kChunk;
+#pragma unroll 1
+      for (int c = c0; c < c0 + kChunk; ++c) {
+        float v;
+        if constexpr (FP8) {
+          if ((__ldg(at + c) & 0x7f) != 0x7f) continue;
+          v = NAN;
         } else {
-          const float o = F16 ? __half2float(__ushort_as_half(out[c0 + i])) : __uint_as_float((uint32_t)out[c0 + i] << 16);
-          out[c0 + i] = (uint16_t)pack_x2<F16>(o + v, 0.f);
+          const uint16_t w = __ldg(reinterpret_cast<const uint16_t*>(at) + c);
+          if (not_finite2<F16>(w) == 0u) continue;
+          v = F16 ? __half2float(__ushort_as_half(w)) : __uint_as_float((uint32_t)w << 16);
+        }
+        if (part != nullptr) {
+          part[c] += v;
+        } else {
+          const float o = F16 ? __half2float(__ushort_as_half(out[c])) : __uint_as_float((uint32_t)out[c] << 16);
+          out[c] = (uint16_t)pack_x2<F16>(o + v, 0.f);
         }
       }
     }

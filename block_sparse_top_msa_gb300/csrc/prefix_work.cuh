@@ -185,6 +185,13 @@ MSA_DEV Before before_of(const PrefixArgs& a, const Ranges& ranges, int group, i
   return f;
 }
 
+// Of two 16-bit values: all bits of those that are not finite.
+template <bool F16>
+MSA_DEV uint32_t not_finite2(uint32_t x) {
+  constexpr uint32_t kExp = F16 ? 0x7c007c00u : 0x7f807f80u;
+  return __vcmpeq2(x & kExp, kExp);
+}
+
 // (m, l) of a part as it is joined: the part of a row that saw NaN has a sum of
 // NaN, and a maximum that is a number, as -inf says that it saw nothing and
 // maxima of parts drop NaN.
